@@ -64,6 +64,10 @@ typedef enum {
 
 enum { EP_ROUND_RNE = 0, EP_ROUND_SR = 1 };
 
+/* Element types of the unquantised row buffers (ep_pack, ep_combine,
+ * ep_combine_backward). */
+enum { EP_DTYPE_BF16 = 0, EP_DTYPE_F32 = 1 };
+
 /* Bits ORed into *dev_status by the kernels. */
 enum {
     EP_DEV_ERR_BAD_EXPERT = 1u,  /* routing id outside [-1, E): slot dropped  */
@@ -395,6 +399,138 @@ ep_status ep_mxfp8_pack(const void *tokens_bf16, int64_t T, int64_t H,
 ep_status ep_mxfp8_colwise(const void *x_bf16, int64_t R_cap, int64_t H,
                            const int32_t *expert_offsets, int E, uint8_t *buf,
                            uint32_t *dev_status, void *stream);
+
+/*
+ * ep_pack -- tokens copied to their expert rows without quantisation: the
+ * BF16 (or FP32) counterpart of ep_nvfp4_pack, same routing gather.
+ *   tokens          device [T, H] of `dtype` (EP_DTYPE_*), row pitch ld_tokens
+ *                   elements (>= H).  Here and in the two calls below H is any
+ *                   size from 1 to 2^20; buffers need the alignment of one
+ *                   element (16 bytes, with H and the pitches whole multiples
+ *                   of 16 bytes, is the fast case).
+ *   dest, k, expert_offsets, expert_counts, E: as produced by ep_route_plan.
+ *   rows            device [R_cap, H] of `dtype`, must not overlap `tokens`:
+ *                   rows[dest(t, j)] = tokens[t]; padding rows zero.
+ * Its gradient is ep_combine without weights.
+ */
+ep_status ep_pack(const void *tokens, int dtype, int64_t T, int64_t H,
+                  int64_t ld_tokens, const int32_t *dest, int k,
+                  const int32_t *expert_offsets, const int32_t *expert_counts,
+                  int E, void *rows, int64_t R_cap, uint32_t *dev_status,
+                  void *stream);
+
+/*
+ * ep_combine -- expert rows back to tokens, weighted by the router:
+ *   out[t] = sum over j of weights(t, j) * rows[r(t, j)], live slots only.
+ *   rows            device [R_cap, H] of `dtype`, row pitch ld_rows elements.
+ *   index           slot_order = 0: device int32 [T*k], r(t, j) = index(t, j)
+ *                   (the plan's dest); a negative entry is a dropped slot, one
+ *                   >= R_cap raises EP_DEV_ERR_CAPACITY and is dropped.
+ *                   slot_order = 1: r(t, j) = t*k + j (the order in which
+ *                   ep_nvfp4_matvec writes, R_cap >= T*k); a negative entry
+ *                   (topk_idx) is a dropped slot; NULL: none is dropped.
+ *   weights         device f32 [T*k] or NULL (all 1).  Weights and rows of
+ *                   dropped slots are not read: whatever they hold does not
+ *                   reach the output.
+ *   out             device [T, H] of `dtype`; a token without a live slot gets
+ *                   zeros.
+ * FP32 fused multiply-adds in slot order, rounded once.
+ */
+ep_status ep_combine(const void *rows, int dtype, int64_t R_cap, int64_t H,
+                     int64_t ld_rows, const int32_t *index, int slot_order,
+                     const float *weights, int64_t T, int k, void *out,
+                     uint32_t *dev_status, void *stream);
+
+/*
+ * ep_combine_backward -- the gradients of ep_combine under a routing plan:
+ *   d_rows[dest(t, j)] = weights(t, j) * d_out[t], padding rows zero;
+ *   d_weights(t, j)    = sum over h of d_out[t][h] * rows[dest(t, j)][h]
+ *                        (0 for a dropped slot).
+ *   d_out           device [T, H] of `dtype`, row pitch ld_out elements.
+ *   rows            device [R_cap, H] of `dtype`, row pitch ld_rows: the rows
+ *                   ep_combine read.  May be NULL when d_weights is NULL.
+ *   weights         device f32 [T*k] or NULL (all 1).
+ *   d_rows          device [R_cap, H] of `dtype`; must not overlap an input.
+ *   d_weights       device f32 [T*k] or NULL (not wanted).
+ * Products and sums are FP32, the dot product's in a fixed order; each d_rows
+ * element is rounded once.  dest names a row at most once, as the plan does.
+ */
+ep_status ep_combine_backward(const void *d_out, int dtype, int64_t T,
+                              int64_t H, int64_t ld_out, const void *rows,
+                              int64_t ld_rows, const int32_t *dest,
+                              const float *weights, int k,
+                              const int32_t *expert_offsets,
+                              const int32_t *expert_counts, int E,
+                              void *d_rows, int64_t R_cap, float *d_weights,
+                              uint32_t *dev_status, void *stream);
+
+/*
+ * ep_swiglu -- the gated activation between the two expert products, with its
+ * input kept for the backward pass in 8 bits.
+ *   x_bf16          device bf16 [R_cap, 2I], row pitch ld_x elements (a
+ *                   multiple of 8): columns [0, I) are the gate g, [I, 2I) the
+ *                   up projection u.  I % 32 == 0, I <= 2^19.
+ *   expert_offsets  device int32 [E+1] or NULL.  With it, rows [0, R) are
+ *                   processed, R = expert_offsets[E]; NULL (E = 1): all R_cap.
+ *   act_bf16        device bf16 [R_cap, I]: g / (1 + exp(-g)) * u, FP32 from
+ *                   the BF16 input, rounded once.
+ *   ckpt            device u8 or NULL: MXFP8 of x in ep_mxfp8_pack's layout
+ *                   (data [R_cap, 2I], then scales [R_cap, 2I/32]; same
+ *                   exponent rule).  An infinity or NaN is stored as E4M3's
+ *                   NaN, and the block's scale comes from its finite elements.
+ * Buffers 16-byte aligned.
+ */
+ep_status ep_swiglu(const void *x_bf16, int64_t ld_x, int64_t R_cap, int64_t I,
+                    const int32_t *expert_offsets, int E, void *act_bf16,
+                    uint8_t *ckpt, uint32_t *dev_status, void *stream);
+
+/*
+ * ep_swiglu_backward -- the gradient of ep_swiglu from its checkpoint.  With
+ * g, u the values ckpt holds and s = 1 / (1 + exp(-g)):
+ *   d_x_bf16        device bf16 [R_cap, 2I]: dg = d_act * u * s * (1 + g (1 - s))
+ *                   in [0, I), du = d_act * g * s in [I, 2I); FP32, rounded
+ *                   once.
+ *   act_bf16        device bf16 [R_cap, I] or NULL: g * s * u again (the second
+ *                   product's weight gradient reads it).
+ *   expert_amax     device f32 [E] or NULL: max-reduced with |dg|, |du| of each
+ *                   expert's rows before their rounding (the caller fills it
+ *                   first, e.g. with zeros).  This is the amax that
+ *                   ep_nvfp4_colwise_rht_bf16 takes for d_x (TE PR #3755, PR
+ *                   description: the dGLU epilogue's exact amax).  A NaN
+ *                   gradient makes it NaN.
+ *   d_act_bf16      device bf16 [R_cap, I], row pitch ld_act (a multiple of 8).
+ *   expert_offsets, E, R_cap: as in ep_swiglu.
+ */
+ep_status ep_swiglu_backward(const void *d_act_bf16, int64_t ld_act,
+                             const uint8_t *ckpt, int64_t R_cap, int64_t I,
+                             const int32_t *expert_offsets, int E,
+                             void *d_x_bf16, void *act_bf16, float *expert_amax,
+                             uint32_t *dev_status, void *stream);
+
+/*
+ * ep_nvfp4_matvec -- products of a few tokens with NVFP4 expert weights, for
+ * decode batches: y[t*k + j] = W_e x, e = topk_idx(t, j).
+ *   x_bf16          device bf16, row pitch ld_x elements (a multiple of 8), 16-byte
+ *                   aligned: [T, K], row t for all of token t's slots, or with
+ *                   x_per_slot [T*k, K], row t*k + j.  K % 32 == 0.
+ *   w_rows          device u8 [E*N, S], S = ep_nvfp4_row_bytes(K), 16-byte
+ *                   aligned: output feature n of expert e is packed row e*N + n,
+ *                   as ep_nvfp4_pack packs a row of K elements (the trailer's
+ *                   row scale is used, its other words are not).
+ *   topk_idx        device int32 [T*k]; -1 = dropped slot (its row of y is
+ *                   zero, its row of x is not read); an id >= E or < -1 raises
+ *                   EP_DEV_ERR_BAD_EXPERT and is dropped.  NULL: E = 1 and
+ *                   k = 1, a dense layer.  Unlike in a routing plan, an id may
+ *                   repeat within a token.
+ *   y_bf16          device bf16 [T*k, N].
+ * Any T is accepted; the call is made for batches whose time is the reading
+ * of the weights.  FP32 accumulation in a fixed order, the row scale applied
+ * to the sum, one rounding.
+ */
+ep_status ep_nvfp4_matvec(const void *x_bf16, int64_t T, int64_t K,
+                          int64_t ld_x, int x_per_slot, const uint8_t *w_rows,
+                          int E, int64_t N, const int32_t *topk_idx, int k,
+                          void *y_bf16, uint32_t *dev_status, void *stream);
 
 /* Human-readable name of a status code. */
 const char *ep_status_string(int status);

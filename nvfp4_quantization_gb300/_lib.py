@@ -19,6 +19,8 @@ _U64 = ctypes.c_uint64
 EP_OK = 0
 EP_ROUND_RNE = 0
 EP_ROUND_SR = 1
+EP_DTYPE_BF16 = 0
+EP_DTYPE_F32 = 1
 EP_DEV_ERR_BAD_EXPERT = 1
 EP_DEV_ERR_DUP_EXPERT = 2
 EP_DEV_ERR_TIMEOUT = 4
@@ -29,7 +31,8 @@ EP_ROUTE_STATIC_SCRATCH_BYTES = 262144   # mirrors the macro in include/epq.h
 SYMBOLS = ("ep_nvfp4_row_bytes", "ep_rows_capacity", "ep_route_workspace_bytes", "ep_route_plan",
            "ep_route_plan_noalloc", "ep_nvfp4_pack", "ep_nvfp4_dispatch", "ep_nvfp4_unpack", "ep_nvfp4_direct_receive",
            "ep_nvfp4_direct_receive_swizzled", "ep_nvfp4_colwise_rht_bf16", "ep_mxfp8_pack",
-           "ep_mxfp8_colwise", "ep_status_string")
+           "ep_mxfp8_colwise", "ep_pack", "ep_combine", "ep_combine_backward", "ep_swiglu", "ep_swiglu_backward",
+           "ep_nvfp4_matvec", "ep_status_string")
 
 
 class EpGrouped(ctypes.Structure):
@@ -75,6 +78,19 @@ def _declare(L):
     L.ep_mxfp8_colwise.restype = _I32
     L.ep_mxfp8_pack.argtypes = [_P, _I64, _I64, _P, _I32, _P, _P, _I32, _P, _I64, _P, _P]
     L.ep_mxfp8_pack.restype = _I32
+    L.ep_pack.argtypes = [_P, _I32, _I64, _I64, _I64, _P, _I32, _P, _P, _I32, _P, _I64, _P, _P]
+    L.ep_pack.restype = _I32
+    L.ep_combine.argtypes = [_P, _I32, _I64, _I64, _I64, _P, _I32, _P, _I64, _I32, _P, _P, _P]
+    L.ep_combine.restype = _I32
+    L.ep_combine_backward.argtypes = [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _P, _I32, _P, _P, _I32, _P, _I64, _P,
+                                      _P, _P]
+    L.ep_combine_backward.restype = _I32
+    L.ep_swiglu.argtypes = [_P, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _P]
+    L.ep_swiglu.restype = _I32
+    L.ep_swiglu_backward.argtypes = [_P, _I64, _P, _I64, _I64, _P, _I32, _P, _P, _P, _P, _P]
+    L.ep_swiglu_backward.restype = _I32
+    L.ep_nvfp4_matvec.argtypes = [_P, _I64, _I64, _I64, _I32, _P, _I32, _I64, _P, _I32, _P, _P, _P]
+    L.ep_nvfp4_matvec.restype = _I32
     L.ep_status_string.argtypes = [_I32]; L.ep_status_string.restype = ctypes.c_char_p
 
 

@@ -13,7 +13,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import EP_ROUND_RNE, EP_ROUND_SR, EpGrouped, check
+from ._lib import EP_DTYPE_BF16, EP_DTYPE_F32, EP_ROUND_RNE, EP_ROUND_SR, EpGrouped, check
 
 DEFAULT_ALIGNMENT = 128
 DEFAULT_SIGN_MASK = 0xA53C
@@ -290,3 +290,293 @@ def ep_mxfp8_pack(tokens: torch.Tensor, plan: RoutePlan, buf: torch.Tensor | Non
                                   _stream(stream))
     check("ep_mxfp8_pack", st)
     return buf
+
+
+# ---------------------------------------------------------------------------
+# around the expert products: rows without quantisation, combine, activation,
+# products of a few tokens
+# ---------------------------------------------------------------------------
+_DTYPE = {torch.bfloat16: EP_DTYPE_BF16, torch.float32: EP_DTYPE_F32}
+
+
+def _need_dense(t: torch.Tensor, name: str, shape: tuple, dtype, device):
+    """A contiguous operand of exactly this shape, on this device."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _need_rows(t: torch.Tensor, name: str, dtypes) -> int:
+    """A 2-D CUDA input whose rows are contiguous; returns its row pitch in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    n, width = t.shape
+    pitch, unit = t.stride()
+    if width > 1 and unit != 1:
+        raise ValueError(f"{name} must have contiguous rows (its last stride is {unit})")
+    if n <= 1:
+        return max(width, 1)
+    if pitch < width:
+        raise ValueError(f"{name} must not have overlapping rows (row stride {pitch}, width {width})")
+    return pitch
+
+
+def _need_plan(plan: RoutePlan, T: int, device):
+    if plan.T != T:
+        raise ValueError(f"the plan is for {plan.T} tokens, got {T}")
+    for t, name, n in ((plan.dest, "plan.dest", T * plan.k), (plan.offsets, "plan.offsets", plan.E + 1),
+                       (plan.counts, "plan.counts", plan.E), (plan.status, "plan.status", 1)):
+        if t.dtype != torch.int32 or t.device != device or t.numel() < n or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor with at least {n} entries on {device}")
+
+
+def _empty(shape, dtype, device, stream):
+    """An output on `stream` (the allocator must know where it is used)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _status_or_new(status, device, stream):
+    if status is None:
+        if stream is None:
+            return new_status(device)
+        with torch.cuda.stream(stream):
+            return new_status(device)
+    if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
+        raise ValueError(f"status must be an int32 tensor on {device}")
+    return status
+
+
+def ep_pack(tokens: torch.Tensor, plan: RoutePlan, rows: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """BF16 or FP32 tokens [T, H] -> expert rows [R_cap, H], copied as they
+    are; padding rows are zeroed.  The gradient is ``ep_combine(d_rows, plan)``."""
+    ld = _need_rows(tokens, "tokens", _DTYPE)
+    T, H = tokens.shape
+    _need_plan(plan, T, tokens.device)
+    if rows is None:
+        rows = _empty((plan.R_cap, H), tokens.dtype, tokens.device, stream)
+    else:
+        _need_dense(rows, "rows", (plan.R_cap, H), tokens.dtype, tokens.device)
+    st = _lib.lib().ep_pack(_ptr(tokens), _DTYPE[tokens.dtype], T, H, ld, _ptr(plan.dest), plan.k, _ptr(plan.offsets),
+                            _ptr(plan.counts), plan.E, _ptr(rows), plan.R_cap, _ptr(plan.status), _stream(stream))
+    check("ep_pack", st)
+    return rows
+
+
+def ep_combine(rows: torch.Tensor, plan: RoutePlan | None = None, weights: torch.Tensor | None = None,
+               topk_idx: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Expert rows -> tokens [T, H]: ``out[t] = sum_j weights[t, j] * row(t, j)``.
+
+    With ``plan`` the rows are in its order ([R_cap, H]); with ``topk_idx``
+    (int32 [T, k]) they are in slot order ([T*k, H], as ep_nvfp4_matvec writes
+    them) and slots whose id is negative are left out.  ``weights`` f32 [T, k],
+    None = 1."""
+    ld = _need_rows(rows, "rows", _DTYPE)
+    n, H = rows.shape
+    dev = rows.device
+    if (plan is None) == (topk_idx is None):
+        raise ValueError("ep_combine takes either plan or topk_idx")
+    if plan is not None:
+        T, k, index = plan.T, plan.k, plan.dest
+        _need_plan(plan, T, dev)
+        if status is None:
+            status = plan.status
+    else:
+        if topk_idx.dim() != 2:
+            raise ValueError("topk_idx must have two dimensions")
+        T, k = topk_idx.shape
+        _need_dense(topk_idx, "topk_idx", (T, k), torch.int32, dev)
+        if n != T * k:
+            raise ValueError(f"rows in slot order must be {T * k}, got {n}")
+        index = topk_idx
+    status = _status_or_new(status, dev, stream)
+    if weights is not None:
+        _need_dense(weights, "weights", (T, k), torch.float32, dev)
+    if out is None:
+        out = _empty((T, H), rows.dtype, dev, stream)
+    else:
+        _need_dense(out, "out", (T, H), rows.dtype, dev)
+    st = _lib.lib().ep_combine(_ptr(rows), _DTYPE[rows.dtype], n, H, ld, _ptr(index), int(plan is None),
+                               _ptr(weights), T, k, _ptr(out), _ptr(status), _stream(stream))
+    check("ep_combine", st)
+    return out
+
+
+def ep_combine_backward(d_out: torch.Tensor, plan: RoutePlan, weights: torch.Tensor | None = None,
+                        rows: torch.Tensor | None = None, d_rows: torch.Tensor | None = None,
+                        d_weights: torch.Tensor | None = None,
+                        stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Gradients of ``ep_combine(rows, plan, weights)`` from d_out [T, H]:
+    (d_rows [R_cap, H], d_weights f32 [T, k]).  Without ``rows`` the weights'
+    gradient is not computed (None)."""
+    ld = _need_rows(d_out, "d_out", _DTYPE)
+    T, H = d_out.shape
+    dev, dt = d_out.device, d_out.dtype
+    _need_plan(plan, T, dev)
+    k, R_cap = plan.k, plan.R_cap
+    ld_rows = H
+    if weights is not None:
+        _need_dense(weights, "weights", (T, k), torch.float32, dev)
+    if rows is not None:
+        ld_rows = _need_rows(rows, "rows", (dt,))
+        if rows.shape != (R_cap, H) or rows.device != dev:
+            raise ValueError(f"rows must have shape {(R_cap, H)} on {dev}, got {tuple(rows.shape)} on {rows.device}")
+        if d_weights is None:
+            d_weights = _empty((T, k), torch.float32, dev, stream)
+        else:
+            _need_dense(d_weights, "d_weights", (T, k), torch.float32, dev)
+    elif d_weights is not None:
+        raise ValueError("d_weights needs rows")
+    if d_rows is None:
+        d_rows = _empty((R_cap, H), dt, dev, stream)
+    else:
+        _need_dense(d_rows, "d_rows", (R_cap, H), dt, dev)
+    st = _lib.lib().ep_combine_backward(_ptr(d_out), _DTYPE[dt], T, H, ld, _ptr(rows), ld_rows, _ptr(plan.dest),
+                                        _ptr(weights), k, _ptr(plan.offsets), _ptr(plan.counts), plan.E,
+                                        _ptr(d_rows), R_cap, _ptr(d_weights), _ptr(plan.status), _stream(stream))
+    check("ep_combine_backward", st)
+    return d_rows, d_weights
+
+
+def swiglu_checkpoint_bytes(R_cap: int, I: int) -> int:
+    """Bytes of ep_swiglu's checkpoint: E4M3 data [R_cap, 2I], then E8M0 scales [R_cap, 2I/32]."""
+    return R_cap * 2 * I + R_cap * (2 * I // 32)
+
+
+def _need_offsets(offsets, E: int, device):
+    if offsets is None:
+        if E != 1:
+            raise ValueError("E must be 1 without offsets")
+    elif offsets.dtype != torch.int32 or offsets.device != device or offsets.numel() < E + 1 or \
+            not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous int32 tensor with at least {E + 1} entries on {device}")
+
+
+def ep_swiglu(x: torch.Tensor, offsets: torch.Tensor | None = None, E: int = 1, act: torch.Tensor | None = None,
+              ckpt: torch.Tensor | None = None, checkpoint: bool = True, status: torch.Tensor | None = None,
+              stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Gated activation of x [R_cap, 2I] (gate columns, then up columns), BF16:
+    (act [R_cap, I], checkpoint).  The checkpoint (uint8,
+    swiglu_checkpoint_bytes) holds x in MXFP8 for ep_swiglu_backward;
+    ``checkpoint=False`` leaves it out (None).  With ``offsets`` (int32 [E+1])
+    only rows [0, offsets[E]) are processed."""
+    ld = _need_rows(x, "x", (torch.bfloat16,))
+    R_cap, width = x.shape
+    if width % 64:
+        raise ValueError(f"x needs two halves of a multiple of 32 columns, got {width}")
+    I, dev = width // 2, x.device
+    _need_offsets(offsets, E, dev)
+    if act is None:
+        act = _empty((R_cap, I), torch.bfloat16, dev, stream)
+    else:
+        _need_dense(act, "act", (R_cap, I), torch.bfloat16, dev)
+    if ckpt is not None:
+        _need_dense(ckpt, "ckpt", (swiglu_checkpoint_bytes(R_cap, I),), torch.uint8, dev)
+    elif checkpoint:
+        ckpt = _empty((swiglu_checkpoint_bytes(R_cap, I),), torch.uint8, dev, stream)
+    status = _status_or_new(status, dev, stream)
+    st = _lib.lib().ep_swiglu(_ptr(x), ld, R_cap, I, _ptr(offsets), E, _ptr(act), _ptr(ckpt), _ptr(status),
+                              _stream(stream))
+    check("ep_swiglu", st)
+    return act, ckpt
+
+
+def ep_swiglu_backward(d_act: torch.Tensor, ckpt: torch.Tensor, offsets: torch.Tensor | None = None, E: int = 1,
+                       d_x: torch.Tensor | None = None, act: torch.Tensor | None = None, recompute: bool = False,
+                       expert_amax: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                       stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Gradient of ep_swiglu from its checkpoint: (d_x [R_cap, 2I], act).  The
+    activation is written again (from the checkpoint's values) into ``act``, or
+    into a new tensor with ``recompute=True``; else None.  ``expert_amax`` (f32
+    [E], filled by the caller, e.g. with zeros) receives the max of each
+    expert's |d_x| before rounding: the amax of ep_nvfp4_colwise_rht_bf16."""
+    ld = _need_rows(d_act, "d_act", (torch.bfloat16,))
+    R_cap, I = d_act.shape
+    dev = d_act.device
+    if I % 32:
+        raise ValueError(f"d_act needs a multiple of 32 columns, got {I}")
+    _need_offsets(offsets, E, dev)
+    _need_dense(ckpt, "ckpt", (swiglu_checkpoint_bytes(R_cap, I),), torch.uint8, dev)
+    if d_x is None:
+        d_x = _empty((R_cap, 2 * I), torch.bfloat16, dev, stream)
+    else:
+        _need_dense(d_x, "d_x", (R_cap, 2 * I), torch.bfloat16, dev)
+    if act is not None:
+        _need_dense(act, "act", (R_cap, I), torch.bfloat16, dev)
+    elif recompute:
+        act = _empty((R_cap, I), torch.bfloat16, dev, stream)
+    if expert_amax is not None:
+        _need_dense(expert_amax, "expert_amax", (E,), torch.float32, dev)
+    status = _status_or_new(status, dev, stream)
+    st = _lib.lib().ep_swiglu_backward(_ptr(d_act), ld, _ptr(ckpt), R_cap, I, _ptr(offsets), E, _ptr(d_x), _ptr(act),
+                                       _ptr(expert_amax), _ptr(status), _stream(stream))
+    check("ep_swiglu_backward", st)
+    return d_x, act
+
+
+def ep_nvfp4_pack_weights(w: torch.Tensor, rounding: int = EP_ROUND_RNE, seed: int = 0, stream=None) -> torch.Tensor:
+    """BF16 weights [E, N, K] -> packed NVFP4 rows [E, N, row_bytes(K)] for
+    ep_nvfp4_matvec: ep_nvfp4_pack with every row in its own place."""
+    _need_cuda(w, "w", torch.bfloat16)
+    if w.dim() != 3:
+        raise ValueError("w must have three dimensions [E, N, K]")
+    E, N, K = w.shape
+    n = E * N
+
+    def pack():
+        offsets = torch.tensor([0, n], dtype=torch.int32, device=w.device)
+        plan = RoutePlan(offsets, offsets[1:], torch.arange(max(n, 1), dtype=torch.int32, device=w.device), n, 1, 1,
+                         DEFAULT_ALIGNMENT, n, new_status(w.device))
+        return ep_nvfp4_pack(w.view(n, K), plan, rounding=rounding, seed=seed)
+
+    if stream is None:
+        rows = pack()
+    else:
+        with torch.cuda.stream(stream):
+            rows = pack()
+    return rows.view(E, N, rows.shape[1])
+
+
+def ep_nvfp4_matvec(x: torch.Tensor, w_rows: torch.Tensor, topk_idx: torch.Tensor | None = None,
+                    y: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Products of a few tokens with NVFP4 expert weights, for decode batches:
+    ``y[t*k + j] = W[topk_idx[t, j]] @ x``, BF16 [T*k, N].
+
+    ``w_rows`` uint8 [E, N, row_bytes(K)] (ep_nvfp4_pack_weights); ``x`` BF16
+    [T, K] (one row for all slots of a token) or [T*k, K] (one per slot).
+    Slots whose id is -1 give zero rows.  Without ``topk_idx`` E must be 1 and
+    the call is a dense layer on x [T, K]."""
+    ld = _need_rows(x, "x", (torch.bfloat16,))
+    n, K = x.shape
+    dev = x.device
+    if w_rows.dim() != 3:
+        raise ValueError("w_rows must have three dimensions [E, N, row_bytes(K)]")
+    E, N, S = w_rows.shape
+    _need_dense(w_rows, "w_rows", (E, N, row_bytes(K)), torch.uint8, dev)
+    if topk_idx is None:
+        if E != 1:
+            raise ValueError("w_rows of several experts needs topk_idx")
+        T, k = n, 1
+    else:
+        if topk_idx.dim() != 2:
+            raise ValueError("topk_idx must have two dimensions")
+        T, k = topk_idx.shape
+        _need_dense(topk_idx, "topk_idx", (T, k), torch.int32, dev)
+        if n != T and n != T * k:
+            raise ValueError(f"x must have {T} or {T * k} rows, got {n}")
+    if y is None:
+        y = _empty((T * k, N), torch.bfloat16, dev, stream)
+    else:
+        _need_dense(y, "y", (T * k, N), torch.bfloat16, dev)
+    status = _status_or_new(status, dev, stream)
+    st = _lib.lib().ep_nvfp4_matvec(_ptr(x), T, K, ld, int(n != T), _ptr(w_rows), E, N, _ptr(topk_idx), k, _ptr(y),
+                                    _ptr(status), _stream(stream))
+    check("ep_nvfp4_matvec", st)
+    return y

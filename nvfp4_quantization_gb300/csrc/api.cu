@@ -378,4 +378,235 @@ ep_status ep_nvfp4_direct_receive_swizzled(const uint8_t *rows, int64_t R_cap, i
                                  dev_status, stream, true);
 }
 
+// Checks of the unquantised [rows, H] buffers (elements of 2 or 4 bytes).
+static bool dtype_ok(int dtype) { return dtype == EP_DTYPE_BF16 || dtype == EP_DTYPE_F32; }
+
+static bool aligned_to(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes) == 0; }
+
+static bool layer_shape_ok(int64_t T, int64_t H, int k, int E)
+{
+    return T >= 0 && T <= (int64_t)INT32_MAX / 32 && H >= 1 && H <= (1 << 20) && k >= 1 && k <= 32 && E >= 1 &&
+           E <= 1024;
+}
+
+static bool pitch_ok(int64_t ld, int64_t H) { return ld >= H && ld <= (int64_t)INT32_MAX; }
+
+static ep_status scatter_common(const void *src, int dtype, int64_t T, int64_t H, int64_t ld_src, const void *rows_in,
+                                int64_t ld_in, const int32_t *dest, const float *weights, int k,
+                                const int32_t *offsets, const int32_t *counts, int E, void *rows_out, int64_t R_cap,
+                                float *d_weights, uint32_t *dev_status, void *stream)
+{
+    if (!offsets || !counts || !dev_status || (T > 0 && (!src || !dest)) || (R_cap > 0 && !rows_out) ||
+        (T > 0 && R_cap > 0 && d_weights && !rows_in))
+        return EP_ERR_NULL;
+    if (!layer_shape_ok(T, H, k, E) || !pitch_ok(ld_src, H) || (rows_in && !pitch_ok(ld_in, H)))
+        return EP_ERR_SHAPE;
+    if (R_cap < 0 || R_cap > (int64_t)INT32_MAX)
+        return EP_ERR_CAPACITY;
+    if (!dtype_ok(dtype))
+        return EP_ERR_ARG;
+    const int elem = dtype == EP_DTYPE_F32 ? 4 : 2;
+    if (!aligned_to(src, elem) || !aligned_to(rows_in, elem) || !aligned_to(rows_out, elem) ||
+        !aligned_to(weights, 4) || !aligned_to(d_weights, 4))
+        return EP_ERR_ALIGN;
+    const int dev = device_of(T > 0 ? src : (const void *)offsets);
+    if (dev < 0 || !on_device(rows_in, dev) || !on_device(dest, dev) || !on_device(weights, dev) ||
+        !on_device(offsets, dev) || !on_device(counts, dev) || !on_device(rows_out, dev) ||
+        !on_device(d_weights, dev) || !on_device(dev_status, dev))
+        return EP_ERR_DEVICE;
+    DeviceGuard g(dev);
+    if (!g.ok)
+        return EP_ERR_DEVICE;
+    LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
+    epq::ScatterArgs a = {};
+    a.src = src;
+    a.ld_src = ld_src;
+    a.rows_in = d_weights ? rows_in : nullptr;
+    a.ld_in = ld_in;
+    a.dest = dest;
+    a.offsets = offsets;
+    a.counts = counts;
+    a.weights = weights;
+    a.rows_out = rows_out;
+    a.d_weights = d_weights;
+    a.T = (int)T;
+    a.k = k;
+    a.H = (int)H;
+    a.E = E;
+    a.R_cap = (int)R_cap;
+    a.status = dev_status;
+    return cuda_status(epq::launch_scatter(c, a, dtype));
+}
+
+ep_status ep_pack(const void *tokens, int dtype, int64_t T, int64_t H, int64_t ld_tokens, const int32_t *dest, int k,
+                  const int32_t *expert_offsets, const int32_t *expert_counts, int E, void *rows, int64_t R_cap,
+                  uint32_t *dev_status, void *stream)
+{
+    return scatter_common(tokens, dtype, T, H, ld_tokens, nullptr, H, dest, nullptr, k, expert_offsets, expert_counts,
+                          E, rows, R_cap, nullptr, dev_status, stream);
+}
+
+ep_status ep_combine_backward(const void *d_out, int dtype, int64_t T, int64_t H, int64_t ld_out, const void *rows,
+                              int64_t ld_rows, const int32_t *dest, const float *weights, int k,
+                              const int32_t *expert_offsets, const int32_t *expert_counts, int E, void *d_rows,
+                              int64_t R_cap, float *d_weights, uint32_t *dev_status, void *stream)
+{
+    return scatter_common(d_out, dtype, T, H, ld_out, rows, ld_rows, dest, weights, k, expert_offsets, expert_counts,
+                          E, d_rows, R_cap, d_weights, dev_status, stream);
+}
+
+ep_status ep_combine(const void *rows, int dtype, int64_t R_cap, int64_t H, int64_t ld_rows, const int32_t *index,
+                     int slot_order, const float *weights, int64_t T, int k, void *out, uint32_t *dev_status,
+                     void *stream)
+{
+    if (!dev_status || (T > 0 && (!out || (R_cap > 0 && !rows) || (!index && !slot_order))))
+        return EP_ERR_NULL;
+    if (!layer_shape_ok(T, H, k, 1) || !pitch_ok(ld_rows, H))
+        return EP_ERR_SHAPE;
+    if (R_cap < 0 || R_cap > (int64_t)INT32_MAX || (slot_order && R_cap < T * (int64_t)k))
+        return EP_ERR_CAPACITY;
+    if (!dtype_ok(dtype))
+        return EP_ERR_ARG;
+    const int elem = dtype == EP_DTYPE_F32 ? 4 : 2;
+    if (!aligned_to(rows, elem) || !aligned_to(out, elem) || !aligned_to(weights, 4))
+        return EP_ERR_ALIGN;
+    const int dev = device_of(R_cap > 0 && T > 0 ? rows : (const void *)dev_status);
+    if (dev < 0 || !on_device(index, dev) || !on_device(weights, dev) || !on_device(out, dev) ||
+        !on_device(dev_status, dev))
+        return EP_ERR_DEVICE;
+    DeviceGuard g(dev);
+    if (!g.ok)
+        return EP_ERR_DEVICE;
+    LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
+    epq::CombineArgs a = {};
+    a.rows = rows;
+    a.ld_rows = ld_rows;
+    a.index = index;
+    a.slot_order = slot_order != 0;
+    a.weights = weights;
+    a.out = out;
+    a.T = (int)T;
+    a.k = k;
+    a.H = (int)H;
+    a.R_cap = (int)R_cap;
+    a.status = dev_status;
+    return cuda_status(epq::launch_combine(c, a, dtype));
+}
+
+// Checks shared by the two passes of the gated activation, on their strided
+// input (`width` columns).
+static ep_status swiglu_checks(const void *in, int64_t ld, int64_t width, int64_t R_cap, int64_t I,
+                               const int32_t *offsets, int E, const uint32_t *dev_status)
+{
+    if (!dev_status || (R_cap > 0 && !in))
+        return EP_ERR_NULL;
+    if (I < 32 || I % 32 != 0 || I > (1 << 19) || E < 1 || E > 1024 || (!offsets && E != 1) || !pitch_ok(ld, width))
+        return EP_ERR_SHAPE;
+    if (R_cap < 0 || R_cap > (int64_t)INT32_MAX)
+        return EP_ERR_CAPACITY;
+    if (!aligned16(in) || ld % 8 != 0)
+        return EP_ERR_ALIGN;
+    return EP_OK;
+}
+
+ep_status ep_swiglu(const void *x_bf16, int64_t ld_x, int64_t R_cap, int64_t I, const int32_t *expert_offsets, int E,
+                    void *act_bf16, uint8_t *ckpt, uint32_t *dev_status, void *stream)
+{
+    ep_status st = swiglu_checks(x_bf16, ld_x, 2 * I, R_cap, I, expert_offsets, E, dev_status);
+    if (st != EP_OK)
+        return st;
+    if (R_cap > 0 && !act_bf16)
+        return EP_ERR_NULL;
+    if (!aligned16(act_bf16) || !aligned16(ckpt))
+        return EP_ERR_ALIGN;
+    const int dev = device_of(R_cap > 0 ? x_bf16 : (const void *)dev_status);
+    if (dev < 0 || !on_device(expert_offsets, dev) || !on_device(act_bf16, dev) || !on_device(ckpt, dev) ||
+        !on_device(dev_status, dev))
+        return EP_ERR_DEVICE;
+    DeviceGuard g(dev);
+    if (!g.ok)
+        return EP_ERR_DEVICE;
+    LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
+    epq::SwigluArgs a = {};
+    a.x = (const uint16_t *)x_bf16;
+    a.ld = ld_x;
+    a.ckpt_out = ckpt;
+    a.offsets = expert_offsets;
+    a.R_cap = (int)R_cap;
+    a.I = (int)I;
+    a.E = E;
+    a.act = (uint16_t *)act_bf16;
+    a.status = dev_status;
+    return cuda_status(epq::launch_swiglu(c, a));
+}
+
+ep_status ep_swiglu_backward(const void *d_act_bf16, int64_t ld_act, const uint8_t *ckpt, int64_t R_cap, int64_t I,
+                             const int32_t *expert_offsets, int E, void *d_x_bf16, void *act_bf16, float *expert_amax,
+                             uint32_t *dev_status, void *stream)
+{
+    ep_status st = swiglu_checks(d_act_bf16, ld_act, I, R_cap, I, expert_offsets, E, dev_status);
+    if (st != EP_OK)
+        return st;
+    if (R_cap > 0 && (!ckpt || !d_x_bf16))
+        return EP_ERR_NULL;
+    if (!aligned16(ckpt) || !aligned16(d_x_bf16) || !aligned16(act_bf16) || !aligned_to(expert_amax, 4))
+        return EP_ERR_ALIGN;
+    const int dev = device_of(R_cap > 0 ? d_act_bf16 : (const void *)dev_status);
+    if (dev < 0 || !on_device(ckpt, dev) || !on_device(expert_offsets, dev) || !on_device(d_x_bf16, dev) ||
+        !on_device(act_bf16, dev) || !on_device(expert_amax, dev) || !on_device(dev_status, dev))
+        return EP_ERR_DEVICE;
+    DeviceGuard g(dev);
+    if (!g.ok)
+        return EP_ERR_DEVICE;
+    LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
+    epq::SwigluArgs a = {};
+    a.d_act = (const uint16_t *)d_act_bf16;
+    a.ld = ld_act;
+    a.ckpt = ckpt;
+    a.offsets = expert_offsets;
+    a.R_cap = (int)R_cap;
+    a.I = (int)I;
+    a.E = E;
+    a.act = (uint16_t *)act_bf16;
+    a.d_x = (uint16_t *)d_x_bf16;
+    a.expert_amax = expert_amax;
+    a.status = dev_status;
+    return cuda_status(epq::launch_swiglu_backward(c, a));
+}
+
+ep_status ep_nvfp4_matvec(const void *x_bf16, int64_t T, int64_t K, int64_t ld_x, int x_per_slot,
+                          const uint8_t *w_rows, int E, int64_t N, const int32_t *topk_idx, int k, void *y_bf16,
+                          uint32_t *dev_status, void *stream)
+{
+    if (!w_rows || !dev_status || (T > 0 && (!x_bf16 || !y_bf16)))
+        return EP_ERR_NULL;
+    if (!shape_ok(T, K, k, E) || N < 1 || N > (1 << 20) || !pitch_ok(ld_x, K) || (T > 0 && !topk_idx && (E != 1 || k != 1)))
+        return EP_ERR_SHAPE;
+    if (!aligned16(x_bf16) || ld_x % 8 != 0 || !aligned16(w_rows) || !aligned_to(y_bf16, 2))
+        return EP_ERR_ALIGN;
+    const int dev = device_of(w_rows);
+    if (dev < 0 || !on_device(x_bf16, dev) || !on_device(topk_idx, dev) || !on_device(y_bf16, dev) ||
+        !on_device(dev_status, dev))
+        return EP_ERR_DEVICE;
+    DeviceGuard g(dev);
+    if (!g.ok)
+        return EP_ERR_DEVICE;
+    LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
+    epq::MatvecArgs a = {};
+    a.x = (const uint16_t *)x_bf16;
+    a.ld_x = ld_x;
+    a.per_slot = x_per_slot != 0;
+    a.w = w_rows;
+    a.S = epq::row_bytes(K);
+    a.topk = topk_idx;
+    a.y = (uint16_t *)y_bf16;
+    a.T = (int)T;
+    a.k = k;
+    a.K = (int)K;
+    a.N = (int)N;
+    a.E = E;
+    a.status = dev_status;
+    return cuda_status(epq::launch_matvec(c, a));
+}
+
 } // extern "C"

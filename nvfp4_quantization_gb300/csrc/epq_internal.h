@@ -116,6 +116,71 @@ cudaError_t launch_direct_receive(const LaunchCtx &c, const uint8_t *rows, int R
                                   int rounding, uint64_t seed, uint32_t sign_mask,
                                   uint32_t *status, bool swz = false, const float *amax_in = nullptr);
 
+// Element types of the unquantised row buffers (EP_DTYPE_* of the C ABI).
+constexpr int kBf16 = 0;
+constexpr int kF32 = 1;
+
+struct CombineArgs {
+    const void *rows;        // [R_cap, H], row pitch ld_rows elements
+    int64_t ld_rows;
+    const int32_t *index;    // [T * k]: row of the slot, or (slot_order) negative = dropped; NULL: none dropped
+    bool slot_order;         // slot (t, j) is row t * k + j
+    const float *weights;    // [T * k] or NULL (1)
+    void *out;               // [T, H]
+    int T, k, H, R_cap;
+    uint32_t *status;
+};
+
+cudaError_t launch_combine(const LaunchCtx &c, const CombineArgs &a, int dtype);
+
+// ep_pack (weights, rows_in, d_weights NULL) and ep_combine_backward.
+struct ScatterArgs {
+    const void *src;         // [T, H], row pitch ld_src elements
+    int64_t ld_src;
+    const void *rows_in;     // [R_cap, H], row pitch ld_in; with d_weights only
+    int64_t ld_in;
+    const int32_t *dest, *offsets, *counts;
+    const float *weights;    // [T * k] or NULL (1)
+    void *rows_out;          // [R_cap, H]
+    float *d_weights;        // [T * k] or NULL
+    int T, k, H, E, R_cap;
+    int pad_split;           // CTAs that share an expert's padding rows (set by the launcher)
+    uint32_t *status;
+};
+
+cudaError_t launch_scatter(const LaunchCtx &c, const ScatterArgs &a, int dtype);
+
+struct SwigluArgs {
+    const uint16_t *x;       // forward: [R_cap, 2I], row pitch ld
+    const uint16_t *d_act;   // backward: [R_cap, I], row pitch ld
+    int64_t ld;
+    const uint8_t *ckpt;     // backward: data [R_cap, 2I], then scales [R_cap, 2I/32]
+    uint8_t *ckpt_out;       // forward: the same, or NULL
+    const int32_t *offsets;  // [E + 1] or NULL: all R_cap rows, one expert
+    int R_cap, I, E;
+    uint16_t *act;           // [R_cap, I]; backward: or NULL
+    uint16_t *d_x;           // backward: [R_cap, 2I]
+    float *expert_amax;      // backward: [E] or NULL
+    uint32_t *status;
+};
+
+cudaError_t launch_swiglu(const LaunchCtx &c, const SwigluArgs &a);
+cudaError_t launch_swiglu_backward(const LaunchCtx &c, const SwigluArgs &a);
+
+struct MatvecArgs {
+    const uint16_t *x;       // [T or T * k, K], row pitch ld_x
+    int64_t ld_x;
+    bool per_slot;           // x has a row per slot, not per token
+    const uint8_t *w;        // packed NVFP4 rows [E * N, S]
+    int64_t S;
+    const int32_t *topk;     // [T * k] or NULL: expert 0
+    uint16_t *y;             // [T * k, N]
+    int T, k, K, N, E;
+    uint32_t *status;
+};
+
+cudaError_t launch_matvec(const LaunchCtx &c, const MatvecArgs &a);
+
 // Tensor map of a 2-D byte tensor [outer][inner] with a row pitch of `pitch`
 // bytes and a box of box_outer rows x box_inner bytes (no swizzle, L2
 // promotion 256 B); false if the driver refuses it.
