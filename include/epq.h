@@ -512,7 +512,7 @@ ep_status ep_swiglu_backward(const void *d_act_bf16, int64_t ld_act,
  * decode batches: y[t*k + j] = W_e x, e = topk_idx(t, j).
  *   x_bf16          device bf16, row pitch ld_x elements (a multiple of 8), 16-byte
  *                   aligned: [T, K], row t for all of token t's slots, or with
- *                   x_per_slot [T*k, K], row t*k + j.  K % 32 == 0.
+ *                   x_per_slot [T*k, K], row t*k + j.  K % 32 == 0, K <= 32768.
  *   w_rows          device u8 [E*N, S], S = ep_nvfp4_row_bytes(K), 16-byte
  *                   aligned: output feature n of expert e is packed row e*N + n,
  *                   as ep_nvfp4_pack packs a row of K elements (the trailer's

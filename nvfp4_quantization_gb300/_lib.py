@@ -97,6 +97,8 @@ def _declare(L):
 def lib() -> ctypes.CDLL:
     """The loaded libepq.so (built first if needed)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()

@@ -296,7 +296,23 @@ def ep_mxfp8_pack(tokens: torch.Tensor, plan: RoutePlan, buf: torch.Tensor | Non
 # around the expert products: rows without quantisation, combine, activation,
 # products of a few tokens
 # ---------------------------------------------------------------------------
+# These calls are made for single tokens too, where a call's host time is its
+# time: operands go to the library as plain addresses, and the current stream's
+# handle is read without building a Stream object (3 us of a 10 us call).
 _DTYPE = {torch.bfloat16: EP_DTYPE_BF16, torch.float32: EP_DTYPE_F32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(stream, device) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _need_dense(t: torch.Tensor, name: str, shape: tuple, dtype, device):
@@ -363,8 +379,8 @@ def ep_pack(tokens: torch.Tensor, plan: RoutePlan, rows: torch.Tensor | None = N
         rows = _empty((plan.R_cap, H), tokens.dtype, tokens.device, stream)
     else:
         _need_dense(rows, "rows", (plan.R_cap, H), tokens.dtype, tokens.device)
-    st = _lib.lib().ep_pack(_ptr(tokens), _DTYPE[tokens.dtype], T, H, ld, _ptr(plan.dest), plan.k, _ptr(plan.offsets),
-                            _ptr(plan.counts), plan.E, _ptr(rows), plan.R_cap, _ptr(plan.status), _stream(stream))
+    st = _lib.lib().ep_pack(_at(tokens), _DTYPE[tokens.dtype], T, H, ld, _at(plan.dest), plan.k, _at(plan.offsets),
+                            _at(plan.counts), plan.E, _at(rows), plan.R_cap, _at(plan.status), _stream_of(stream, tokens.device))
     check("ep_pack", st)
     return rows
 
@@ -403,8 +419,8 @@ def ep_combine(rows: torch.Tensor, plan: RoutePlan | None = None, weights: torch
         out = _empty((T, H), rows.dtype, dev, stream)
     else:
         _need_dense(out, "out", (T, H), rows.dtype, dev)
-    st = _lib.lib().ep_combine(_ptr(rows), _DTYPE[rows.dtype], n, H, ld, _ptr(index), int(plan is None),
-                               _ptr(weights), T, k, _ptr(out), _ptr(status), _stream(stream))
+    st = _lib.lib().ep_combine(_at(rows), _DTYPE[rows.dtype], n, H, ld, _at(index), int(plan is None),
+                               _at(weights), T, k, _at(out), _at(status), _stream_of(stream, dev))
     check("ep_combine", st)
     return out
 
@@ -438,9 +454,9 @@ def ep_combine_backward(d_out: torch.Tensor, plan: RoutePlan, weights: torch.Ten
         d_rows = _empty((R_cap, H), dt, dev, stream)
     else:
         _need_dense(d_rows, "d_rows", (R_cap, H), dt, dev)
-    st = _lib.lib().ep_combine_backward(_ptr(d_out), _DTYPE[dt], T, H, ld, _ptr(rows), ld_rows, _ptr(plan.dest),
-                                        _ptr(weights), k, _ptr(plan.offsets), _ptr(plan.counts), plan.E,
-                                        _ptr(d_rows), R_cap, _ptr(d_weights), _ptr(plan.status), _stream(stream))
+    st = _lib.lib().ep_combine_backward(_at(d_out), _DTYPE[dt], T, H, ld, _at(rows), ld_rows, _at(plan.dest),
+                                        _at(weights), k, _at(plan.offsets), _at(plan.counts), plan.E,
+                                        _at(d_rows), R_cap, _at(d_weights), _at(plan.status), _stream_of(stream, dev))
     check("ep_combine_backward", st)
     return d_rows, d_weights
 
@@ -482,8 +498,8 @@ def ep_swiglu(x: torch.Tensor, offsets: torch.Tensor | None = None, E: int = 1, 
     elif checkpoint:
         ckpt = _empty((swiglu_checkpoint_bytes(R_cap, I),), torch.uint8, dev, stream)
     status = _status_or_new(status, dev, stream)
-    st = _lib.lib().ep_swiglu(_ptr(x), ld, R_cap, I, _ptr(offsets), E, _ptr(act), _ptr(ckpt), _ptr(status),
-                              _stream(stream))
+    st = _lib.lib().ep_swiglu(_at(x), ld, R_cap, I, _at(offsets), E, _at(act), _at(ckpt), _at(status),
+                              _stream_of(stream, dev))
     check("ep_swiglu", st)
     return act, ckpt
 
@@ -515,8 +531,8 @@ def ep_swiglu_backward(d_act: torch.Tensor, ckpt: torch.Tensor, offsets: torch.T
     if expert_amax is not None:
         _need_dense(expert_amax, "expert_amax", (E,), torch.float32, dev)
     status = _status_or_new(status, dev, stream)
-    st = _lib.lib().ep_swiglu_backward(_ptr(d_act), ld, _ptr(ckpt), R_cap, I, _ptr(offsets), E, _ptr(d_x), _ptr(act),
-                                       _ptr(expert_amax), _ptr(status), _stream(stream))
+    st = _lib.lib().ep_swiglu_backward(_at(d_act), ld, _at(ckpt), R_cap, I, _at(offsets), E, _at(d_x), _at(act),
+                                       _at(expert_amax), _at(status), _stream_of(stream, dev))
     check("ep_swiglu_backward", st)
     return d_x, act
 
@@ -576,7 +592,7 @@ def ep_nvfp4_matvec(x: torch.Tensor, w_rows: torch.Tensor, topk_idx: torch.Tenso
     else:
         _need_dense(y, "y", (T * k, N), torch.bfloat16, dev)
     status = _status_or_new(status, dev, stream)
-    st = _lib.lib().ep_nvfp4_matvec(_ptr(x), T, K, ld, int(n != T), _ptr(w_rows), E, N, _ptr(topk_idx), k, _ptr(y),
-                                    _ptr(status), _stream(stream))
+    st = _lib.lib().ep_nvfp4_matvec(_at(x), T, K, ld, int(n != T), _at(w_rows), E, N, _at(topk_idx), k, _at(y),
+                                    _at(status), _stream_of(stream, dev))
     check("ep_nvfp4_matvec", st)
     return y

@@ -4,8 +4,26 @@
 //
 // The weights are packed NVFP4 rows as the pack writes them (E2M1 codes, an
 // E4M3 scale per 16 elements, an FP32 row scale in the trailer): one row per
-// output feature.  Products and sums are FP32; the row scale is applied to the
-// finished sum, which is rounded once.
+// output feature.
+//
+// Bound: the rows of the experts in use are read once from HBM; everything
+// else is small.  To keep up, the arithmetic goes to the warp-level matrix
+// instruction (m16n8k16, f16 inputs, FP32 accumulators) with 16 weight rows as
+// M and up to 8 slots of the same expert as N:
+//  - code * s_b has at most six significant bits and lies in [2^-10, 2688], so
+//    it is exact in f16, and one accumulator runs over the whole row; S(n) is
+//    applied to the finished sum.
+//  - x is BF16; a slot's elements are scaled by one power of two that brings
+//    its largest to [2^14, 2^15) and taken to f16: exact for every element
+//    within 2^-28 of the largest, and off by at most 2^-40 of the largest
+//    below that (FP32 accumulation loses more).  Infinities and NaN stay.
+//  - the summation index is free to be permuted: lane (g, t) of a warp takes
+//    64 consecutive elements of rows g and g + 8 (two 16-byte loads each), so
+//    a warp reads 128 contiguous bytes of every row, and no fragment shuffle
+//    is needed; x lies in shared memory in the order in which the lanes want
+//    it.
+// A row's sum is computed by one warp in one order, whatever else is in the
+// batch: a slot's result does not depend on the other slots.
 #include "epq_device.cuh"
 #include "epq_internal.h"
 
@@ -13,47 +31,333 @@ namespace epq {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 16;        // weight rows of a warp's tile
+constexpr int kGroup = 8;        // slots that share a pass over an expert's rows
+constexpr int kStep = 256;       // elements of a row that a warp takes at a time
+constexpr int kDepth = 4;        // steps in flight per warp
+constexpr int kMaxE = 1024;
+constexpr int kMaxSmem = 200 * 1024;   // of x: three slots at the longest row, K = 32768
 
-// One warp per (slot, output feature).
-__global__ void __launch_bounds__(kThreads) matvec_kernel(MatvecArgs a)
+// A lane's share of a step: 64 elements of rows g and g + 8.
+struct Step {
+    uint4 lo0, lo1, hi0, hi1;
+    uint32_t slo, shi;    // four block scales each
+    float rlo, rhi;       // row scales (with a tile's last step)
+};
+
+// One word of eight E2M1 codes -> four f16 pairs (exact).
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4])
 {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int blocks = (a.N + kThreads / 32 - 1) / (kThreads / 32);
-    const int n = blockIdx.x % blocks * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t s = blockIdx.x / blocks;
-    if (n >= a.N)
-        return;
-    int e = a.topk ? __ldg(a.topk + s) : 0;
-    if (e < -1 || e >= a.E) {
-        if (lane == 0)
-            raise_status(a.status, kDevErrBadExpert);
-        e = -1;
-    }
-    float acc = 0.0f, row_scale = 0.0f;
-    if (e >= 0) {
-        const uint8_t *row = a.w + ((int64_t)e * a.N + n) * a.S;
-        const uint16_t *x = a.x + (a.per_slot ? s : s / a.k) * a.ld_x;
-        row_scale = __ldg(reinterpret_cast<const float *>(row + a.S - 16));
-        for (int q = lane; q < a.K / 8; q += 32) {
-            const uint32_t cw = __ldg(reinterpret_cast<const uint32_t *>(row) + q);
-            const float sc = e4m3_to_f32(__ldg(row + a.K / 2 + (q >> 1)));
-            float part = 0.0f;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Block scales 2i and 2i + 1 of a word of four, each in both halves.
+__device__ __forceinline__ void scale_pair(uint32_t two, uint32_t &s0, uint32_t &s1)
+{
+    const uint32_t v = cvt_f16x2_from_e4m3x2(two);
+    s0 = __byte_perm(v, v, 0x1010);
+    s1 = __byte_perm(v, v, 0x3232);
+}
+
+// 16 rows x 64 elements of this lane's share against its slot's x.
+__device__ __forceinline__ void multiply(float (&acc)[4], const Step &st, const uint4 *xs, int stride, bool on)
+{
+    uint32_t slo[4], shi[4];
+    scale_pair(st.slo & 0xffffu, slo[0], slo[1]);
+    scale_pair(st.slo >> 16, slo[2], slo[3]);
+    scale_pair(st.shi & 0xffffu, shi[0], shi[1]);
+    scale_pair(st.shi >> 16, shi[2], shi[3]);
+    const uint32_t lo[8] = {st.lo0.x, st.lo0.y, st.lo0.z, st.lo0.w, st.lo1.x, st.lo1.y, st.lo1.z, st.lo1.w};
+    const uint32_t hi[8] = {st.hi0.x, st.hi0.y, st.hi0.z, st.hi0.w, st.hi1.x, st.hi1.y, st.hi1.z, st.hi1.w};
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const float2 v = f16x2_to_f32x2(cvt_f16x2_from_e2m1x2((cw >> (8 * b)) & 0xffu));
-                part = fmaf(v.x, u2f((uint32_t)__ldg(x + q * 8 + 2 * b) << 16), part);
-                part = fmaf(v.y, u2f((uint32_t)__ldg(x + q * 8 + 2 * b + 1) << 16), part);
+    for (int j = 0; j < 8; ++j) {
+        uint4 b = make_uint4(0, 0, 0, 0);
+        if (on)
+            b = xs[j * stride];
+        uint32_t l[4], h[4];
+        codes_to_f16(lo[j], l);
+        codes_to_f16(hi[j], h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            l[i] = hmul2_rn(l[i], slo[j >> 1]);
+            h[i] = hmul2_rn(h[i], shi[j >> 1]);
+        }
+        mma16816(acc, l[0], h[0], l[1], h[1], b.x, b.y);
+        mma16816(acc, l[2], h[2], l[3], h[3], b.z, b.w);
+    }
+}
+
+struct Shared {
+    int first[kMaxE + 1];   // groups of slots before expert e
+    int count[kMaxE];       // slots of expert e
+    int warp_sum[kWarps];
+    int slot[kGroup];       // the group's slots
+    int shift[kGroup];      // x was multiplied by 2^shift
+};
+
+__device__ __forceinline__ int expert_of_slot(const MatvecArgs &a, int s) { return a.topk ? __ldg(a.topk + s) : 0; }
+
+// Exclusive prefix of one value per thread over the CTA; *total gets the sum.
+__device__ __forceinline__ int cta_prefix(int v, int *warp_sum, int *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    __syncthreads();
+    if (lane == 31)
+        warp_sum[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        before += i < warp ? warp_sum[i] : 0;
+        all += warp_sum[i];
+    }
+    *total = all;
+    return before + x - v;
+}
+
+// Number of groups of each expert, as a prefix over the experts; slots without
+// an expert get their zero rows here.
+__device__ int count_groups(const MatvecArgs &a, Shared &sh, int per_group)
+{
+    const int slots = a.T * a.k;
+    for (int e = threadIdx.x; e < a.E; e += kThreads)
+        sh.count[e] = 0;
+    __syncthreads();
+    for (int s = threadIdx.x; s < slots; s += kThreads) {
+        const int e = expert_of_slot(a, s);
+        if (e >= 0 && e < a.E)
+            atomicAdd(&sh.count[e], 1);
+        else if (e != -1 && blockIdx.x == 0)
+            raise_status(a.status, kDevErrBadExpert);
+    }
+    __syncthreads();
+    for (int s = blockIdx.x; s < slots; s += gridDim.x) {
+        const int e = expert_of_slot(a, s);
+        if (e < 0 || e >= a.E)
+            for (int n = threadIdx.x; n < a.N; n += kThreads)
+                a.y[(int64_t)s * a.N + n] = 0;
+    }
+    constexpr int kPer = kMaxE / kThreads;
+    int g[kPer], mine = 0, total;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        g[i] = e < a.E ? (sh.count[e] + per_group - 1) / per_group : 0;
+        mine += g[i];
+    }
+    int at = cta_prefix(mine, sh.warp_sum, &total);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        if (e < a.E)
+            sh.first[e] = at;
+        at += g[i];
+    }
+    if (threadIdx.x == 0)
+        sh.first[a.E] = total;
+    __syncthreads();
+    return total;
+}
+
+// The slots of expert e with rank [from, from + per_group), in slot order.
+__device__ void find_slots(const MatvecArgs &a, Shared &sh, int e, int from, int per_group)
+{
+    const int slots = a.T * a.k, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int share = (slots + kThreads - 1) / kThreads * 32;   // slots of a warp, whole 32s
+    const int s0 = warp * share, s1 = min(s0 + share, slots);
+    int mine = 0;
+    for (int s = s0 + lane; s < s1; s += 32)
+        mine += expert_of_slot(a, s) == e;
+    int total;
+    int rank = cta_prefix(mine, sh.warp_sum, &total);
+    rank = __shfl_sync(0xffffffffu, rank, 0);                   // of the warp's first match
+    for (int s = s0; s < s1; s += 32) {
+        const bool hit = s + lane < s1 && expert_of_slot(a, s + lane) == e;
+        const uint32_t all = __ballot_sync(0xffffffffu, hit);
+        const int r = rank + __popc(all & ((1u << lane) - 1)) - from;
+        if (hit && r >= 0 && r < per_group)
+            sh.slot[r] = s + lane;
+        rank += __popc(all);
+    }
+    __syncthreads();
+}
+
+// x of the group's m slots -> f16 in shared memory: 8 elements k..k+7 of slot
+// c at 16-byte place (((k / 256) * 8 + (k / 8) % 8) * 4 + (k / 64) % 4) * m + c,
+// which is where lane (c, (k / 64) % 4) looks for word (k / 8) % 8 of its 64.
+__device__ void stage_x(const MatvecArgs &a, Shared &sh, int m, uint4 *xs, int steps)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // two warps a slot (the pair agrees on the largest by reading all of it)
+    for (int c = warp >> 1; c < m; c += kWarps / 2) {
+        const int s = sh.slot[c];
+        const uint4 *x = reinterpret_cast<const uint4 *>(a.x + (int64_t)(a.per_slot ? s : s / a.k) * a.ld_x);
+        const int nq = a.K / 8;
+        uint32_t top = 0;
+        for (int q = lane; q < nq; q += 32) {
+            const uint4 v = __ldg(x + q);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t l = w[i] & 0x7fffu, h = (w[i] >> 16) & 0x7fffu;
+                top = max(top, l < 0x7f80u ? l : 0u);
+                top = max(top, h < 0x7f80u ? h : 0u);
             }
-            acc = fmaf(part, sc, acc);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        // 2^(14 - exponent of the largest); a subnormal largest counts as 2^-126
+        const int shift = top ? 14 - (max((int)(top >> 7), 1) - 127) : 0;
+        // 2^shift in two factors: shift reaches 140
+        const float f0 = exp2i(shift / 2), f1 = exp2i(shift - shift / 2);
+        if (lane == 0)
+            sh.shift[c] = shift;
+        for (int q = lane + 32 * (warp & 1); q < steps * 32; q += 64) {
+            uint4 o = make_uint4(0, 0, 0, 0);
+            if (q < nq) {
+                const uint4 v = __ldg(x + q);
+                o.x = cvt_f16x2(u2f(v.x << 16) * f0 * f1, u2f(v.x & 0xffff0000u) * f0 * f1);
+                o.y = cvt_f16x2(u2f(v.y << 16) * f0 * f1, u2f(v.y & 0xffff0000u) * f0 * f1);
+                o.z = cvt_f16x2(u2f(v.z << 16) * f0 * f1, u2f(v.z & 0xffff0000u) * f0 * f1);
+                o.w = cvt_f16x2(u2f(v.w << 16) * f0 * f1, u2f(v.w & 0xffff0000u) * f0 * f1);
+            }
+            xs[(((q >> 5) * 8 + (q & 7)) * 4 + ((q >> 3) & 3)) * m + c] = o;
         }
     }
-    for (int o = 16; o; o >>= 1)
-        acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0)
-        a.y[s * a.N + n] = (uint16_t)cvt_bf16x2(e >= 0 ? acc * row_scale : 0.0f, 0.0f);
+}
+
+// Persistent: the (group of slots, tile of rows) pairs are dealt to the CTAs
+// in contiguous ranges, so a CTA meets few groups; its warps take the tiles of
+// a group in turn, each with kDepth steps of loads in flight.
+__global__ void __launch_bounds__(kThreads, 1) matvec_kernel(MatvecArgs a, int per_group)
+{
+    extern __shared__ uint4 xs[];
+    __shared__ Shared sh;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int groups = count_groups(a, sh, per_group);
+    const int tiles = (a.N + kTile - 1) / kTile;
+    const int steps = (a.K + kStep - 1) / kStep;
+    const int64_t total = (int64_t)groups * tiles;
+    int64_t at = total * blockIdx.x / gridDim.x;
+    const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+
+    while (at < end) {
+        const int group = (int)(at / tiles);
+        const int tile0 = (int)(at - (int64_t)group * tiles);
+        const int tile1 = (int)min((int64_t)tiles, end - (int64_t)group * tiles);
+        at += tile1 - tile0;
+        int e = 0, hi = a.E - 1;            // last expert with first[e] <= group
+        while (e < hi) {
+            const int mid = (e + hi + 1) >> 1;
+            if (sh.first[mid] <= group)
+                e = mid;
+            else
+                hi = mid - 1;
+        }
+        const int from = (group - sh.first[e]) * per_group;
+        const int m = min(per_group, sh.count[e] - from);
+
+        // this warp's steps over its tiles of the group
+        const uint8_t *w = a.w + (int64_t)e * a.N * a.S;
+        const int mine = tile0 + warp < tile1 ? (tile1 - tile0 - warp + kWarps - 1) / kWarps : 0;
+        const int n_steps = mine * steps;
+        int l_tile = tile0 + warp, l_step = 0;      // next step to load
+        Step st[kDepth];
+        auto load = [&](Step &p) {
+            const int row = l_tile * kTile + g;
+            const uint8_t *lo = w + (int64_t)min(row, a.N - 1) * a.S;
+            const uint8_t *hi8 = w + (int64_t)min(row + 8, a.N - 1) * a.S;
+            const int k0 = l_step * kStep + t * 64;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            p.lo0 = p.lo1 = p.hi0 = p.hi1 = zero;
+            p.slo = p.shi = 0;
+            if (k0 < a.K) {
+                p.lo0 = __ldg(reinterpret_cast<const uint4 *>(lo + k0 / 2));
+                p.hi0 = __ldg(reinterpret_cast<const uint4 *>(hi8 + k0 / 2));
+                p.slo = __ldg(reinterpret_cast<const uint32_t *>(lo + a.K / 2 + k0 / 16));
+                p.shi = __ldg(reinterpret_cast<const uint32_t *>(hi8 + a.K / 2 + k0 / 16));
+                if (k0 + 32 < a.K) {
+                    p.lo1 = __ldg(reinterpret_cast<const uint4 *>(lo + k0 / 2 + 16));
+                    p.hi1 = __ldg(reinterpret_cast<const uint4 *>(hi8 + k0 / 2 + 16));
+                } else {                    // the word's upper half is past the scales
+                    p.slo &= 0xffffu;
+                    p.shi &= 0xffffu;
+                }
+            }
+            if (++l_step == steps) {
+                p.rlo = __ldg(reinterpret_cast<const float *>(lo + a.S - 16));
+                p.rhi = __ldg(reinterpret_cast<const float *>(hi8 + a.S - 16));
+                l_step = 0;
+                l_tile += kWarps;
+            }
+        };
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+            if (d < n_steps)
+                load(st[d]);
+
+        find_slots(a, sh, e, from, per_group);
+        stage_x(a, sh, m, xs, steps);
+        __syncthreads();
+
+        const bool on = g < m;
+        const uint4 *x_lane = xs + t * m + g;
+        float acc[4] = {};
+        int c_tile = tile0 + warp, c_step = 0;
+        for (int i = 0; i < n_steps; i += kDepth) {
+#pragma unroll
+            for (int d = 0; d < kDepth; ++d) {
+                if (i + d >= n_steps)
+                    break;
+                multiply(acc, st[d], x_lane + (int64_t)c_step * 32 * m, 4 * m, on);
+                if (++c_step == steps) {
+                    const int row = c_tile * kTile + g;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int c = 2 * t + (v & 1), n = row + (v & 2 ? 8 : 0);
+                        if (c < m && n < a.N) {
+                            // in 64 bits: the two scales together may pass FP32's range
+                            const double r = (double)acc[v] * (v & 2 ? st[d].rhi : st[d].rlo);
+                            const double back = __hiloint2double((1023 - sh.shift[c]) << 20, 0);
+                            a.y[(int64_t)sh.slot[c] * a.N + n] = (uint16_t)cvt_bf16x2((float)(r * back), 0.0f);
+                        }
+                        acc[v] = 0.0f;
+                    }
+                    c_step = 0;
+                    c_tile += kWarps;
+                }
+                if (i + d + kDepth < n_steps)
+                    load(st[d]);
+            }
+        }
+        __syncthreads();                    // before the next group's x and slots
+    }
 }
 
 } // namespace
@@ -63,10 +367,17 @@ cudaError_t launch_matvec(const LaunchCtx &c, const MatvecArgs &a)
     const int64_t slots = (int64_t)a.T * a.k;
     if (slots == 0)
         return cudaSuccess;
-    const int64_t grid = slots * ((a.N + kThreads / 32 - 1) / (kThreads / 32));
-    if (grid > (int64_t)INT32_MAX)
-        return cudaErrorInvalidValue;
-    return launch_pdl(matvec_kernel, dim3((unsigned)grid), dim3(kThreads), 0, c.stream, a);
+    const int x_bytes = (a.K + kStep - 1) / kStep * kStep * 2;   // of one slot
+    static std::atomic<uint32_t> done[2] = {};
+    cudaError_t e = ensure_smem_limit(matvec_kernel, c.device, kMaxSmem, done);
+    if (e != cudaSuccess)
+        return e;
+    int per_group = kMaxSmem / x_bytes;
+    per_group = per_group > kGroup ? kGroup : per_group;
+    if (per_group > slots)
+        per_group = (int)slots;
+    return launch_pdl(matvec_kernel, dim3((unsigned)c.num_sms), dim3(kThreads), (size_t)per_group * x_bytes, c.stream,
+                      a, per_group);
 }
 
 } // namespace epq
