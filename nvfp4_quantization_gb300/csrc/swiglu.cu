@@ -10,10 +10,14 @@
 //             amax_e = max over the rows of expert e of |dg|, |du| (FP32,
 //             before the rounding to BF16)
 //
-// Both are one pass over the data.  A thread owns 8 consecutive gate columns
-// and the 8 up columns beside them (16-byte BF16 loads and stores, 8-byte
-// loads and stores of E4M3); the four lanes of a block of 32 share its
-// maximum.
+// Both are one pass over the data, and what bounds them is how many
+// instructions a pair (g, u) costs beside its 8 bytes of traffic: arithmetic
+// runs on FP32 pairs, maxima on BF16 pairs, and the sigmoid is one ex2 and one
+// reciprocal.  A thread owns 8 consecutive gate columns and the 8 up columns
+// beside them (16-byte BF16 loads and stores, 8-byte loads and stores of
+// E4M3); the four lanes of a block of 32 share its maximum.  A CTA walks a
+// contiguous range of (rows, columns) blocks, and the next block's loads are
+// in flight while the current one is computed.
 #include "epq_device.cuh"
 #include "epq_internal.h"
 
@@ -22,40 +26,60 @@ namespace epq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunkRows = 16;   // rows that a CTA takes at a time
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + expf(-g)); }
-
-__device__ __forceinline__ void unpack8(uint4 r, float (&f)[8])
+__device__ __forceinline__ float ex2_approx(float x)
 {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = u2f(w[i] << 16);
-        f[2 * i + 1] = u2f(w[i] & 0xffff0000u);
-    }
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+__device__ __forceinline__ float rcp_approx(float x)
 {
-    return make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// Largest |x| (BF16 bits) of 8 elements; `finite`: infinities and NaN left out.
-template <bool FINITE>
-__device__ __forceinline__ uint32_t absmax8(uint4 r)
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// 1 / (1 + exp(-g)) of two finite values.  exp(-g) = 2^t (1 + r ln 2) with
+// t = RN(-g log2 e) and r what the product lost: its rounding error (exact by
+// a fused multiply-add; Dekker, "A floating-point technique for extending the
+// available precision", 1971) and the part of log2 e below FP32.  Without r
+// the result would lose as many bits as |t| has.
+__device__ __forceinline__ float2 sigmoid2(float2 g)
 {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-        if (!FINITE || lo < 0x7f80u)
-            m = max(m, lo);
-        if (!FINITE || hi < 0x7f80u)
-            m = max(m, hi);
-    }
-    return m;
+    const float hi = -1.44269504088896340736f;
+    const float lo = (float)(-1.44269504088896340736 - (double)hi);
+    const float2 t = mul2(g, both(hi));
+    float2 r = fma2(g, both(hi), make_float2(-t.x, -t.y));
+    r = fma2(g, both(lo), r);
+    const float2 c = fma2(r, both(0.69314718055994530942f), both(1.0f));
+    const float2 e = mul2(make_float2(ex2_approx(t.x), ex2_approx(t.y)), c);
+    const float2 d = add2(e, both(1.0f));
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) { return make_float2(u2f(w << 16), u2f(w & 0xffff0000u)); }
+
+__device__ __forceinline__ uint32_t to_bf16_pair(float2 v) { return cvt_bf16x2(v.x, v.y); }
+
+// max(|a|, |b|) per BF16 half; a NaN in either wins (signs are meaningless).
+__device__ __forceinline__ uint32_t absmax_pair(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// max(m, |a|, |b|), NaN if one of them is.
+__device__ __forceinline__ float max_abs_nan(float m, float2 v)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(fabsf(v.x)), "f"(fabsf(v.y)));
+    return d;
 }
 
 __device__ __forceinline__ uint32_t quad_max(uint32_t m)
@@ -64,44 +88,64 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m)
     return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
-// 8 elements of a block of 32 held by four neighbouring lanes -> E4M3 codes
-// and the scale byte.  Every lane of the warp calls this.  An infinity or NaN
-// is stored as E4M3's NaN, under the scale of the block's finite elements, so
-// it shows in the backward pass instead of passing for 448.
-__device__ __forceinline__ uint2 encode8(uint4 r, const float (&f)[8], uint32_t &sbyte)
+// Exponent of a block whose largest |x| has BF16 bits b (finite): the smallest
+// e >= -127 with max <= 448 * 2^e; 448 = 1.75 * 2^8 is exponent field 135,
+// mantissa field 96, so e = field - 135, plus 1 above that mantissa.
+__device__ __forceinline__ int block_exponent(uint32_t b)
 {
-    uint32_t b = quad_max(absmax8<false>(r));
-    const bool bad = b >= 0x7f80u;
-    if (__any_sync(0xffffffffu, bad)) {
-        const uint32_t fin = quad_max(absmax8<true>(r));
-        b = bad ? fin : b;
-    }
-    // 448 = 1.75 * 2^8: BF16 exponent field 135, mantissa field 96
-    const int ef = (int)(b >> 7), mt = (int)(b & 0x7fu);
-    const int e = max(-127, ef == 0 ? -127 : ef - 135 + (mt > 96 ? 1 : 0));
-    sbyte = (uint32_t)(e + 127);
-    const float inv = exp2i(-e);
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] = f[i] * inv;
-        if (bad && (f2u(f[i]) & 0x7f800000u) == 0x7f800000u)
-            v[i] = u2f(0x7fffffffu);
-    }
-    return make_uint2(cvt_e4m3x2(v[0], v[1]) | cvt_e4m3x2(v[2], v[3]) << 16,
-                      cvt_e4m3x2(v[4], v[5]) | cvt_e4m3x2(v[6], v[7]) << 16);
+    const int e = (int)((b + 31u) >> 7) - 135;
+    return b < 0x80u ? -127 : max(-127, e);
 }
 
-__device__ __forceinline__ void decode8(uint2 c, uint32_t sbyte, float (&f)[8])
+// Blocks with an infinity or a NaN: those elements become E4M3's NaN, under
+// the scale of the block's finite elements, so they show in the backward pass
+// instead of passing for 448.  Kept out of line: it is rare.
+__device__ __noinline__ uint2 encode8_nonfinite(const uint4 *r, uint32_t *sbyte)
 {
-    const float s = sbyte ? u2f(sbyte << 23) : u2f(0x00400000u);   // 2^(sbyte - 127)
-    const uint32_t two[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 v = f16x2_to_f32x2(cvt_f16x2_from_e4m3x2(two[i]));
-        f[2 * i] = v.x * s;
-        f[2 * i + 1] = v.y * s;
+    const uint32_t w[4] = {r->x, r->y, r->z, r->w};
+    uint32_t b = 0;
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t m = (w[i >> 1] >> (16 * (i & 1))) & 0x7fffu;
+        b = max(b, m < 0x7f80u ? m : 0u);
     }
+    b = quad_max(b);
+    const int e = block_exponent(b);
+    *sbyte = (uint32_t)(e + 127);
+    uint32_t o[2] = {0, 0};
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t h = (w[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+        const float v = (h & 0x7f80u) == 0x7f80u ? u2f(0x7fffffffu) : u2f(h << 16) * exp2i(-e);
+        o[i >> 2] |= (cvt_e4m3x2(v, 0.0f) & 0xffu) << (8 * (i & 3));
+    }
+    return make_uint2(o[0], o[1]);
+}
+
+// 8 elements of a block of 32 held by four neighbouring lanes -> E4M3 codes
+// and the scale byte.  Every lane of the warp calls this.
+__device__ __forceinline__ uint2 encode8(uint4 r, uint32_t &sbyte)
+{
+    const uint32_t m = absmax_pair(absmax_pair(r.x, r.y), absmax_pair(r.z, r.w));
+    const uint32_t b = quad_max(max(m & 0x7fffu, (m >> 16) & 0x7fffu));
+    if (__any_sync(0xffffffffu, b >= 0x7f80u))
+        return encode8_nonfinite(&r, &sbyte);
+    const int e = block_exponent(b);
+    sbyte = (uint32_t)(e + 127);
+    const float2 inv = both(exp2i(-e));
+    const float2 v0 = mul2(bf16_pair(r.x), inv), v1 = mul2(bf16_pair(r.y), inv);
+    const float2 v2 = mul2(bf16_pair(r.z), inv), v3 = mul2(bf16_pair(r.w), inv);
+    return make_uint2(cvt_e4m3x2(v0.x, v0.y) | cvt_e4m3x2(v1.x, v1.y) << 16,
+                      cvt_e4m3x2(v2.x, v2.y) | cvt_e4m3x2(v3.x, v3.y) << 16);
+}
+
+// Two E4M3 codes times 2^(sbyte - 127).
+__device__ __forceinline__ float2 decode2(uint32_t two, float2 s)
+{
+    return mul2(f16x2_to_f32x2(cvt_f16x2_from_e4m3x2(two)), s);
+}
+
+__device__ __forceinline__ float2 scale_of(uint32_t sbyte)
+{
+    return both(sbyte ? u2f(sbyte << 23) : u2f(0x00400000u));
 }
 
 __device__ __forceinline__ int used_rows(const SwigluArgs &a)
@@ -114,49 +158,79 @@ __device__ __forceinline__ int used_rows(const SwigluArgs &a)
     return min(R, a.R_cap);
 }
 
-// Threads are cols x (256 / cols): a warp stays within one row.
+// A CTA's walk over blocks of (256 / cols) rows x cols units of 8 columns, in
+// row order; a warp stays within one row.
+struct Walk {
+    int nu, cols, tx, ty, step, blocks, r, qb;
+    int64_t left;
+
+    __device__ __forceinline__ Walk(const SwigluArgs &a, int cols_, int R)
+        : nu(a.I / 8), cols(cols_), tx(threadIdx.x % cols_), ty(threadIdx.x / cols_), step(kThreads / cols_)
+    {
+        blocks = (nu + cols - 1) / cols;
+        const int64_t total = (int64_t)((R + step - 1) / step) * blocks;
+        const int64_t from = total * blockIdx.x / gridDim.x;
+        left = total * (blockIdx.x + 1) / gridDim.x - from;
+        r = (int)(from / blocks) * step + ty;
+        qb = (int)(from % blocks);
+    }
+    __device__ __forceinline__ int unit() const { return qb * cols + tx; }
+    __device__ __forceinline__ void next()
+    {
+        --left;
+        if (++qb == blocks) {
+            qb = 0;
+            r += step;
+        }
+    }
+};
+
 template <bool CKPT>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluArgs a, int cols)
 {
     pdl_launch_dependents();
     pdl_wait();
     const int R = used_rows(a);
-    const int nu = a.I / 8;
-    const int tx = threadIdx.x % cols, ty = threadIdx.x / cols, step = kThreads / cols;
     uint8_t *scales = CKPT ? a.ckpt_out + (int64_t)a.R_cap * 2 * a.I : nullptr;
-    for (int r0 = blockIdx.x * kChunkRows; r0 < R; r0 += gridDim.x * kChunkRows) {
-        const int r1 = min(r0 + kChunkRows, R);
-        for (int r = r0 + ty; r < r1; r += step) {
-            const uint16_t *x = a.x + (int64_t)r * a.ld;
-            for (int q0 = 0; q0 < nu; q0 += cols) {
-                const int q = q0 + tx;
-                const bool on = q < nu;
-                uint4 rg = make_uint4(0, 0, 0, 0), ru = rg;
-                if (on) {
-                    rg = __ldg(reinterpret_cast<const uint4 *>(x + q * 8));
-                    ru = __ldg(reinterpret_cast<const uint4 *>(x + a.I + q * 8));
-                }
-                float g[8], u[8], o[8];
-                unpack8(rg, g);
-                unpack8(ru, u);
+    Walk at(a, cols, R);
+    uint4 rg = make_uint4(0, 0, 0, 0), ru = rg;
+    auto fetch = [&]() {
+        if (at.left > 0 && at.r < R && at.unit() < at.nu) {
+            const uint16_t *x = a.x + (int64_t)at.r * a.ld + at.unit() * 8;
+            rg = __ldg(reinterpret_cast<const uint4 *>(x));
+            ru = __ldg(reinterpret_cast<const uint4 *>(x + a.I));
+        }
+    };
+    fetch();
+    while (at.left > 0) {
+        const uint4 g = rg, u = ru;
+        const int r = at.r, q = at.unit();
+        const bool on = r < R && q < at.nu;
+        at.next();
+        fetch();
+        const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+        uint32_t o[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    o[i] = g[i] * sigmoid(g[i]) * u[i];
-                if (on)
-                    *reinterpret_cast<uint4 *>(a.act + (int64_t)r * a.I + q * 8) = pack8(o);
-                if (CKPT) {
-                    uint32_t sg, su;
-                    const uint2 cg = encode8(rg, g, sg), cu = encode8(ru, u, su);
-                    if (on) {
-                        uint8_t *row = a.ckpt_out + (int64_t)r * 2 * a.I;
-                        *reinterpret_cast<uint2 *>(row + q * 8) = cg;
-                        *reinterpret_cast<uint2 *>(row + a.I + q * 8) = cu;
-                        if ((q & 3) == 0) {
-                            uint8_t *sr = scales + (int64_t)r * (a.I / 16);
-                            sr[q >> 2] = (uint8_t)sg;
-                            sr[a.I / 32 + (q >> 2)] = (uint8_t)su;
-                        }
-                    }
+        for (int i = 0; i < 4; ++i) {
+            // the sigmoid of +-256 is that of +-infinity; a NaN comes back with the product
+            uint32_t c;
+            asm("{\n\t.reg .b32 m;\n\tmin.bf16x2 m, %1, %2;\n\tmax.bf16x2 %0, m, %3;\n\t}"
+                : "=r"(c) : "r"(gw[i]), "r"(0x43804380u), "r"(0xc380c380u));
+            o[i] = to_bf16_pair(mul2(mul2(bf16_pair(gw[i]), sigmoid2(bf16_pair(c))), bf16_pair(uw[i])));
+        }
+        if (on)
+            *reinterpret_cast<uint4 *>(a.act + (int64_t)r * a.I + q * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (CKPT) {
+            uint32_t sg, su;
+            const uint2 cg = encode8(g, sg), cu = encode8(u, su);
+            if (on) {
+                uint8_t *row = a.ckpt_out + (int64_t)r * 2 * a.I + q * 8;
+                *reinterpret_cast<uint2 *>(row) = cg;
+                *reinterpret_cast<uint2 *>(row + a.I) = cu;
+                if ((q & 3) == 0) {
+                    uint8_t *sr = scales + (int64_t)r * (a.I / 16) + (q >> 2);
+                    sr[0] = (uint8_t)sg;
+                    sr[a.I / 32] = (uint8_t)su;
                 }
             }
         }
@@ -169,53 +243,70 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluArgs a,
     pdl_launch_dependents();
     pdl_wait();
     const int R = used_rows(a);
-    const int nu = a.I / 8;
-    const int tx = threadIdx.x % cols, ty = threadIdx.x / cols, step = kThreads / cols;
     const uint8_t *scales = a.ckpt + (int64_t)a.R_cap * 2 * a.I;
-    int cur = -1;         // expert whose rows `top` covers (the same in all lanes of a warp)
-    uint32_t top = 0;     // its largest |dg|, |du| so far, as bits (NaN is the largest)
+    Walk at(a, cols, R);
+    uint4 rd = make_uint4(0, 0, 0, 0);
+    uint2 rg = make_uint2(0, 0), ru = rg;
+    uint32_t rsg = 0, rsu = 0;
+    auto fetch = [&]() {
+        if (at.left > 0 && at.r < R && at.unit() < at.nu) {
+            const int q = at.unit();
+            const uint8_t *row = a.ckpt + (int64_t)at.r * 2 * a.I + q * 8;
+            const uint8_t *sr = scales + (int64_t)at.r * (a.I / 16) + (q >> 2);
+            rd = __ldg(reinterpret_cast<const uint4 *>(a.d_act + (int64_t)at.r * a.ld + q * 8));
+            rg = __ldg(reinterpret_cast<const uint2 *>(row));
+            ru = __ldg(reinterpret_cast<const uint2 *>(row + a.I));
+            rsg = __ldg(sr);
+            rsu = __ldg(sr + a.I / 32);
+        }
+    };
+    int cur = -1;         // expert whose rows `top` covers (the same in all lanes of a warp) ...
+    int cur_end = 0;      // ... and where they end
+    float top = 0.0f;     // its largest |dg|, |du| so far
     auto flush = [&]() {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, top);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, f2u(top));
         if (cur >= 0 && (threadIdx.x & 31) == 0 && m)
             red_max_nonneg(a.expert_amax + cur, u2f(m));
-        top = 0;
+        top = 0.0f;
     };
-    for (int r0 = blockIdx.x * kChunkRows; r0 < R; r0 += gridDim.x * kChunkRows) {
-        const int r1 = min(r0 + kChunkRows, R);
-        for (int r = r0 + ty; r < r1; r += step) {
-            if (a.expert_amax) {
-                const int e = a.offsets ? expert_of_dest(a.offsets, a.E, r) : 0;
-                if (e != cur) {
-                    flush();
-                    cur = e;
-                }
-            }
-            const uint8_t *row = a.ckpt + (int64_t)r * 2 * a.I;
-            const uint8_t *sr = scales + (int64_t)r * (a.I / 16);
-            for (int q = tx; q < nu; q += cols) {
-                const uint4 rd = __ldg(reinterpret_cast<const uint4 *>(a.d_act + (int64_t)r * a.ld + q * 8));
-                const uint2 cg = __ldg(reinterpret_cast<const uint2 *>(row + q * 8));
-                const uint2 cu = __ldg(reinterpret_cast<const uint2 *>(row + a.I + q * 8));
-                const uint32_t sg = __ldg(sr + (q >> 2)), su = __ldg(sr + a.I / 32 + (q >> 2));
-                float d[8], g[8], u[8], dg[8], du[8], o[8];
-                unpack8(rd, d);
-                decode8(cg, sg, g);
-                decode8(cu, su, u);
+    fetch();
+    while (at.left > 0) {
+        const uint4 d = rd;
+        const uint2 cg = rg, cu = ru;
+        const float2 sg = scale_of(rsg), su = scale_of(rsu);
+        const int r = at.r, q = at.unit();
+        const bool on = r < R && q < at.nu;
+        at.next();
+        fetch();
+        if (a.expert_amax && r < R && (cur < 0 || r >= cur_end)) {
+            flush();
+            cur = a.offsets ? expert_of_dest(a.offsets, a.E, r) : 0;
+            cur_end = a.offsets ? __ldg(a.offsets + cur + 1) : R;
+        }
+        if (on) {
+            const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+            const uint32_t gw[4] = {cg.x & 0xffffu, cg.x >> 16, cg.y & 0xffffu, cg.y >> 16};
+            const uint32_t uw[4] = {cu.x & 0xffffu, cu.x >> 16, cu.y & 0xffffu, cu.y >> 16};
+            uint32_t og[4], ou[4], oa[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float s = sigmoid(g[i]);
-                    const float silu = g[i] * s;
-                    du[i] = d[i] * silu;
-                    dg[i] = d[i] * u[i] * fmaf(silu, 1.0f - s, s);
-                    o[i] = silu * u[i];
-                    top = max(top, max(f2u(dg[i]) & 0x7fffffffu, f2u(du[i]) & 0x7fffffffu));
-                }
-                uint16_t *dx = a.d_x + (int64_t)r * 2 * a.I;
-                *reinterpret_cast<uint4 *>(dx + q * 8) = pack8(dg);
-                *reinterpret_cast<uint4 *>(dx + a.I + q * 8) = pack8(du);
+            for (int i = 0; i < 4; ++i) {
+                const float2 dv = bf16_pair(dw[i]), g = decode2(gw[i], sg), u = decode2(uw[i], su);
+                const float2 s = sigmoid2(g);
+                const float2 silu = mul2(g, s);
+                const float2 du = mul2(dv, silu);
+                const float2 slope = fma2(silu, fma2(s, both(-1.0f), both(1.0f)), s);
+                const float2 dg = mul2(mul2(dv, u), slope);
+                top = max_abs_nan(max_abs_nan(top, dg), du);
+                og[i] = to_bf16_pair(dg);
+                ou[i] = to_bf16_pair(du);
                 if (ACT)
-                    *reinterpret_cast<uint4 *>(a.act + (int64_t)r * a.I + q * 8) = pack8(o);
+                    oa[i] = to_bf16_pair(mul2(silu, u));
             }
+            uint16_t *dx = a.d_x + (int64_t)r * 2 * a.I + q * 8;
+            *reinterpret_cast<uint4 *>(dx) = make_uint4(og[0], og[1], og[2], og[3]);
+            *reinterpret_cast<uint4 *>(dx + a.I) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+            if (ACT)
+                *reinterpret_cast<uint4 *>(a.act + (int64_t)r * a.I + q * 8) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
         }
     }
     if (a.expert_amax)
@@ -228,11 +319,22 @@ int column_threads(int I)
     return nu <= 32 ? 32 : nu <= 64 ? 64 : nu <= 128 ? 128 : 256;
 }
 
-int grid_of(const LaunchCtx &c, int R_cap)
+// One wave of resident CTAs (or fewer, if there is less work).
+template <void (*kernel)(SwigluArgs, int)> cudaError_t launch_walk(const LaunchCtx &c, const SwigluArgs &a)
 {
-    const int64_t chunks = ((int64_t)R_cap + kChunkRows - 1) / kChunkRows;
-    const int64_t most = (int64_t)c.num_sms * 8;
-    return (int)(chunks < most ? chunks : most);
+    static std::atomic<int> resident{0};    // CTAs per SM, asked for once
+    const int cols = column_threads(a.I), step = kThreads / cols;
+    const int64_t blocks = ((int64_t)a.R_cap + step - 1) / step * ((a.I / 8 + cols - 1) / cols);
+    int per_sm = resident.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0);
+        if (e != cudaSuccess)
+            return e;
+        per_sm = per_sm < 1 ? 1 : per_sm;
+        resident.store(per_sm, std::memory_order_relaxed);
+    }
+    const int64_t wave = (int64_t)c.num_sms * per_sm;
+    return launch_pdl(kernel, dim3((unsigned)(blocks < wave ? blocks : wave)), dim3(kThreads), 0, c.stream, a, cols);
 }
 
 } // namespace
@@ -241,20 +343,14 @@ cudaError_t launch_swiglu(const LaunchCtx &c, const SwigluArgs &a)
 {
     if (a.R_cap == 0)
         return cudaSuccess;
-    const dim3 grid(grid_of(c, a.R_cap));
-    const int cols = column_threads(a.I);
-    return a.ckpt_out ? launch_pdl(swiglu_kernel<true>, grid, dim3(kThreads), 0, c.stream, a, cols)
-                      : launch_pdl(swiglu_kernel<false>, grid, dim3(kThreads), 0, c.stream, a, cols);
+    return a.ckpt_out ? launch_walk<swiglu_kernel<true>>(c, a) : launch_walk<swiglu_kernel<false>>(c, a);
 }
 
 cudaError_t launch_swiglu_backward(const LaunchCtx &c, const SwigluArgs &a)
 {
     if (a.R_cap == 0)
         return cudaSuccess;
-    const dim3 grid(grid_of(c, a.R_cap));
-    const int cols = column_threads(a.I);
-    return a.act ? launch_pdl(swiglu_backward_kernel<true>, grid, dim3(kThreads), 0, c.stream, a, cols)
-                 : launch_pdl(swiglu_backward_kernel<false>, grid, dim3(kThreads), 0, c.stream, a, cols);
+    return a.act ? launch_walk<swiglu_backward_kernel<true>>(c, a) : launch_walk<swiglu_backward_kernel<false>>(c, a);
 }
 
 } // namespace epq
