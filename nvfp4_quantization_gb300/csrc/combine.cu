@@ -261,10 +261,12 @@ bool multiple_of(const void *p, int64_t ld, int64_t H, int elem, int bytes)
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * elem) % bytes == 0 && (H * elem) % bytes == 0;
 }
 
+// Threads for a row of `units` loads: the fewest whole warps that take it in
+// the same number of passes as kThreads would.
 int block_of(int64_t units)
 {
-    const int64_t n = (units + 31) / 32 * 32;
-    return (int)(n > kThreads ? kThreads : n);
+    const int64_t passes = (units + kThreads - 1) / kThreads;
+    return (int)(((units + passes - 1) / passes + 31) / 32 * 32);
 }
 
 template <typename T, int VEC> cudaError_t combine_vec(const LaunchCtx &c, const CombineArgs &a)

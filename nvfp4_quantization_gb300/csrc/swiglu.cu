@@ -99,25 +99,27 @@ __device__ __forceinline__ int block_exponent(uint32_t b)
 
 // Blocks with an infinity or a NaN: those elements become E4M3's NaN, under
 // the scale of the block's finite elements, so they show in the backward pass
-// instead of passing for 448.  Kept out of line: it is rare.
-__device__ __noinline__ uint2 encode8_nonfinite(const uint4 *r, uint32_t *sbyte)
+// instead of passing for 448.  Kept out of line: it is rare.  Codes in x and y,
+// scale byte in z.
+__device__ __noinline__ uint3 encode8_nonfinite(uint4 r)
 {
-    const uint32_t w[4] = {r->x, r->y, r->z, r->w};
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     uint32_t b = 0;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t m = (w[i >> 1] >> (16 * (i & 1))) & 0x7fffu;
         b = max(b, m < 0x7f80u ? m : 0u);
     }
     b = quad_max(b);
     const int e = block_exponent(b);
-    *sbyte = (uint32_t)(e + 127);
     uint32_t o[2] = {0, 0};
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t h = (w[i >> 1] >> (16 * (i & 1))) & 0xffffu;
         const float v = (h & 0x7f80u) == 0x7f80u ? u2f(0x7fffffffu) : u2f(h << 16) * exp2i(-e);
         o[i >> 2] |= (cvt_e4m3x2(v, 0.0f) & 0xffu) << (8 * (i & 3));
     }
-    return make_uint2(o[0], o[1]);
+    return make_uint3(o[0], o[1], (uint32_t)(e + 127));
 }
 
 // 8 elements of a block of 32 held by four neighbouring lanes -> E4M3 codes
@@ -126,8 +128,11 @@ __device__ __forceinline__ uint2 encode8(uint4 r, uint32_t &sbyte)
 {
     const uint32_t m = absmax_pair(absmax_pair(r.x, r.y), absmax_pair(r.z, r.w));
     const uint32_t b = quad_max(max(m & 0x7fffu, (m >> 16) & 0x7fffu));
-    if (__any_sync(0xffffffffu, b >= 0x7f80u))
-        return encode8_nonfinite(&r, &sbyte);
+    if (__any_sync(0xffffffffu, b >= 0x7f80u)) {
+        const uint3 v = encode8_nonfinite(r);
+        sbyte = v.z;
+        return make_uint2(v.x, v.y);
+    }
     const int e = block_exponent(b);
     sbyte = (uint32_t)(e + 127);
     const float2 inv = both(exp2i(-e));

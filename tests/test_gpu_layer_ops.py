@@ -487,6 +487,8 @@ def test_matvec_ids():
     topk = torch.tensor([[0, 0, 2], [-1, -1, -1], [1, -1, 1], [2, 2, 2]], dtype=torch.int32, device="cuda")
     check_matvec(x, w_rows, topk, nq.ep_nvfp4_matvec(x, w_rows, topk, status=status))
     assert int(status) == 0
+    for t in range(4):       # one token alone: each of its slots is a pass of its own
+        check_matvec(x[t: t + 1], w_rows, topk[t: t + 1], nq.ep_nvfp4_matvec(x[t: t + 1], w_rows, topk[t: t + 1]))
     topk[0, 1], topk[3, 2] = 3, -2
     check_matvec(x, w_rows, topk, nq.ep_nvfp4_matvec(x, w_rows, topk, status=status))
     assert int(status) == nq.EP_DEV_ERR_BAD_EXPERT
