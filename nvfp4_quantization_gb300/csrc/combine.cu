@@ -280,7 +280,8 @@ template <typename T, int VEC> cudaError_t combine_vec(const LaunchCtx &c, const
 
 template <typename T, int VEC, bool DOT> cudaError_t scatter_vec(const LaunchCtx &c, ScatterArgs a)
 {
-    const int block = block_of(a.H / VEC);
+    const int64_t units = a.H / VEC;
+    const int block = (int)(units >= kThreads ? kThreads : (units + 31) / 32 * 32);
     a.pad_split = a.E >= 256 ? 8 : 32;
     const dim3 grid((unsigned)(a.T + a.E * a.pad_split));
     return a.k <= 2 ? launch_pdl(scatter_kernel<T, VEC, 2, DOT>, grid, dim3(block), 0, c.stream, a)

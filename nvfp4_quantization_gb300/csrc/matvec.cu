@@ -20,10 +20,12 @@
 //    (Hardware converts two codes in one instruction; taking them apart by
 //    shifts and masks instead costs 4.3 instructions a pair and twice the time.)
 //  - the summation index is free to be permuted: lane (g, t) of a warp takes
-//    64 consecutive elements of rows g and g + 8 (two 16-byte loads each), so
-//    a warp reads 128 contiguous bytes of every row, and no fragment shuffle
-//    is needed; x lies in shared memory in the order in which the lanes want
-//    it.
+//    64 consecutive elements of rows g and g + 8, so no fragment shuffle is
+//    needed; x lies in shared memory in the order in which the lanes want it.
+//  - the rows come by TMA, 16 rows x 512 elements (256 bytes of codes, 32 of
+//    scales a row) at a time, into a ring of each warp's own.  Loaded straight
+//    to registers the same fragments cost the L1 eight lines a request and
+//    held the kernel at 40 % of HBM.
 // A row's sum is computed by one warp in one order, whatever else is in the
 // batch: a slot's result does not depend on the other slots.
 #include "epq_device.cuh"
@@ -36,17 +38,16 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;        // weight rows of a warp's tile
-constexpr int kStep = 256;       // elements of a row that a warp takes at a time
-constexpr int kDepth = 4;        // steps in flight per warp
+constexpr int kHalf = 256;       // elements of a row that a warp multiplies at a time
+constexpr int kStep = 512;       // ... and loads at a time
+constexpr int kHalfBytes = kTile * kHalf / 2;     // codes of a half step
+constexpr int kCodeBytes = kTile * kStep / 2;     // of a step
+constexpr int kScaleBytes = kTile * kStep / 16;
+constexpr int kMinDepth = 2;     // steps in flight per warp
+constexpr int kMaxDepth = 3;
 constexpr int kMaxE = 1024;
 constexpr int kIds = 2048;       // slots whose expert is kept in shared memory
-constexpr int kMaxSmem = 200 * 1024;   // of x: three slots at the longest row, K = 32768
-
-// A lane's share of a step: 64 elements of rows g and g + 8.
-struct Step {
-    uint4 lo0, lo1, hi0, hi1;
-    uint32_t slo, shi;    // four block scales each
-};
+constexpr int kMaxSmem = 212 * 1024;   // dynamic: the warps' rings and x
 
 // One word of eight E2M1 codes -> four f16 pairs (exact).
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4])
@@ -77,18 +78,24 @@ __device__ __forceinline__ void scale_pair(uint32_t two, uint32_t &s0, uint32_t 
     s1 = __byte_perm(v, v, 0x3232);
 }
 
-// 16 rows x 64 elements of this lane's share against its column of x, whose
-// words lie 4 * G places apart.
+// Half a step of 16 rows: this lane's 64 elements of rows g and g + 8 against
+// its column of x, whose words lie 4 * G places apart.  `c0`, `c1`: the places of
+// the lane's two 16-byte chunks of row g (row g + 8 is 1024 bytes on).
 template <int G>
-__device__ __forceinline__ void multiply(float (&acc)[4], const Step &st, const uint4 *xs)
+__device__ __forceinline__ void multiply(float (&acc)[4], const uint8_t *c0, const uint8_t *c1, const uint8_t *scales,
+                                         const uint4 *xs)
 {
+    const uint32_t two_lo = *reinterpret_cast<const uint32_t *>(scales);
+    const uint32_t two_hi = *reinterpret_cast<const uint32_t *>(scales + 8 * (kStep / 16));
+    const uint4 lo0 = *reinterpret_cast<const uint4 *>(c0), lo1 = *reinterpret_cast<const uint4 *>(c1);
+    const uint4 hi0 = *reinterpret_cast<const uint4 *>(c0 + 1024), hi1 = *reinterpret_cast<const uint4 *>(c1 + 1024);
     uint32_t slo[4], shi[4];
-    scale_pair(st.slo & 0xffffu, slo[0], slo[1]);
-    scale_pair(st.slo >> 16, slo[2], slo[3]);
-    scale_pair(st.shi & 0xffffu, shi[0], shi[1]);
-    scale_pair(st.shi >> 16, shi[2], shi[3]);
-    const uint32_t lo[8] = {st.lo0.x, st.lo0.y, st.lo0.z, st.lo0.w, st.lo1.x, st.lo1.y, st.lo1.z, st.lo1.w};
-    const uint32_t hi[8] = {st.hi0.x, st.hi0.y, st.hi0.z, st.hi0.w, st.hi1.x, st.hi1.y, st.hi1.z, st.hi1.w};
+    scale_pair(two_lo & 0xffffu, slo[0], slo[1]);
+    scale_pair(two_lo >> 16, slo[2], slo[3]);
+    scale_pair(two_hi & 0xffffu, shi[0], shi[1]);
+    scale_pair(two_hi >> 16, shi[2], shi[3]);
+    const uint32_t lo[8] = {lo0.x, lo0.y, lo0.z, lo0.w, lo1.x, lo1.y, lo1.z, lo1.w};
+    const uint32_t hi[8] = {hi0.x, hi0.y, hi0.z, hi0.w, hi1.x, hi1.y, hi1.z, hi1.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const uint4 b = xs[j * 4 * G];
@@ -112,6 +119,7 @@ struct Shared {
     int warp_sum[kWarps];
     int slot[8];            // the group's slots
     uint32_t top[8];        // largest finite |x| of each, as BF16 bits
+    uint64_t full[kWarps * kMaxDepth];   // a ring place has its step
 };
 
 // Expert of a slot as the caller gave it, with ids outside [-1, E) as -2.
@@ -230,11 +238,11 @@ __device__ void find_slots(const MatvecArgs &a, Shared &sh, int e, int from, int
 __device__ __forceinline__ int x_shift(uint32_t top) { return top ? 14 - (max((int)(top >> 7), 1) - 127) : 0; }
 
 // x of the group's m slots -> f16 in shared memory: elements 8q .. 8q + 7 of
-// slot c at 16-byte place (((q / 32) * 8 + q % 8) * 4 + (q / 8) % 4) * G + c,
-// which is where lane (c, t) looks for word q % 8 of its 64 elements of step
-// q / 32.
+// slot c at 16-byte place (((q / 32) * 8 + q % 8) * G + c) * 4 + (q / 8) % 4,
+// which is where lane (c, t) looks for word q % 8 of its 64 elements of half
+// step q / 32 (eight neighbouring lanes: 128 neighbouring bytes).
 template <int G>
-__device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, uint4 *xs, int steps)
+__device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, uint4 *xs, int halves)
 {
     const int nq = a.K / 8;
     const uint4 *x[G];
@@ -274,7 +282,7 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, 
         const int shift = x_shift(sh.top[c]);
         const float2 f0 = make_float2(exp2i(shift / 2), exp2i(shift / 2));
         const float2 f1 = make_float2(exp2i(shift - shift / 2), exp2i(shift - shift / 2));
-        for (int q = threadIdx.x; q < steps * 32; q += kThreads) {
+        for (int q = threadIdx.x; q < halves * 32; q += kThreads) {
             uint4 o = make_uint4(0, 0, 0, 0);
             if (q < nq) {
                 const uint4 v = __ldg(x[c] + q);
@@ -287,118 +295,144 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, 
                 }
                 o = make_uint4(h[0], h[1], h[2], h[3]);
             }
-            xs[(((q >> 5) * 8 + (q & 7)) * 4 + ((q >> 3) & 3)) * G + c] = o;
+            xs[(((q >> 5) * 8 + (q & 7)) * G + c) * 4 + ((q >> 3) & 3)] = o;
         }
     }
 }
 
-// Persistent: the (group of slots, tile of rows) pairs are dealt to the CTAs
-// in contiguous ranges, so a CTA meets few groups; its warps take the tiles of
-// a group in turn, each with kDepth steps of loads in flight, the next tile's
-// first ones among them.  G: columns of x in shared memory (slots per group).
-// FULL: K is a whole number of steps.
-template <int G, bool FULL>
-__global__ void __launch_bounds__(kThreads, 1) matvec_kernel(MatvecArgs a)
+// Expert of a group of slots: the last one with first[e] <= group.
+__device__ __forceinline__ int expert_of_group(const Shared &sh, int E, int group)
 {
-    extern __shared__ uint4 xs[];
+    int e = 0, hi = E - 1;
+    while (e < hi) {
+        const int mid = (e + hi + 1) >> 1;
+        if (sh.first[mid] <= group)
+            e = mid;
+        else
+            hi = mid - 1;
+    }
+    return e;
+}
+
+// Persistent: the (group of slots, tile of rows) pairs are dealt to the CTAs
+// in contiguous ranges, so a CTA meets few groups; a CTA's warps take the
+// pairs of its range in turn.  The steps of a warp's pairs run through its ring
+// without a gap, also where the group changes.  G: columns of x in shared
+// memory (slots per group).
+template <int G>
+__global__ void __launch_bounds__(kThreads, 1)
+matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap scales_map,
+              MatvecArgs a, int depth)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Shared sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    uint64_t *full = sh.full + warp * depth;
+    if (lane == 0) {
+        for (int i = 0; i < depth; ++i)
+            mbar_init(full + i, 1);
+        fence_mbar_init();
+    }
     pdl_launch_dependents();
     pdl_wait();
-    const int groups = count_groups(a, sh, G);
+    const int groups = count_groups(a, sh, G);          // (its barriers publish the mbarriers too)
     const int tiles = (a.N + kTile - 1) / kTile;
-    const int steps = (a.K + kStep - 1) / kStep;
+    const int steps = (a.K + kStep - 1) / kStep, halves = (a.K + kHalf - 1) / kHalf;
     const int64_t total = (int64_t)groups * tiles;
     int64_t at = total * blockIdx.x / gridDim.x;
     const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, t = lane & 3;
 
+    uint8_t *codes = smem + (size_t)warp * depth * kCodeBytes;
+    uint8_t *scales = smem + (size_t)kWarps * depth * kCodeBytes + (size_t)warp * depth * kScaleBytes;
+    uint4 *xs = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * depth * (kCodeBytes + kScaleBytes));
+
+    // the step to load next: tile p_tile of group p_group, step p_step, into place p_at
+    int64_t p_item = at + warp;
+    int p_group = 0, p_tile = 0, p_row = 0, p_step = 0, p_at = 0;
+    auto locate = [&]() {
+        if (p_item >= end)
+            return;
+        p_group = (int)(p_item / tiles);
+        p_tile = (int)(p_item - (int64_t)p_group * tiles);
+        p_row = expert_of_group(sh, a.E, p_group) * a.N + p_tile * kTile;
+    };
+    int in_flight = 0;
+    auto load = [&]() {
+        if (p_item >= end)
+            return;
+        if (lane == 0) {
+            const bool two = 2 * p_step + 1 < halves;
+            uint8_t *to = codes + p_at * kCodeBytes;
+            mbar_arrive_expect_tx(full + p_at, (two ? kCodeBytes : kHalfBytes) + kScaleBytes);
+            tma_load_2d(to, &codes_map, p_step * (kStep / 2), p_row, full + p_at);
+            if (two)
+                tma_load_2d(to + kHalfBytes, &codes_map, p_step * (kStep / 2) + kHalf / 2, p_row, full + p_at);
+            tma_load_2d(scales + p_at * kScaleBytes, &scales_map, p_step * (kStep / 16), p_row, full + p_at);
+        }
+        ++in_flight;
+        if (++p_at == depth)
+            p_at = 0;
+        if (++p_step == steps) {
+            p_step = 0;
+            p_item += kWarps;
+            p_tile += kWarps;
+            p_row += kWarps * kTile;
+            if (p_tile >= tiles)
+                locate();
+        }
+    };
+    locate();
+    for (int i = 0; i < depth; ++i)
+        load();
+
+    int64_t item = at + warp;
+    int c_at = 0;
+    uint32_t parity = 0;
+    bool lost = false;                  // a wait gave up: no more loads, no more waits
     while (at < end) {
         const int group = (int)(at / tiles);
-        const int tile0 = (int)(at - (int64_t)group * tiles);
-        const int tile1 = (int)min((int64_t)tiles, end - (int64_t)group * tiles);
-        at += tile1 - tile0;
-        int e = 0, hi = a.E - 1;            // last expert with first[e] <= group
-        while (e < hi) {
-            const int mid = (e + hi + 1) >> 1;
-            if (sh.first[mid] <= group)
-                e = mid;
-            else
-                hi = mid - 1;
-        }
+        const int64_t stop = min(end, (int64_t)(group + 1) * tiles);
+        const int e = expert_of_group(sh, a.E, group);
         const int from = (group - sh.first[e]) * G;
         const int m = min(G, sh.count[e] - from);
-
-        const uint8_t *w = a.w + (int64_t)e * a.N * a.S;
-        const uint8_t *lo, *hi8;            // this lane's rows of the tile being loaded
-        Step st[kDepth];
-        auto rows_of = [&](int tile) {      // rows past N read the last one
-            lo = w + (int64_t)min(tile * kTile + g, a.N - 1) * a.S;
-            hi8 = w + (int64_t)min(tile * kTile + g + 8, a.N - 1) * a.S;
-        };
-        auto load = [&](Step &p, int step) {
-            const int k0 = step * kStep + t * 64;
-            if (FULL || k0 + 32 < a.K) {
-                p.lo0 = __ldg(reinterpret_cast<const uint4 *>(lo + k0 / 2));
-                p.lo1 = __ldg(reinterpret_cast<const uint4 *>(lo + k0 / 2 + 16));
-                p.hi0 = __ldg(reinterpret_cast<const uint4 *>(hi8 + k0 / 2));
-                p.hi1 = __ldg(reinterpret_cast<const uint4 *>(hi8 + k0 / 2 + 16));
-                p.slo = __ldg(reinterpret_cast<const uint32_t *>(lo + a.K / 2 + k0 / 16));
-                p.shi = __ldg(reinterpret_cast<const uint32_t *>(hi8 + a.K / 2 + k0 / 16));
-            } else {
-                p.lo0 = p.lo1 = p.hi0 = p.hi1 = make_uint4(0, 0, 0, 0);
-                p.slo = p.shi = 0;
-                if (k0 < a.K) {             // the row ends after 32 elements and two scales
-                    p.lo0 = __ldg(reinterpret_cast<const uint4 *>(lo + k0 / 2));
-                    p.hi0 = __ldg(reinterpret_cast<const uint4 *>(hi8 + k0 / 2));
-                    p.slo = __ldg(reinterpret_cast<const uint16_t *>(lo + a.K / 2 + k0 / 16));
-                    p.shi = __ldg(reinterpret_cast<const uint16_t *>(hi8 + a.K / 2 + k0 / 16));
-                }
-            }
-        };
-        int tile = tile0 + warp;
-        float scale_lo = 0.0f, scale_hi = 0.0f;
-        if (tile < tile1) {
-            rows_of(tile);
-#pragma unroll
-            for (int d = 0; d < kDepth; ++d)
-                if (d < steps)
-                    load(st[d], d);
-            scale_lo = __ldg(reinterpret_cast<const float *>(lo + a.S - 16));
-            scale_hi = __ldg(reinterpret_cast<const float *>(hi8 + a.S - 16));
-        }
-
+        const uint8_t *w = a.w + (int64_t)e * a.N * a.S + a.S - 16;     // the row scales
         find_slots(a, sh, e, from, G);
-        stage_x<G>(a, sh, m, xs, steps);
+        stage_x<G>(a, sh, m, xs, halves);
         __syncthreads();
 
-        const uint4 *x_lane = xs + t * G + g % G;
-        while (tile < tile1) {
-            const int next = tile + kWarps;
+        const uint4 *x_lane = xs + (g % G) * 4 + t;
+        for (; item < stop && !lost; item += kWarps) {
+            const int row = (int)(item - (int64_t)group * tiles) * kTile + g;
+            const float row_lo = __ldg(reinterpret_cast<const float *>(w + (int64_t)min(row, a.N - 1) * a.S));
+            const float row_hi = __ldg(reinterpret_cast<const float *>(w + (int64_t)min(row + 8, a.N - 1) * a.S));
             const uint4 *x = x_lane;
             float acc[4] = {};
-            for (int s0 = 0; s0 < steps; s0 += kDepth) {
-                const bool last = s0 + kDepth >= steps;
-                if (last && next < tile1)
-                    rows_of(next);
-#pragma unroll
-                for (int d = 0; d < kDepth; ++d) {
-                    if (s0 + d < steps)
-                        multiply<G>(acc, st[d], x + d * 32 * G);
-                    const int ahead = last ? d : s0 + kDepth + d;
-                    if ((!last || next < tile1) && ahead < steps)
-                        load(st[d], ahead);
+            for (int s = 0; s < steps; ++s) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(full + c_at, parity))) {
+                    lost = true;
+                    break;
                 }
-                x += kDepth * 32 * G;
+                --in_flight;
+                const uint8_t *c = codes + c_at * kCodeBytes + g * 128;
+                const uint8_t *c0 = c + (((2 * t) ^ g) << 4), *c1 = c + (((2 * t + 1) ^ g) << 4);
+                const uint8_t *sc = scales + c_at * kScaleBytes + g * (kStep / 16) + t * 4;
+                multiply<G>(acc, c0, c1, sc, x);
+                if (2 * s + 1 < halves)
+                    multiply<G>(acc, c0 + kHalfBytes, c1 + kHalfBytes, sc + kHalf / 16, x + 32 * G);
+                x += 64 * G;
+                if (++c_at == depth) {
+                    c_at = 0;
+                    parity ^= 1u;
+                }
+                __syncwarp();           // every lane has read the place that is loaded next
+                load();
             }
-            const float row_lo = scale_lo, row_hi = scale_hi;
-            if (next < tile1) {
-                scale_lo = __ldg(reinterpret_cast<const float *>(lo + a.S - 16));
-                scale_hi = __ldg(reinterpret_cast<const float *>(hi8 + a.S - 16));
-            }
+            if (lost)
+                break;
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const int c = 2 * t + (v & 1), n = tile * kTile + g + (v & 2 ? 8 : 0);
+                const int c = 2 * t + (v & 1), n = row + (v & 2 ? 8 : 0);
                 if (c < m && n < a.N) {
                     // in 64 bits: the two scales together may pass FP32's range
                     const double back = __hiloint2double((1023 - x_shift(sh.top[c])) << 20, 0);
@@ -406,25 +440,40 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(MatvecArgs a)
                     a.y[(int64_t)sh.slot[c] * a.N + n] = (uint16_t)cvt_bf16x2((float)r, 0.0f);
                 }
             }
-            tile = next;
         }
+        at = stop;
         __syncthreads();                    // before the next group's x and slots
+    }
+    if (lost && lane == 0) {
+        raise_status(a.status, kDevErrTimeout);
+        // never leave with a load in flight
+        for (; in_flight > 0; --in_flight) {
+            (void)mbar_wait_bounded(full + c_at, parity);
+            if (++c_at == depth) {
+                c_at = 0;
+                parity ^= 1u;
+            }
+        }
     }
     zero_rows(a, sh);
 }
 
-template <int G, bool FULL> cudaError_t launch_group(const LaunchCtx &c, const MatvecArgs &a, size_t smem)
+template <int G> cudaError_t launch_group(const LaunchCtx &c, const MatvecArgs &a, size_t x_bytes)
 {
     static std::atomic<uint32_t> done[2] = {};
-    cudaError_t e = ensure_smem_limit(matvec_kernel<G, FULL>, c.device, kMaxSmem, done);
+    cudaError_t e = ensure_smem_limit(matvec_kernel<G>, c.device, kMaxSmem, done);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(matvec_kernel<G, FULL>, dim3((unsigned)c.num_sms), dim3(kThreads), smem, c.stream, a);
-}
-
-template <int G> cudaError_t launch_steps(const LaunchCtx &c, const MatvecArgs &a, size_t x_bytes)
-{
-    return a.K % kStep == 0 ? launch_group<G, true>(c, a, G * x_bytes) : launch_group<G, false>(c, a, G * x_bytes);
+    const uint64_t rows = (uint64_t)a.E * a.N;
+    CUtensorMap codes, scales;
+    if (!make_map(&codes, a.w, (uint64_t)a.K / 2, rows, (uint64_t)a.S, kHalf / 2, kTile, true) ||
+        !make_map(&scales, a.w + a.K / 2, (uint64_t)a.K / 16, rows, (uint64_t)a.S, kStep / 16, kTile))
+        return cudaErrorInvalidValue;
+    const size_t ring = (size_t)kWarps * (kCodeBytes + kScaleBytes);
+    int depth = (int)((kMaxSmem - G * x_bytes) / ring);
+    depth = depth > kMaxDepth ? kMaxDepth : depth;
+    return launch_pdl(matvec_kernel<G>, dim3((unsigned)c.num_sms), dim3(kThreads), depth * ring + G * x_bytes,
+                      c.stream, codes, scales, a, depth);
 }
 
 } // namespace
@@ -435,15 +484,16 @@ cudaError_t launch_matvec(const LaunchCtx &c, const MatvecArgs &a)
         return cudaSuccess;
     // Slots of one expert that share a pass over its rows: as many as there are
     // tokens (a router names an expert once per token; if it is named more
-    // often, it gets more passes), at most 8, and as fit in shared memory.
-    const size_t x_bytes = (size_t)((a.K + kStep - 1) / kStep) * kStep * 2;
-    if (a.T == 1 || 2 * x_bytes > kMaxSmem)
-        return launch_steps<1>(c, a, x_bytes);
-    if (a.T == 2 || 4 * x_bytes > kMaxSmem)
-        return launch_steps<2>(c, a, x_bytes);
-    if (a.T <= 4 || 8 * x_bytes > kMaxSmem)
-        return launch_steps<4>(c, a, x_bytes);
-    return launch_steps<8>(c, a, x_bytes);
+    // often, it gets more passes), at most 8, and as leave the rings two steps.
+    const size_t x_bytes = (size_t)((a.K + kHalf - 1) / kHalf) * kHalf * 2;
+    const size_t room = kMaxSmem - (size_t)kMinDepth * kWarps * (kCodeBytes + kScaleBytes);
+    if (a.T == 1)
+        return launch_group<1>(c, a, x_bytes);
+    if (a.T == 2 || 4 * x_bytes > room)
+        return launch_group<2>(c, a, x_bytes);
+    if (a.T <= 4 || 8 * x_bytes > room)
+        return launch_group<4>(c, a, x_bytes);
+    return launch_group<8>(c, a, x_bytes);
 }
 
 } // namespace epq
