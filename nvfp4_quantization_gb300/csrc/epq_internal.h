@@ -182,11 +182,11 @@ struct MatvecArgs {
 cudaError_t launch_matvec(const LaunchCtx &c, const MatvecArgs &a);
 
 // Tensor map of a 2-D byte tensor [outer][inner] with a row pitch of `pitch`
-// bytes and a box of box_outer rows x box_inner bytes (L2 promotion 256 B; no
-// swizzle, or the 128-byte one: 16-byte chunk c of box row r lands at chunk
-// c ^ (r mod 8)); false if the driver refuses it.
+// bytes and a box of box_outer rows x box_inner bytes (no swizzle, L2
+// promotion 256 B); false if the driver refuses it.  elem = 2: inner and
+// box_inner count 16-bit units instead.
 bool make_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t pitch,
-              uint32_t box_inner, uint32_t box_outer, bool swizzle128 = false);
+              uint32_t box_inner, uint32_t box_outer, int elem = 1);
 
 // Bytes of a packed NVFP4 row: roundup16(9H/16 + 16).
 inline int64_t row_bytes(int64_t H) { return (9 * H / 16 + 16 + 15) / 16 * 16; }

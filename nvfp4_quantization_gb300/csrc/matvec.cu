@@ -21,13 +21,14 @@
 //    shifts and masks instead costs 4.3 instructions a pair and twice the time.)
 //  - the summation index is free to be permuted: lane (g, t) of a warp takes
 //    64 consecutive elements of rows g and g + 8, so no fragment shuffle is
-//    needed; x lies in shared memory in the order in which the lanes want it.
-//  - the rows come by TMA, 16 rows x 512 elements (256 bytes of codes, 32 of
-//    scales a row) at a time, into a ring of each warp's own.  Loaded straight
-//    to registers the same fragments cost the L1 eight lines a request and
-//    held the kernel at 40 % of HBM.
-// A row's sum is computed by one warp in one order, whatever else is in the
-// batch: a slot's result does not depend on the other slots.
+//    needed, and x is brought into the order in which the lanes want it.
+//  - the rows come by TMA, 16 rows x 512 elements at a time, into a ring of
+//    each warp's own: a warp waits for nobody but its own copies.
+// What bounds it: with the rows at HBM's rate the conversion and the matrix
+// instruction take about 60 % of the issue slots, so a step's bookkeeping has
+// to be small beside its 32 matrix instructions.
+// A row's sum is computed by one warp in an order that depends on K alone: a
+// slot's result does not depend on the other slots of the batch.
 #include "epq_device.cuh"
 #include "epq_internal.h"
 
@@ -39,15 +40,11 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;        // weight rows of a warp's tile
 constexpr int kHalf = 256;       // elements of a row that a warp multiplies at a time
-constexpr int kStep = 512;       // ... and loads at a time
-constexpr int kHalfBytes = kTile * kHalf / 2;     // codes of a half step
-constexpr int kCodeBytes = kTile * kStep / 2;     // of a step
-constexpr int kScaleBytes = kTile * kStep / 16;
-constexpr int kMinDepth = 2;     // steps in flight per warp
-constexpr int kMaxDepth = 3;
+constexpr int kMaxDepth = 6;     // steps in flight per warp, at most ...
+constexpr int kMinDepth = 2;     // ... and at least
 constexpr int kMaxE = 1024;
-constexpr int kIds = 2048;       // slots whose expert is kept in shared memory
-constexpr int kMaxSmem = 212 * 1024;   // dynamic: the warps' rings and x
+constexpr int kIds = 1024;       // slots whose expert is kept in shared memory
+constexpr int kMaxSmem = 220 * 1024;   // dynamic: the warps' rings and x
 
 // One word of eight E2M1 codes -> four f16 pairs (exact).
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4])
@@ -64,7 +61,7 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4])
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -78,48 +75,85 @@ __device__ __forceinline__ void scale_pair(uint32_t two, uint32_t &s0, uint32_t 
     s1 = __byte_perm(v, v, 0x3232);
 }
 
-// Half a step of 16 rows: this lane's 64 elements of rows g and g + 8 against
-// its column of x, whose words lie 4 * G places apart.  `c0`, `c1`: the places of
-// the lane's two 16-byte chunks of row g (row g + 8 is 1024 bytes on).
-template <int G>
-__device__ __forceinline__ void multiply(float (&acc)[4], const uint8_t *c0, const uint8_t *c1, const uint8_t *scales,
-                                         const uint4 *xs)
+// 256 elements of 16 rows: this lane's 64 elements of rows g and g + 8 against
+// its column of x.  `x(j)`: elements 8j .. 8j + 7 of the 64 as f16; `lo`, `hi`:
+// the rows' codes in the lane's order; `slo`, `shi`: their four block scales.
+// Two accumulators, whose sum is the result: one instruction need not wait for
+// the one before.
+template <typename X>
+__device__ __forceinline__ void multiply(float (&acc)[2][4], const uint4 (&lo)[2], const uint4 (&hi)[2], uint32_t slo,
+                                         uint32_t shi, X x)
 {
-    const uint32_t two_lo = *reinterpret_cast<const uint32_t *>(scales);
-    const uint32_t two_hi = *reinterpret_cast<const uint32_t *>(scales + 8 * (kStep / 16));
-    const uint4 lo0 = *reinterpret_cast<const uint4 *>(c0), lo1 = *reinterpret_cast<const uint4 *>(c1);
-    const uint4 hi0 = *reinterpret_cast<const uint4 *>(c0 + 1024), hi1 = *reinterpret_cast<const uint4 *>(c1 + 1024);
-    uint32_t slo[4], shi[4];
-    scale_pair(two_lo & 0xffffu, slo[0], slo[1]);
-    scale_pair(two_lo >> 16, slo[2], slo[3]);
-    scale_pair(two_hi & 0xffffu, shi[0], shi[1]);
-    scale_pair(two_hi >> 16, shi[2], shi[3]);
-    const uint32_t lo[8] = {lo0.x, lo0.y, lo0.z, lo0.w, lo1.x, lo1.y, lo1.z, lo1.w};
-    const uint32_t hi[8] = {hi0.x, hi0.y, hi0.z, hi0.w, hi1.x, hi1.y, hi1.z, hi1.w};
+    uint32_t s_lo[4], s_hi[4];
+    scale_pair(slo & 0xffffu, s_lo[0], s_lo[1]);
+    scale_pair(slo >> 16, s_lo[2], s_lo[3]);
+    scale_pair(shi & 0xffffu, s_hi[0], s_hi[1]);
+    scale_pair(shi >> 16, s_hi[2], s_hi[3]);
+    const uint32_t w_lo[8] = {lo[0].x, lo[0].y, lo[0].z, lo[0].w, lo[1].x, lo[1].y, lo[1].z, lo[1].w};
+    const uint32_t w_hi[8] = {hi[0].x, hi[0].y, hi[0].z, hi[0].w, hi[1].x, hi[1].y, hi[1].z, hi[1].w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint4 b = xs[j * 4 * G];
+        const uint4 b = x(j);
         uint32_t l[4], h[4];
-        codes_to_f16(lo[j], l);
-        codes_to_f16(hi[j], h);
+        codes_to_f16(w_lo[j], l);
+        codes_to_f16(w_hi[j], h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            l[i] = hmul2_rn(l[i], slo[j >> 1]);
-            h[i] = hmul2_rn(h[i], shi[j >> 1]);
+            l[i] = hmul2_rn(l[i], s_lo[j >> 1]);
+            h[i] = hmul2_rn(h[i], s_hi[j >> 1]);
         }
-        mma16816(acc, l[0], h[0], l[1], h[1], b.x, b.y);
-        mma16816(acc, l[2], h[2], l[3], h[3], b.z, b.w);
+        mma16816(acc[0], l[0], h[0], l[1], h[1], b.x, b.y);
+        mma16816(acc[1], l[2], h[2], l[3], h[3], b.z, b.w);
     }
 }
 
+// A warp's place of the ring: kTile rows of HALVES halves of codes, whose pitch
+// of 16 bytes more than they need (the next step's first ones) keeps the lanes
+// of a warp off each other's banks; then their scales.
+template <int HALVES> struct Place {
+    static constexpr int code_pitch = HALVES * kHalf / 2 + 16;
+    static constexpr int scale_pitch = HALVES * kHalf / 16;
+    static constexpr int codes = kTile * code_pitch;
+    static constexpr int bytes = codes + kTile * scale_pitch;
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"((uint64_t)m), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+// Bounded wait of a whole warp on its barrier (as mbar_wait_bounded, the first
+// attempt in line).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        return true;
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+
 struct Shared {
-    int first[kMaxE + 1];   // groups of slots before expert e
-    int count[kMaxE];       // slots of expert e
+    int first[kMaxE + 1];   // groups of slots before expert e (slots of expert e while counting)
     int16_t ids[kIds];      // expert of a slot (-1: none), batches up to kIds slots
     int warp_sum[kWarps];
     int slot[8];            // the group's slots
     uint32_t top[8];        // largest finite |x| of each, as BF16 bits
-    uint64_t full[kWarps * kMaxDepth];   // a ring place has its step
+    uint64_t full[kWarps * kMaxDepth];   // a place of a ring has its rows
 };
 
 // Expert of a slot as the caller gave it, with ids outside [-1, E) as -2.
@@ -164,14 +198,14 @@ __device__ int count_groups(const MatvecArgs &a, Shared &sh, int per_group)
 {
     const int slots = a.T * a.k;
     for (int e = threadIdx.x; e < a.E; e += kThreads)
-        sh.count[e] = 0;
+        sh.first[e] = 0;
     __syncthreads();
     for (int s = threadIdx.x; s < slots; s += kThreads) {
         const int e = read_id(a, s);
         if (slots <= kIds)
             sh.ids[s] = (int16_t)e;
         if (e >= 0)
-            atomicAdd(&sh.count[e], 1);
+            atomicAdd(&sh.first[e], 1);
         else if (e == -2 && blockIdx.x == 0)
             raise_status(a.status, kDevErrBadExpert);
     }
@@ -181,7 +215,7 @@ __device__ int count_groups(const MatvecArgs &a, Shared &sh, int per_group)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x * kPer + i;
-        g[i] = e < a.E ? (sh.count[e] + per_group - 1) / per_group : 0;
+        g[i] = e < a.E ? (sh.first[e] + per_group - 1) / per_group : 0;
         mine += g[i];
     }
     int at = cta_prefix(mine, sh.warp_sum, &total);
@@ -198,18 +232,66 @@ __device__ int count_groups(const MatvecArgs &a, Shared &sh, int per_group)
     return total;
 }
 
+// Batches of up to 32 slots: every warp works the groups out for itself, one
+// slot a lane, without a barrier (a kernel's first copies start a microsecond
+// sooner).
+struct SmallBatch {
+    int id;            // the lane's expert; negative: none
+    int rank;          // of the slot among its expert's
+    uint32_t leaders;  // lanes that begin a group
+
+    __device__ __forceinline__ void read(const MatvecArgs &a, int per_group)
+    {
+        const int lane = threadIdx.x & 31, slots = a.T * a.k;
+        id = lane < slots ? read_id(a, lane) : -1;
+        if (id == -2 && blockIdx.x == 0 && threadIdx.x < 32)
+            raise_status(a.status, kDevErrBadExpert);
+        const uint32_t same = __match_any_sync(0xffffffffu, id);
+        rank = __popc(same & ((1u << lane) - 1));
+        leaders = __ballot_sync(0xffffffffu, id >= 0 && rank % per_group == 0);
+    }
+    __device__ __forceinline__ int groups() const { return __popc(leaders); }
+    __device__ __forceinline__ int leader(int group) const
+    {
+        const int lane = threadIdx.x & 31;
+        const bool it = (leaders >> lane & 1u) && __popc(leaders & ((1u << lane) - 1)) == group;
+        return __ffs(__ballot_sync(0xffffffffu, it)) - 1;
+    }
+    __device__ __forceinline__ int expert(int group) const { return __shfl_sync(0xffffffffu, id, leader(group)); }
+    // the group's slots to shared memory (the caller's barrier publishes them)
+    __device__ __forceinline__ int find(Shared &sh, int group, int per_group) const
+    {
+        const int lane = threadIdx.x & 31, l = leader(group);
+        const int e = __shfl_sync(0xffffffffu, id, l), c = rank - __shfl_sync(0xffffffffu, rank, l);
+        const bool hit = id == e && c >= 0 && c < per_group;
+        if (threadIdx.x < 32) {
+            if (hit)
+                sh.slot[c] = lane;
+            if (lane < 8)
+                sh.top[lane] = 0;
+        }
+        return __popc(__ballot_sync(0xffffffffu, hit));
+    }
+};
+
+__device__ __forceinline__ int64_t quotient(int64_t a, int b)
+{
+    return a < (int64_t)UINT32_MAX ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Zero rows for the slots without an expert.
 __device__ void zero_rows(const MatvecArgs &a, const Shared &sh)
 {
     const int slots = a.T * a.k;
     for (int s = blockIdx.x; s < slots; s += gridDim.x)
-        if (slot_expert(a, sh, s) < 0)
+        if ((slots <= 32 ? read_id(a, s) : slot_expert(a, sh, s)) < 0)
             for (int n = threadIdx.x; n < a.N; n += kThreads)
                 a.y[(int64_t)s * a.N + n] = 0;
 }
 
-// The slots of expert e with rank [from, from + per_group), in slot order.
-__device__ void find_slots(const MatvecArgs &a, Shared &sh, int e, int from, int per_group)
+// The slots of expert e with rank [from, from + per_group), in slot order;
+// returns how many there are.
+__device__ int find_slots(const MatvecArgs &a, Shared &sh, int e, int from, int per_group)
 {
     const int slots = a.T * a.k, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int share = (slots + kThreads - 1) / kThreads * 32;   // slots of a warp, whole 32s
@@ -231,72 +313,74 @@ __device__ void find_slots(const MatvecArgs &a, Shared &sh, int e, int from, int
     if (threadIdx.x < 8)
         sh.top[threadIdx.x] = 0;
     __syncthreads();
+    return min(per_group, total - from);
 }
 
 // The power of two that a slot's x is multiplied by: its largest element comes
 // to [2^14, 2^15).  A subnormal largest counts as 2^-126.
 __device__ __forceinline__ int x_shift(uint32_t top) { return top ? 14 - (max((int)(top >> 7), 1) - 127) : 0; }
 
-// x of the group's m slots -> f16 in shared memory: elements 8q .. 8q + 7 of
-// slot c at 16-byte place (((q / 32) * 8 + q % 8) * G + c) * 4 + (q / 8) % 4,
-// which is where lane (c, t) looks for word q % 8 of its 64 elements of half
-// step q / 32 (eight neighbouring lanes: 128 neighbouring bytes).
-template <int G>
-__device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, uint4 *xs, int halves)
+__device__ __forceinline__ uint32_t finite_absmax(uint32_t top, uint4 v)
 {
-    const int nq = a.K / 8;
-    const uint4 *x[G];
-    uint32_t top[G];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int c = 0; c < G; ++c) {
-        const int s = sh.slot[c < m ? c : 0];
-        x[c] = reinterpret_cast<const uint4 *>(a.x + (int64_t)(a.per_slot ? s : s / a.k) * a.ld_x);
-        top[c] = 0;
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t l = w[i] & 0x7fffu, h = (w[i] >> 16) & 0x7fffu;
+        top = max(top, max(l < 0x7f80u ? l : 0u, h < 0x7f80u ? h : 0u));
     }
-    for (int q = threadIdx.x; q < nq; q += kThreads) {
+    return top;
+}
+
+// 8 BF16 values times 2^shift, as f16.  The power comes in two factors: it
+// reaches 2^140.
+__device__ __forceinline__ uint4 to_f16(uint4 v, int shift)
+{
+    const float2 f0 = make_float2(exp2i(shift / 2), exp2i(shift / 2));
+    const float2 f1 = make_float2(exp2i(shift - shift / 2), exp2i(shift - shift / 2));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
 #pragma unroll
-        for (int c = 0; c < G; ++c) {
-            if (c >= m)
-                break;
-            const uint4 v = __ldg(x[c] + q);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t l = w[i] & 0x7fffu, h = (w[i] >> 16) & 0x7fffu;
-                top[c] = max(top[c], max(l < 0x7f80u ? l : 0u, h < 0x7f80u ? h : 0u));
-            }
-        }
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = mul2(mul2(make_float2(u2f(w[i] << 16), u2f(w[i] & 0xffff0000u)), f0), f1);
+        h[i] = cvt_f16x2(p.x, p.y);
     }
-#pragma unroll
-    for (int c = 0; c < G; ++c) {
-        const uint32_t w = __reduce_max_sync(0xffffffffu, top[c]);
-        if (c < m && (threadIdx.x & 31) == 0 && w)
-            atomicMax(&sh.top[c], w);
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+__device__ __forceinline__ const uint16_t *x_row(const MatvecArgs &a, int s)
+{
+    return a.x + (int64_t)(a.per_slot ? s : s / a.k) * a.ld_x;
+}
+
+// v * scale * 2^-shift, rounded once to FP32 in its normal range: the two
+// scales together may pass that range where the result does not, so the
+// exponents are added as integers and applied in two factors.  (In 64-bit
+// arithmetic this costs the kernel a third of its time.)
+__device__ __forceinline__ float rescale(float v, float scale, int shift)
+{
+    const uint32_t b = f2u(scale);
+    int e = (int)((b >> 23) & 0xffu);
+    float m = scale;
+    if (e == 0 || e == 255)
+        e = 0;                          // zero, subnormal, infinity, NaN: as it is
+    else {
+        m = u2f((b & 0x807fffffu) | 0x3f800000u);
+        e -= 127;
     }
-    __syncthreads();
+    e = max(-250, min(250, e - shift));     // beyond these the result is 0 or infinite anyway
+    return v * m * exp2i(e / 2) * exp2i(e - e / 2);
+}
+
+// The finished sums of a lane (rows `row` and row + 8, slots 2t and 2t + 1).
+__device__ __forceinline__ void write_sums(const MatvecArgs &a, const Shared &sh, const float (&acc)[4], int m, int row,
+                                           int t, float scale_lo, float scale_hi)
+{
 #pragma unroll
-    for (int c = 0; c < G; ++c) {
-        if (c >= m)
-            break;
-        // in two factors: the shift reaches 140
-        const int shift = x_shift(sh.top[c]);
-        const float2 f0 = make_float2(exp2i(shift / 2), exp2i(shift / 2));
-        const float2 f1 = make_float2(exp2i(shift - shift / 2), exp2i(shift - shift / 2));
-        for (int q = threadIdx.x; q < halves * 32; q += kThreads) {
-            uint4 o = make_uint4(0, 0, 0, 0);
-            if (q < nq) {
-                const uint4 v = __ldg(x[c] + q);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                uint32_t h[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 p = mul2(mul2(make_float2(u2f(w[i] << 16), u2f(w[i] & 0xffff0000u)), f0), f1);
-                    h[i] = cvt_f16x2(p.x, p.y);
-                }
-                o = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-            xs[(((q >> 5) * 8 + (q & 7)) * G + c) * 4 + ((q >> 3) & 3)] = o;
-        }
+    for (int v = 0; v < 4; ++v) {
+        const int c = 2 * t + (v & 1), n = row + (v & 2 ? 8 : 0);
+        if (c < m && n < a.N)
+            a.y[(int64_t)sh.slot[c] * a.N + n] =
+                (uint16_t)cvt_bf16x2(rescale(acc[v], v & 2 ? scale_hi : scale_lo, x_shift(sh.top[c])), 0.0f);
     }
 }
 
@@ -314,21 +398,66 @@ __device__ __forceinline__ int expert_of_group(const Shared &sh, int E, int grou
     return e;
 }
 
+// x of the group's m slots -> f16 in shared memory: elements 8q .. 8q + 7 of
+// slot c at 16-byte place (((q / 32) * 8 + q % 8) * G + c) * 4 + (q / 8) % 4,
+// which is where lane (c, t) looks for word q % 8 of its 64 elements of half
+// step q / 32 (eight neighbouring lanes: 128 neighbouring bytes).
+template <int G>
+__device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, uint4 *xs, int halves)
+{
+    const int nq = a.K / 8;
+    const uint4 *x[G];
+    uint32_t top[G];
+#pragma unroll
+    for (int c = 0; c < G; ++c) {
+        x[c] = reinterpret_cast<const uint4 *>(x_row(a, sh.slot[c < m ? c : 0]));
+        top[c] = 0;
+    }
+    const bool once = nq <= kThreads;   // a thread has eight elements of a slot, and keeps them
+    uint4 kept[G];
+    for (int q = threadIdx.x; q < nq; q += kThreads) {
+#pragma unroll
+        for (int c = 0; c < G; ++c) {
+            if (c < m) {
+                kept[c] = __ldg(x[c] + q);
+                top[c] = finite_absmax(top[c], kept[c]);
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < G; ++c) {
+        const uint32_t w = __reduce_max_sync(0xffffffffu, top[c]);
+        if (c < m && (threadIdx.x & 31) == 0 && w)
+            atomicMax(&sh.top[c], w);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < G; ++c) {
+        if (c >= m)
+            break;
+        const int shift = x_shift(sh.top[c]);
+        for (int q = threadIdx.x; q < halves * 32; q += kThreads)
+            xs[(((q >> 5) * 8 + (q & 7)) * G + c) * 4 + ((q >> 3) & 3)] =
+                q < nq ? to_f16(once ? kept[c] : __ldg(x[c] + q), shift) : make_uint4(0, 0, 0, 0);
+    }
+}
+
 // Persistent: the (group of slots, tile of rows) pairs are dealt to the CTAs
 // in contiguous ranges, so a CTA meets few groups; a CTA's warps take the
 // pairs of its range in turn.  The steps of a warp's pairs run through its ring
 // without a gap, also where the group changes.  G: columns of x in shared
-// memory (slots per group).
-template <int G>
+// memory (slots per group); HALVES: of a step.
+template <int G, int HALVES>
 __global__ void __launch_bounds__(kThreads, 1)
 matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap scales_map,
               MatvecArgs a, int depth)
 {
-    extern __shared__ __align__(1024) uint8_t smem[];
+    using P = Place<HALVES>;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    uint64_t *full = sh.full + warp * depth;
+    uint64_t *full = sh.full + warp * kMaxDepth;
     if (lane == 0) {
         for (int i = 0; i < depth; ++i)
             mbar_init(full + i, 1);
@@ -336,43 +465,48 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
     }
     pdl_launch_dependents();
     pdl_wait();
-    const int groups = count_groups(a, sh, G);          // (its barriers publish the mbarriers too)
+    const bool small = a.T * a.k <= 32;
+    SmallBatch batch;
+    int groups;
+    if (small) {
+        batch.read(a, G);
+        groups = batch.groups();
+        __syncwarp();                   // the warp's mbarriers are its own
+    } else {
+        groups = count_groups(a, sh, G);
+    }
+    auto expert = [&](int group) { return small ? batch.expert(group) : expert_of_group(sh, a.E, group); };
     const int tiles = (a.N + kTile - 1) / kTile;
-    const int steps = (a.K + kStep - 1) / kStep, halves = (a.K + kHalf - 1) / kHalf;
+    const int halves = (a.K + kHalf - 1) / kHalf;
+    const int steps = (halves + HALVES - 1) / HALVES;
     const int64_t total = (int64_t)groups * tiles;
-    int64_t at = total * blockIdx.x / gridDim.x;
-    const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
+    int64_t at = quotient(total * blockIdx.x, gridDim.x);
+    const int64_t end = quotient(total * (blockIdx.x + 1), gridDim.x);
 
-    uint8_t *codes = smem + (size_t)warp * depth * kCodeBytes;
-    uint8_t *scales = smem + (size_t)kWarps * depth * kCodeBytes + (size_t)warp * depth * kScaleBytes;
-    uint4 *xs = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * depth * (kCodeBytes + kScaleBytes));
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * depth * P::bytes);
+    uint4 *xs = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * depth * P::bytes);
 
-    // the step to load next: tile p_tile of group p_group, step p_step, into place p_at
+    // the step to load next: step p_step of the tile at row p_row, into place p_at
     int64_t p_item = at + warp;
-    int p_group = 0, p_tile = 0, p_row = 0, p_step = 0, p_at = 0;
+    int p_tile = 0, p_row = 0, p_step = 0, p_at = 0, in_flight = 0;
     auto locate = [&]() {
         if (p_item >= end)
             return;
-        p_group = (int)(p_item / tiles);
-        p_tile = (int)(p_item - (int64_t)p_group * tiles);
-        p_row = expert_of_group(sh, a.E, p_group) * a.N + p_tile * kTile;
+        const int group = (int)quotient(p_item, tiles);
+        p_tile = (int)(p_item - (int64_t)group * tiles);
+        p_row = expert(group) * a.N + p_tile * kTile;
     };
-    int in_flight = 0;
     auto load = [&]() {
         if (p_item >= end)
             return;
         if (lane == 0) {
-            const bool two = 2 * p_step + 1 < halves;
-            uint8_t *to = codes + p_at * kCodeBytes;
-            mbar_arrive_expect_tx(full + p_at, (two ? kCodeBytes : kHalfBytes) + kScaleBytes);
-            tma_load_2d(to, &codes_map, p_step * (kStep / 2), p_row, full + p_at);
-            if (two)
-                tma_load_2d(to + kHalfBytes, &codes_map, p_step * (kStep / 2) + kHalf / 2, p_row, full + p_at);
-            tma_load_2d(scales + p_at * kScaleBytes, &scales_map, p_step * (kStep / 16), p_row, full + p_at);
+            const uint32_t to = ring + (uint32_t)(p_at * P::bytes);
+            mbar_arrive_expect_tx(full + p_at, P::bytes);
+            tma_load_2d_at(to, &codes_map, p_step * (HALVES * kHalf / 4), p_row, smem_u32(full + p_at));
+            tma_load_2d_at(to + P::codes, &scales_map, p_step * (HALVES * kHalf / 16), p_row, smem_u32(full + p_at));
         }
         ++in_flight;
-        if (++p_at == depth)
-            p_at = 0;
+        p_at = p_at + 1 == depth ? 0 : p_at + 1;
         if (++p_step == steps) {
             p_step = 0;
             p_item += kWarps;
@@ -390,37 +524,48 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
     int c_at = 0;
     uint32_t parity = 0;
     bool lost = false;                  // a wait gave up: no more loads, no more waits
+    const uint32_t c_lane = ring + (uint32_t)(g * P::code_pitch + t * 32);
+    const uint32_t s_lane = ring + (uint32_t)(P::codes + g * P::scale_pitch + t * 4);
+    const uint32_t x_lane = smem_u32(xs) + (uint32_t)(((g % G) * 4 + t) * 16);
     while (at < end) {
-        const int group = (int)(at / tiles);
+        const int group = (int)quotient(at, tiles);
         const int64_t stop = min(end, (int64_t)(group + 1) * tiles);
-        const int e = expert_of_group(sh, a.E, group);
-        const int from = (group - sh.first[e]) * G;
-        const int m = min(G, sh.count[e] - from);
+        const int e = expert(group);
         const uint8_t *w = a.w + (int64_t)e * a.N * a.S + a.S - 16;     // the row scales
-        find_slots(a, sh, e, from, G);
+        int m;
+        if (small) {
+            m = batch.find(sh, group, G);
+            __syncthreads();
+        } else {
+            m = find_slots(a, sh, e, (group - sh.first[e]) * G, G);
+        }
         stage_x<G>(a, sh, m, xs, halves);
         __syncthreads();
 
-        const uint4 *x_lane = xs + (g % G) * 4 + t;
         for (; item < stop && !lost; item += kWarps) {
             const int row = (int)(item - (int64_t)group * tiles) * kTile + g;
             const float row_lo = __ldg(reinterpret_cast<const float *>(w + (int64_t)min(row, a.N - 1) * a.S));
             const float row_hi = __ldg(reinterpret_cast<const float *>(w + (int64_t)min(row + 8, a.N - 1) * a.S));
-            const uint4 *x = x_lane;
-            float acc[4] = {};
-            for (int s = 0; s < steps; ++s) {
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(full + c_at, parity))) {
+            uint32_t x = x_lane;
+            float acc[2][4] = {};
+            for (int left = halves; left > 0; left -= HALVES) {
+                if (!warp_wait(full + c_at, parity)) {
                     lost = true;
                     break;
                 }
                 --in_flight;
-                const uint8_t *c = codes + c_at * kCodeBytes + g * 128;
-                const uint8_t *c0 = c + (((2 * t) ^ g) << 4), *c1 = c + (((2 * t + 1) ^ g) << 4);
-                const uint8_t *sc = scales + c_at * kScaleBytes + g * (kStep / 16) + t * 4;
-                multiply<G>(acc, c0, c1, sc, x);
-                if (2 * s + 1 < halves)
-                    multiply<G>(acc, c0 + kHalfBytes, c1 + kHalfBytes, sc + kHalf / 16, x + 32 * G);
-                x += 64 * G;
+                const uint32_t c = c_lane + (uint32_t)(c_at * P::bytes), s = s_lane + (uint32_t)(c_at * P::bytes);
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    if (h < left) {
+                        const uint32_t ch = c + h * (kHalf / 2), sh8 = s + h * (kHalf / 16);
+                        const uint4 wl[2] = {lds128(ch), lds128(ch + 16)};
+                        const uint4 wh[2] = {lds128(ch + 8 * P::code_pitch), lds128(ch + 8 * P::code_pitch + 16)};
+                        multiply(acc, wl, wh, lds32(sh8), lds32(sh8 + 8 * P::scale_pitch),
+                                 [&](int j) { return lds128(x + (h * 32 * G + j * 4 * G) * 16); });
+                    }
+                }
+                x += HALVES * 32 * G * 16;
                 if (++c_at == depth) {
                     c_at = 0;
                     parity ^= 1u;
@@ -430,19 +575,12 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
             }
             if (lost)
                 break;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int c = 2 * t + (v & 1), n = row + (v & 2 ? 8 : 0);
-                if (c < m && n < a.N) {
-                    // in 64 bits: the two scales together may pass FP32's range
-                    const double back = __hiloint2double((1023 - x_shift(sh.top[c])) << 20, 0);
-                    const double r = (double)acc[v] * (v & 2 ? row_hi : row_lo) * back;
-                    a.y[(int64_t)sh.slot[c] * a.N + n] = (uint16_t)cvt_bf16x2((float)r, 0.0f);
-                }
-            }
+            const float sum[4] = {acc[0][0] + acc[1][0], acc[0][1] + acc[1][1], acc[0][2] + acc[1][2],
+                                  acc[0][3] + acc[1][3]};
+            write_sums(a, sh, sum, m, row, t, row_lo, row_hi);
         }
         at = stop;
-        __syncthreads();                    // before the next group's x and slots
+        __syncthreads();                // before the next group's x and slots
     }
     if (lost && lane == 0) {
         raise_status(a.status, kDevErrTimeout);
@@ -458,22 +596,36 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
     zero_rows(a, sh);
 }
 
-template <int G> cudaError_t launch_group(const LaunchCtx &c, const MatvecArgs &a, size_t x_bytes)
+// Depth of the rings that x of G slots leaves room for.
+template <int HALVES> int ring_depth(size_t x_bytes)
 {
+    const size_t ring = (size_t)kWarps * Place<HALVES>::bytes;
+    const int d = x_bytes < kMaxSmem ? (int)((kMaxSmem - x_bytes) / ring) : 0;
+    return d > kMaxDepth ? kMaxDepth : d;
+}
+
+template <int G, int HALVES> cudaError_t launch_ring(const LaunchCtx &c, const MatvecArgs &a, size_t x_bytes)
+{
+    using P = Place<HALVES>;
     static std::atomic<uint32_t> done[2] = {};
-    cudaError_t e = ensure_smem_limit(matvec_kernel<G>, c.device, kMaxSmem, done);
+    cudaError_t e = ensure_smem_limit(matvec_kernel<G, HALVES>, c.device, kMaxSmem, done);
     if (e != cudaSuccess)
         return e;
     const uint64_t rows = (uint64_t)a.E * a.N;
+    const int depth = ring_depth<HALVES>(x_bytes);
     CUtensorMap codes, scales;
-    if (!make_map(&codes, a.w, (uint64_t)a.K / 2, rows, (uint64_t)a.S, kHalf / 2, kTile, true) ||
-        !make_map(&scales, a.w + a.K / 2, (uint64_t)a.K / 16, rows, (uint64_t)a.S, kStep / 16, kTile))
+    // codes in 16-bit units: a box has at most 256 of them along a side
+    if (!make_map(&codes, a.w, (uint64_t)a.K / 4, rows, (uint64_t)a.S, P::code_pitch / 2, kTile, 2) ||
+        !make_map(&scales, a.w + a.K / 2, (uint64_t)a.K / 16, rows, (uint64_t)a.S, P::scale_pitch, kTile))
         return cudaErrorInvalidValue;
-    const size_t ring = (size_t)kWarps * (kCodeBytes + kScaleBytes);
-    int depth = (int)((kMaxSmem - G * x_bytes) / ring);
-    depth = depth > kMaxDepth ? kMaxDepth : depth;
-    return launch_pdl(matvec_kernel<G>, dim3((unsigned)c.num_sms), dim3(kThreads), depth * ring + G * x_bytes,
-                      c.stream, codes, scales, a, depth);
+    return launch_pdl(matvec_kernel<G, HALVES>, dim3((unsigned)c.num_sms), dim3(kThreads),
+                      (size_t)kWarps * depth * P::bytes + x_bytes, c.stream, codes, scales, a, depth);
+}
+
+template <int G> cudaError_t launch_group(const LaunchCtx &c, const MatvecArgs &a, size_t x_bytes)
+{
+    return ring_depth<2>(G * x_bytes) >= kMinDepth ? launch_ring<G, 2>(c, a, G * x_bytes)
+                                                   : launch_ring<G, 1>(c, a, G * x_bytes);
 }
 
 } // namespace
@@ -484,14 +636,14 @@ cudaError_t launch_matvec(const LaunchCtx &c, const MatvecArgs &a)
         return cudaSuccess;
     // Slots of one expert that share a pass over its rows: as many as there are
     // tokens (a router names an expert once per token; if it is named more
-    // often, it gets more passes), at most 8, and as leave the rings two steps.
+    // often, it gets more passes), at most 8, and as leave the rings two of the
+    // smaller steps.
     const size_t x_bytes = (size_t)((a.K + kHalf - 1) / kHalf) * kHalf * 2;
-    const size_t room = kMaxSmem - (size_t)kMinDepth * kWarps * (kCodeBytes + kScaleBytes);
     if (a.T == 1)
         return launch_group<1>(c, a, x_bytes);
-    if (a.T == 2 || 4 * x_bytes > room)
+    if (a.T == 2 || ring_depth<1>(4 * x_bytes) < kMinDepth)
         return launch_group<2>(c, a, x_bytes);
-    if (a.T <= 4 || 8 * x_bytes > room)
+    if (a.T <= 4 || ring_depth<1>(8 * x_bytes) < kMinDepth)
         return launch_group<4>(c, a, x_bytes);
     return launch_group<8>(c, a, x_bytes);
 }

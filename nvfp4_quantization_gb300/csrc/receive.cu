@@ -887,7 +887,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 
 // 2-D byte tensor [outer][inner] with a row pitch of `pitch` bytes.
 bool make_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t pitch,
-                     uint32_t box_inner, uint32_t box_outer, bool swizzle128)
+                     uint32_t box_inner, uint32_t box_outer, int elem)
 {
     auto enc = tensor_map_encoder();
     if (!enc)
@@ -896,9 +896,8 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, 
     cuuint64_t strides[1] = {pitch};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

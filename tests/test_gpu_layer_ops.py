@@ -441,7 +441,7 @@ MV = [  # T, k, E, N, K, dropped share, one x row per slot, extra row pitch
     (7, 3, 5, 50, 96, 0.3, True, None), (32, 8, 16, 130, 512, 0, True, 8), (3, 4, 4, 64, 7168, 0.2, False, 16),
     (70, 2, 3, 33, 160, 0.1, False, None), (130, 1, 2, 40, 2080, 0, False, None), (0, 2, 4, 16, 64, 0, False, None),
     (300, 8, 40, 17, 64, 0.5, True, None), (16, 32, 1024, 8, 32, 0, False, None), (2, 8, 8, 4099, 352, 0, False, None),
-    (9, 1, 2, 20, 19968, 0.1, True, None), (3, 2, 3, 21, 32768, 0.2, False, None)]
+    (9, 1, 2, 20, 19968, 0.1, True, None), (12, 2, 4, 70, 8192, 0, False, None), (5, 2, 4, 33, 8224, 0, True, 8), (3, 2, 3, 21, 32768, 0.2, False, None)]
 
 
 @pytest.mark.parametrize("T,k,E,N,K,drop,per_slot,extra", MV)
