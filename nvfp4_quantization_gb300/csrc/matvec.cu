@@ -27,8 +27,12 @@
 // What bounds it: with the rows at HBM's rate the conversion and the matrix
 // instruction take about 60 % of the issue slots, so a step's bookkeeping has
 // to be small beside its 32 matrix instructions.
-// A row's sum is computed by one warp in an order that depends on K alone: a
-// slot's result does not depend on the other slots of the batch.
+//  - up to four warps share a tile, each taking every fourth step of its rows;
+//    one of them adds the partial sums up.  A tile of one warp's own would take
+//    it a sixth of a large call's time, and that is what the warps would wait
+//    for each other where the group of slots (and so x) changes.
+// The order of a row's sum depends on K alone: a slot's result does not depend
+// on the other slots of the batch.
 #include "epq_device.cuh"
 #include "epq_internal.h"
 
@@ -43,8 +47,8 @@ constexpr int kHalf = 256;       // elements of a row that a warp multiplies at 
 constexpr int kMaxDepth = 6;     // steps in flight per warp, at most ...
 constexpr int kMinDepth = 2;     // ... and at least
 constexpr int kMaxE = 1024;
-constexpr int kIds = 1024;       // slots whose expert is kept in shared memory
-constexpr int kMaxSmem = 220 * 1024;   // dynamic: the warps' rings and x
+constexpr int kIds = 512;        // slots whose expert is kept in shared memory
+constexpr int kMaxParts = 4;     // warps that share a tile, at most
 
 // One word of eight E2M1 codes -> four f16 pairs (exact).
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4])
@@ -67,12 +71,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Block scales 2i and 2i + 1 of a word of four, each in both halves.
+// Block scales 2i and 2i + 1 of a word of four, each in both halves (moves
+// that the multiplication's operands absorb).
 __device__ __forceinline__ void scale_pair(uint32_t two, uint32_t &s0, uint32_t &s1)
 {
     const uint32_t v = cvt_f16x2_from_e4m3x2(two);
-    s0 = __byte_perm(v, v, 0x1010);
-    s1 = __byte_perm(v, v, 0x3232);
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b32 %0, {lo, lo};\n\tmov.b32 %1, {hi, hi};\n\t}"
+        : "=r"(s0), "=r"(s1) : "r"(v));
 }
 
 // 256 elements of 16 rows: this lane's 64 elements of rows g and g + 8 against
@@ -148,13 +153,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
 }
 
 struct Shared {
-    int first[kMaxE + 1];   // groups of slots before expert e (slots of expert e while counting)
     int16_t ids[kIds];      // expert of a slot (-1: none), batches up to kIds slots
     int warp_sum[kWarps];
     int slot[8];            // the group's slots
     uint32_t top[8];        // largest finite |x| of each, as BF16 bits
     uint64_t full[kWarps * kMaxDepth];   // a place of a ring has its rows
+    float4 partial[kWarps][32];          // partial sums of a tile, lane by lane
 };
+
+// Dynamic shared memory: the warps' rings, x of a group, and int[E + 1]
+// `first`, the groups of slots before each expert.
+constexpr int kMaxSmem = 227 * 1024 - (int)sizeof(Shared);
+
 
 // Expert of a slot as the caller gave it, with ids outside [-1, E) as -2.
 __device__ __forceinline__ int read_id(const MatvecArgs &a, int s)
@@ -193,19 +203,20 @@ __device__ __forceinline__ int cta_prefix(int v, int *warp_sum, int *total)
     return before + x - v;
 }
 
-// Number of groups of each expert, as a prefix over the experts.
-__device__ int count_groups(const MatvecArgs &a, Shared &sh, int per_group)
+// Number of groups of each expert, as a prefix over the experts (`first` holds
+// the slots of each while they are counted).
+__device__ int count_groups(const MatvecArgs &a, Shared &sh, int *first, int per_group)
 {
     const int slots = a.T * a.k;
     for (int e = threadIdx.x; e < a.E; e += kThreads)
-        sh.first[e] = 0;
+        first[e] = 0;
     __syncthreads();
     for (int s = threadIdx.x; s < slots; s += kThreads) {
         const int e = read_id(a, s);
         if (slots <= kIds)
             sh.ids[s] = (int16_t)e;
         if (e >= 0)
-            atomicAdd(&sh.first[e], 1);
+            atomicAdd(&first[e], 1);
         else if (e == -2 && blockIdx.x == 0)
             raise_status(a.status, kDevErrBadExpert);
     }
@@ -215,7 +226,7 @@ __device__ int count_groups(const MatvecArgs &a, Shared &sh, int per_group)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x * kPer + i;
-        g[i] = e < a.E ? (sh.first[e] + per_group - 1) / per_group : 0;
+        g[i] = e < a.E ? (first[e] + per_group - 1) / per_group : 0;
         mine += g[i];
     }
     int at = cta_prefix(mine, sh.warp_sum, &total);
@@ -223,11 +234,11 @@ __device__ int count_groups(const MatvecArgs &a, Shared &sh, int per_group)
     for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x * kPer + i;
         if (e < a.E)
-            sh.first[e] = at;
+            first[e] = at;
         at += g[i];
     }
     if (threadIdx.x == 0)
-        sh.first[a.E] = total;
+        first[a.E] = total;
     __syncthreads();
     return total;
 }
@@ -320,15 +331,26 @@ __device__ int find_slots(const MatvecArgs &a, Shared &sh, int e, int from, int 
 // to [2^14, 2^15).  A subnormal largest counts as 2^-126.
 __device__ __forceinline__ int x_shift(uint32_t top) { return top ? 14 - (max((int)(top >> 7), 1) - 127) : 0; }
 
+// Largest finite |x| of 8 BF16 values and `top`, as bits.  (Halves compared in
+// pairs; an infinity, or two NaN meeting, sends it the long way.)
 __device__ __forceinline__ uint32_t finite_absmax(uint32_t top, uint4 v)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m;
+    asm("{\n\t.reg .b32 p, q;\n\t"
+        "max.xorsign.abs.bf16x2 p, %1, %2;\n\t"
+        "max.xorsign.abs.bf16x2 q, %3, %4;\n\t"
+        "max.xorsign.abs.bf16x2 %0, p, q;\n\t}" : "=r"(m) : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+    m = max(m & 0x7fffu, (m >> 16) & 0x7fffu);
+    if (m >= 0x7f80u) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t l = w[i] & 0x7fffu, h = (w[i] >> 16) & 0x7fffu;
-        top = max(top, max(l < 0x7f80u ? l : 0u, h < 0x7f80u ? h : 0u));
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t l = w[i] & 0x7fffu, h = (w[i] >> 16) & 0x7fffu;
+            m = max(m, max(l < 0x7f80u ? l : 0u, h < 0x7f80u ? h : 0u));
+        }
     }
-    return top;
+    return max(top, m);
 }
 
 // 8 BF16 values times 2^shift, as f16.  The power comes in two factors: it
@@ -385,12 +407,12 @@ __device__ __forceinline__ void write_sums(const MatvecArgs &a, const Shared &sh
 }
 
 // Expert of a group of slots: the last one with first[e] <= group.
-__device__ __forceinline__ int expert_of_group(const Shared &sh, int E, int group)
+__device__ __forceinline__ int expert_of_group(const int *first, int E, int group)
 {
     int e = 0, hi = E - 1;
     while (e < hi) {
         const int mid = (e + hi + 1) >> 1;
-        if (sh.first[mid] <= group)
+        if (first[mid] <= group)
             e = mid;
         else
             hi = mid - 1;
@@ -443,20 +465,26 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, 
 }
 
 // Persistent: the (group of slots, tile of rows) pairs are dealt to the CTAs
-// in contiguous ranges, so a CTA meets few groups; a CTA's warps take the
-// pairs of its range in turn.  The steps of a warp's pairs run through its ring
-// without a gap, also where the group changes.  G: columns of x in shared
-// memory (slots per group); HALVES: of a step.
+// in contiguous ranges, so a CTA meets few groups; a CTA's teams of `parts`
+// warps take the pairs of its range in turn.  The steps of a warp's pairs run
+// through its ring without a gap, also where the group changes.  G: columns of
+// x in shared memory (slots per group); HALVES: of a step.
 template <int G, int HALVES>
 __global__ void __launch_bounds__(kThreads, 1)
 matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap scales_map,
-              MatvecArgs a, int depth)
+              MatvecArgs a, int depth, int parts)
 {
     using P = Place<HALVES>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
+    const int halves = (a.K + kHalf - 1) / kHalf;
+    const int steps = (halves + HALVES - 1) / HALVES;
+    const int part = warp & (parts - 1), team = warp / parts, teams = kWarps / parts;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * depth * P::bytes);
+    uint4 *xs = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * depth * P::bytes);
+    int *first = reinterpret_cast<int *>(xs + (size_t)halves * 32 * G);
     uint64_t *full = sh.full + warp * kMaxDepth;
     if (lane == 0) {
         for (int i = 0; i < depth; ++i)
@@ -473,22 +501,17 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
         groups = batch.groups();
         __syncwarp();                   // the warp's mbarriers are its own
     } else {
-        groups = count_groups(a, sh, G);
+        groups = count_groups(a, sh, first, G);
     }
-    auto expert = [&](int group) { return small ? batch.expert(group) : expert_of_group(sh, a.E, group); };
+    auto expert = [&](int group) { return small ? batch.expert(group) : expert_of_group(first, a.E, group); };
     const int tiles = (a.N + kTile - 1) / kTile;
-    const int halves = (a.K + kHalf - 1) / kHalf;
-    const int steps = (halves + HALVES - 1) / HALVES;
     const int64_t total = (int64_t)groups * tiles;
     int64_t at = quotient(total * blockIdx.x, gridDim.x);
     const int64_t end = quotient(total * (blockIdx.x + 1), gridDim.x);
 
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * depth * P::bytes);
-    uint4 *xs = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * depth * P::bytes);
-
     // the step to load next: step p_step of the tile at row p_row, into place p_at
-    int64_t p_item = at + warp;
-    int p_tile = 0, p_row = 0, p_step = 0, p_at = 0, in_flight = 0;
+    int64_t p_item = at + team;
+    int p_tile = 0, p_row = 0, p_step = part, p_at = 0, in_flight = 0;
     auto locate = [&]() {
         if (p_item >= end)
             return;
@@ -507,11 +530,12 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
         }
         ++in_flight;
         p_at = p_at + 1 == depth ? 0 : p_at + 1;
-        if (++p_step == steps) {
-            p_step = 0;
-            p_item += kWarps;
-            p_tile += kWarps;
-            p_row += kWarps * kTile;
+        p_step += parts;
+        if (p_step >= steps) {
+            p_step = part;
+            p_item += teams;
+            p_tile += teams;
+            p_row += teams * kTile;
             if (p_tile >= tiles)
                 locate();
         }
@@ -520,8 +544,8 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
     for (int i = 0; i < depth; ++i)
         load();
 
-    int64_t item = at + warp;
-    int c_at = 0;
+    int64_t item = at + team;
+    int c_at = 0, turn = 0;             // turn: whose it is to add a tile's parts up
     uint32_t parity = 0;
     bool lost = false;                  // a wait gave up: no more loads, no more waits
     const uint32_t c_lane = ring + (uint32_t)(g * P::code_pitch + t * 32);
@@ -537,18 +561,23 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
             m = batch.find(sh, group, G);
             __syncthreads();
         } else {
-            m = find_slots(a, sh, e, (group - sh.first[e]) * G, G);
+            m = find_slots(a, sh, e, (group - first[e]) * G, G);
         }
         stage_x<G>(a, sh, m, xs, halves);
         __syncthreads();
 
-        for (; item < stop && !lost; item += kWarps) {
+        for (; item < stop; item += teams) {
             const int row = (int)(item - (int64_t)group * tiles) * kTile + g;
-            const float row_lo = __ldg(reinterpret_cast<const float *>(w + (int64_t)min(row, a.N - 1) * a.S));
-            const float row_hi = __ldg(reinterpret_cast<const float *>(w + (int64_t)min(row + 8, a.N - 1) * a.S));
-            uint32_t x = x_lane;
+            const bool adds = part == turn;
+            turn = (turn + 1) & (parts - 1);
+            float row_lo = 0.0f, row_hi = 0.0f;
+            if (adds) {
+                row_lo = __ldg(reinterpret_cast<const float *>(w + (int64_t)min(row, a.N - 1) * a.S));
+                row_hi = __ldg(reinterpret_cast<const float *>(w + (int64_t)min(row + 8, a.N - 1) * a.S));
+            }
+            uint32_t x = x_lane + (uint32_t)(part * HALVES * 32 * G * 16);
             float acc[2][4] = {};
-            for (int left = halves; left > 0; left -= HALVES) {
+            for (int left = halves - part * HALVES; left > 0 && !lost; left -= parts * HALVES) {
                 if (!warp_wait(full + c_at, parity)) {
                     lost = true;
                     break;
@@ -565,7 +594,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
                                  [&](int j) { return lds128(x + (h * 32 * G + j * 4 * G) * 16); });
                     }
                 }
-                x += HALVES * 32 * G * 16;
+                x += (uint32_t)(parts * HALVES * 32 * G * 16);
                 if (++c_at == depth) {
                     c_at = 0;
                     parity ^= 1u;
@@ -573,11 +602,24 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
                 __syncwarp();           // every lane has read the place that is loaded next
                 load();
             }
-            if (lost)
-                break;
-            const float sum[4] = {acc[0][0] + acc[1][0], acc[0][1] + acc[1][1], acc[0][2] + acc[1][2],
-                                  acc[0][3] + acc[1][3]};
-            write_sums(a, sh, sum, m, row, t, row_lo, row_hi);
+            float sum[4] = {acc[0][0] + acc[1][0], acc[0][1] + acc[1][1], acc[0][2] + acc[1][2], acc[0][3] + acc[1][3]};
+            if (parts > 1) {
+                named_bar_sync(1 + team, 32 * parts);       // the tile before has been added up
+                sh.partial[warp][lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                named_bar_sync(1 + team, 32 * parts);
+                if (adds) {
+                    sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
+                    for (int p = 0; p < parts; ++p) {
+                        const float4 v = sh.partial[team * parts + p][lane];
+                        sum[0] += v.x;
+                        sum[1] += v.y;
+                        sum[2] += v.z;
+                        sum[3] += v.w;
+                    }
+                }
+            }
+            if (adds && !lost)
+                write_sums(a, sh, sum, m, row, t, row_lo, row_hi);
         }
         at = stop;
         __syncthreads();                // before the next group's x and slots
@@ -597,10 +639,10 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
 }
 
 // Depth of the rings that x of G slots leaves room for.
-template <int HALVES> int ring_depth(size_t x_bytes)
+template <int HALVES> int ring_depth(size_t x_bytes, int E)
 {
-    const size_t ring = (size_t)kWarps * Place<HALVES>::bytes;
-    const int d = x_bytes < kMaxSmem ? (int)((kMaxSmem - x_bytes) / ring) : 0;
+    const size_t ring = (size_t)kWarps * Place<HALVES>::bytes, rest = x_bytes + sizeof(int) * (size_t)(E + 1);
+    const int d = rest < (size_t)kMaxSmem ? (int)((kMaxSmem - rest) / ring) : 0;
     return d > kMaxDepth ? kMaxDepth : d;
 }
 
@@ -612,19 +654,22 @@ template <int G, int HALVES> cudaError_t launch_ring(const LaunchCtx &c, const M
     if (e != cudaSuccess)
         return e;
     const uint64_t rows = (uint64_t)a.E * a.N;
-    const int depth = ring_depth<HALVES>(x_bytes);
+    const int depth = ring_depth<HALVES>(x_bytes, a.E);
     CUtensorMap codes, scales;
     // codes in 16-bit units: a box has at most 256 of them along a side
     if (!make_map(&codes, a.w, (uint64_t)a.K / 4, rows, (uint64_t)a.S, P::code_pitch / 2, kTile, 2) ||
         !make_map(&scales, a.w + a.K / 2, (uint64_t)a.K / 16, rows, (uint64_t)a.S, P::scale_pitch, kTile))
         return cudaErrorInvalidValue;
+    const int steps = (a.K + HALVES * kHalf - 1) / (HALVES * kHalf);
+    const int parts = steps >= kMaxParts ? kMaxParts : steps >= 2 ? 2 : 1;
     return launch_pdl(matvec_kernel<G, HALVES>, dim3((unsigned)c.num_sms), dim3(kThreads),
-                      (size_t)kWarps * depth * P::bytes + x_bytes, c.stream, codes, scales, a, depth);
+                      (size_t)kWarps * depth * P::bytes + x_bytes + sizeof(int) * (size_t)(a.E + 1), c.stream, codes,
+                      scales, a, depth, parts);
 }
 
 template <int G> cudaError_t launch_group(const LaunchCtx &c, const MatvecArgs &a, size_t x_bytes)
 {
-    return ring_depth<2>(G * x_bytes) >= kMinDepth ? launch_ring<G, 2>(c, a, G * x_bytes)
+    return ring_depth<2>(G * x_bytes, a.E) >= kMinDepth ? launch_ring<G, 2>(c, a, G * x_bytes)
                                                    : launch_ring<G, 1>(c, a, G * x_bytes);
 }
 
@@ -641,9 +686,9 @@ cudaError_t launch_matvec(const LaunchCtx &c, const MatvecArgs &a)
     const size_t x_bytes = (size_t)((a.K + kHalf - 1) / kHalf) * kHalf * 2;
     if (a.T == 1)
         return launch_group<1>(c, a, x_bytes);
-    if (a.T == 2 || ring_depth<1>(4 * x_bytes) < kMinDepth)
+    if (a.T == 2 || ring_depth<1>(4 * x_bytes, a.E) < kMinDepth)
         return launch_group<2>(c, a, x_bytes);
-    if (a.T <= 4 || ring_depth<1>(8 * x_bytes) < kMinDepth)
+    if (a.T <= 4 || ring_depth<1>(8 * x_bytes, a.E) < kMinDepth)
         return launch_group<4>(c, a, x_bytes);
     return launch_group<8>(c, a, x_bytes);
 }
