@@ -31,8 +31,8 @@
 //    one of them adds the partial sums up.  A tile of one warp's own would take
 //    it a sixth of a large call's time, and that is what the warps would wait
 //    for each other where the group of slots (and so x) changes.
-// The order of a row's sum depends on K alone: a slot's result does not depend
-// on the other slots of the batch.
+// The order of a row's sum depends on the shape (K, T, E), never on the
+// routing: a slot's result does not depend on where the other slots went.
 #include "epq_device.cuh"
 #include "epq_internal.h"
 
@@ -112,6 +112,42 @@ __device__ __forceinline__ void multiply(float (&acc)[2][4], const uint4 (&lo)[2
     }
 }
 
+// The same for a single column of x, whose seven neighbours the instruction
+// computes anyway: lane t's elements of x stand in column t for its even blocks
+// and in column 4 + t for its odd ones, with zeros elsewhere, so eight
+// instructions leave the sums of eight blocks a row apart, and the block scales
+// are applied to those sums instead of to the weights (12 operations a row
+// pair in place of 32).  `x(j, odd)`: as above where the lane's column is t (or
+// 4 + t), else zeros; `slo`, `shi`: the block scales of lanes L and L + 1, L =
+// 2 (t mod 2), of rows g and g + 8; `pick`: selects byte t / 2 of both words.
+template <typename X>
+__device__ __forceinline__ void multiply_one(float2 &acc, const uint4 (&lo)[2], const uint4 (&hi)[2], uint2 slo,
+                                             uint2 shi, uint32_t pick, X x)
+{
+    const uint32_t w_lo[8] = {lo[0].x, lo[0].y, lo[0].z, lo[0].w, lo[1].x, lo[1].y, lo[1].z, lo[1].w};
+    const uint32_t w_hi[8] = {hi[0].x, hi[0].y, hi[0].z, hi[0].w, hi[1].x, hi[1].y, hi[1].z, hi[1].w};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {       // blocks 2i and 2i + 1 of every lane
+        float sums[4] = {};
+#pragma unroll
+        for (int j = 4 * i; j < 4 * i + 4; ++j) {
+            const uint4 b = x(j, (j >> 1) & 1);
+            uint32_t l[4], h[4];
+            codes_to_f16(w_lo[j], l);
+            codes_to_f16(w_hi[j], h);
+            mma16816(sums, l[0], h[0], l[1], h[1], b.x, b.y);
+            mma16816(sums, l[2], h[2], l[3], h[3], b.z, b.w);
+        }
+        const uint32_t sel = pick + 0x22u * i;
+        const float2 s_lo = f16x2_to_f32x2(cvt_f16x2_from_e4m3x2(__byte_perm(slo.x, slo.y, sel)));
+        const float2 s_hi = f16x2_to_f32x2(cvt_f16x2_from_e4m3x2(__byte_perm(shi.x, shi.y, sel)));
+        acc.x = fmaf(sums[0], s_lo.x, acc.x);
+        acc.y = fmaf(sums[2], s_hi.x, acc.y);
+        acc.x = fmaf(sums[1], s_lo.y, acc.x);
+        acc.y = fmaf(sums[3], s_hi.y, acc.y);
+    }
+}
+
 // A warp's place of the ring: kTile rows of HALVES halves of codes, whose pitch
 // of 16 bytes more than they need (the next step's first ones) keeps the lanes
 // of a warp off each other's banks; then their scales.
@@ -134,6 +170,13 @@ __device__ __forceinline__ uint32_t lds32(uint32_t at)
 {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t at)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
     return v;
 }
 
@@ -161,8 +204,10 @@ struct Shared {
     float4 partial[kWarps][32];          // partial sums of a tile, lane by lane
 };
 
-// Dynamic shared memory: the warps' rings, x of a group, and int[E + 1]
-// `first`, the groups of slots before each expert.
+// Dynamic shared memory: the warps' rings, x of a group, kZeros bytes of zeros
+// (where it is one slot), and int[E + 1] `first`, the groups of slots before
+// each expert.
+constexpr int kZeros = 2 * kHalf * 2;
 constexpr int kMaxSmem = 227 * 1024 - (int)sizeof(Shared);
 
 
@@ -484,7 +529,10 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
     const int part = warp & (parts - 1), team = warp / parts, teams = kWarps / parts;
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * depth * P::bytes);
     uint4 *xs = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * depth * P::bytes);
-    int *first = reinterpret_cast<int *>(xs + (size_t)halves * 32 * G);
+    uint4 *zeros = xs + (size_t)halves * 32 * G;
+    int *first = reinterpret_cast<int *>(G == 1 ? zeros + kZeros / 16 : zeros);
+    if (G == 1 && threadIdx.x < kZeros / 16)
+        zeros[threadIdx.x] = make_uint4(0, 0, 0, 0);    // (published by the barriers before the first product)
     uint64_t *full = sh.full + warp * kMaxDepth;
     if (lane == 0) {
         for (int i = 0; i < depth; ++i)
@@ -551,6 +599,10 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
     const uint32_t c_lane = ring + (uint32_t)(g * P::code_pitch + t * 32);
     const uint32_t s_lane = ring + (uint32_t)(P::codes + g * P::scale_pitch + t * 4);
     const uint32_t x_lane = smem_u32(xs) + (uint32_t)(((g % G) * 4 + t) * 16);
+    // one slot: which blocks' x this lane's column holds, and the scales of its sums
+    const bool even = g == t, odd = g == t + 4;
+    const uint32_t s_one = ring + (uint32_t)(P::codes + g * P::scale_pitch + (t & 1) * 8);
+    const uint32_t pick = (uint32_t)(t >> 1) * 0x11u + 0x40u;
     while (at < end) {
         const int group = (int)quotient(at, tiles);
         const int64_t stop = min(end, (int64_t)(group + 1) * tiles);
@@ -577,21 +629,30 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
             }
             uint32_t x = x_lane + (uint32_t)(part * HALVES * 32 * G * 16);
             float acc[2][4] = {};
+            float2 one = make_float2(0.0f, 0.0f);
             for (int left = halves - part * HALVES; left > 0 && !lost; left -= parts * HALVES) {
                 if (!warp_wait(full + c_at, parity)) {
                     lost = true;
                     break;
                 }
                 --in_flight;
-                const uint32_t c = c_lane + (uint32_t)(c_at * P::bytes), s = s_lane + (uint32_t)(c_at * P::bytes);
+                const uint32_t place = (uint32_t)(c_at * P::bytes), c = c_lane + place;
+                const uint32_t x_even = even ? x : smem_u32(zeros), x_odd = odd ? x : smem_u32(zeros);
 #pragma unroll
                 for (int h = 0; h < HALVES; ++h) {
                     if (h < left) {
-                        const uint32_t ch = c + h * (kHalf / 2), sh8 = s + h * (kHalf / 16);
+                        const uint32_t ch = c + h * (kHalf / 2);
                         const uint4 wl[2] = {lds128(ch), lds128(ch + 16)};
                         const uint4 wh[2] = {lds128(ch + 8 * P::code_pitch), lds128(ch + 8 * P::code_pitch + 16)};
-                        multiply(acc, wl, wh, lds32(sh8), lds32(sh8 + 8 * P::scale_pitch),
-                                 [&](int j) { return lds128(x + (h * 32 * G + j * 4 * G) * 16); });
+                        if (G == 1) {
+                            const uint32_t s = s_one + place + h * (kHalf / 16);
+                            multiply_one(one, wl, wh, lds64(s), lds64(s + 8 * P::scale_pitch), pick,
+                                         [&](int j, int o) { return lds128((o ? x_odd : x_even) + (h * 32 + j * 4) * 16); });
+                        } else {
+                            const uint32_t s = s_lane + place + h * (kHalf / 16);
+                            multiply(acc, wl, wh, lds32(s), lds32(s + 8 * P::scale_pitch),
+                                     [&](int j) { return lds128(x + (h * 32 * G + j * 4 * G) * 16); });
+                        }
                     }
                 }
                 x += (uint32_t)(parts * HALVES * 32 * G * 16);
@@ -603,6 +664,14 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
                 load();
             }
             float sum[4] = {acc[0][0] + acc[1][0], acc[0][1] + acc[1][1], acc[0][2] + acc[1][2], acc[0][3] + acc[1][3]};
+            if (G == 1) {               // the lanes of a row hold a quarter of its blocks each
+                for (int o = 1; o < 4; o <<= 1) {
+                    one.x += __shfl_xor_sync(0xffffffffu, one.x, o);
+                    one.y += __shfl_xor_sync(0xffffffffu, one.y, o);
+                }
+                sum[0] = one.x;         // (slot 0 is lane t = 0's)
+                sum[2] = one.y;
+            }
             if (parts > 1) {
                 named_bar_sync(1 + team, 32 * parts);       // the tile before has been added up
                 sh.partial[warp][lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
@@ -641,7 +710,8 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
 // Depth of the rings that x of G slots leaves room for.
 template <int HALVES> int ring_depth(size_t x_bytes, int E)
 {
-    const size_t ring = (size_t)kWarps * Place<HALVES>::bytes, rest = x_bytes + sizeof(int) * (size_t)(E + 1);
+    const size_t ring = (size_t)kWarps * Place<HALVES>::bytes;
+    const size_t rest = x_bytes + sizeof(int) * (size_t)(E + 1);
     const int d = rest < (size_t)kMaxSmem ? (int)((kMaxSmem - rest) / ring) : 0;
     return d > kMaxDepth ? kMaxDepth : d;
 }
@@ -685,7 +755,7 @@ cudaError_t launch_matvec(const LaunchCtx &c, const MatvecArgs &a)
     // smaller steps.
     const size_t x_bytes = (size_t)((a.K + kHalf - 1) / kHalf) * kHalf * 2;
     if (a.T == 1)
-        return launch_group<1>(c, a, x_bytes);
+        return launch_group<1>(c, a, x_bytes + kZeros);
     if (a.T == 2 || ring_depth<1>(4 * x_bytes, a.E) < kMinDepth)
         return launch_group<2>(c, a, x_bytes);
     if (a.T <= 4 || ring_depth<1>(8 * x_bytes, a.E) < kMinDepth)
