@@ -19,7 +19,9 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// VEC consecutive elements of type T as one load or store.
+// What a thread loads and stores at a time, a unit: VEC consecutive elements of
+// type T, 16 bytes where every row starts on 16 bytes and is a whole number of
+// them, else 4, else (BF16 rows of odd length) one element.
 template <int BYTES> struct Raw;
 template <> struct Raw<16> { using type = uint4; };
 template <> struct Raw<4> { using type = uint32_t; };
@@ -97,21 +99,28 @@ __device__ __forceinline__ int live_row(int d, int R_cap, uint32_t *status)
 }
 
 // ---------------------------------------------------------------- combine
+// One thread per UNR units of a token, a CTA's share of the row side by side;
+// the rows of KCH slots are in flight at once.  Narrow units come several to a
+// thread: with one, too few bytes are in flight (4096 tokens x 4097, top-4,
+// FP32: 115 us; with two 83 us).
+template <typename T, int VEC, int KCH> constexpr int units_in_flight()
+{
+    return sizeof(T) * VEC >= 16 ? (KCH > 2 ? 1 : 2) : sizeof(T) * VEC >= 4 && KCH > 2 ? 2 : 4;
+}
+
 template <typename T, int VEC, int KCH>
 __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a)
 {
+    constexpr int UNR = units_in_flight<T, VEC, KCH>();
     pdl_launch_dependents();
     pdl_wait();
     const int64_t t = blockIdx.x;
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-    if (c >= a.H)
+    const int c0 = (blockIdx.y * UNR * blockDim.x + threadIdx.x) * VEC, step = blockDim.x * VEC;
+    if (c0 >= a.H)
         return;
     const T *rows = static_cast<const T *>(a.rows);
     const int64_t slot0 = t * a.k;
-    float acc[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-        acc[i] = 0.0f;
+    float acc[UNR][VEC] = {};
     for (int j0 = 0; j0 < a.k; j0 += KCH) {
         int d[KCH];
         float w[KCH];
@@ -128,25 +137,35 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a)
                     w[j] = __ldg(a.weights + s);
             }
         }
-        RawOf<T, VEC> raw[KCH];
+        RawOf<T, VEC> raw[KCH][UNR];
 #pragma unroll
         for (int j = 0; j < KCH; ++j) {
             d[j] = live_row(d[j], a.R_cap, a.status);
-            if (d[j] >= 0)
-                raw[j] = load_raw<T, VEC>(rows + (int64_t)d[j] * a.ld_rows + c);
+            if (d[j] >= 0) {
+#pragma unroll
+                for (int u = 0; u < UNR; ++u)
+                    if (c0 + u * step < a.H)
+                        raw[j][u] = load_raw<T, VEC>(rows + (int64_t)d[j] * a.ld_rows + c0 + u * step);
+            }
         }
 #pragma unroll
         for (int j = 0; j < KCH; ++j) {
             if (d[j] < 0)
                 continue;
-            float f[VEC];
-            unpack_raw(raw[j], f);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                acc[i] = fmaf(w[j], f[i], acc[i]);
+            for (int u = 0; u < UNR; ++u) {
+                float f[VEC];
+                unpack_raw(raw[j][u], f);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    acc[u][i] = fmaf(w[j], f[i], acc[u][i]);
+            }
         }
     }
-    store_raw<T, VEC>(static_cast<T *>(a.out) + t * a.H + c, pack_raw<T, VEC>(acc));
+#pragma unroll
+    for (int u = 0; u < UNR; ++u)
+        if (c0 + u * step < a.H)
+            store_raw<T, VEC>(static_cast<T *>(a.out) + t * a.H + c0 + u * step, pack_raw<T, VEC>(acc[u]));
 }
 
 // ---------------------------------------------------------------- scatter
@@ -158,7 +177,7 @@ __device__ void zero_padding(const ScatterArgs &a, int cta)
     const int e = cta / a.pad_split;
     const int end = __ldg(a.offsets + e + 1);
     T *rows = static_cast<T *>(a.rows_out);
-    float zero[VEC] = {};
+    const RawOf<T, VEC> zero = {};
     for (int r = __ldg(a.offsets + e) + __ldg(a.counts + e) + cta % a.pad_split; r < end; r += a.pad_split) {
         if (r < 0 || r >= a.R_cap) {
             if (threadIdx.x == 0)
@@ -166,7 +185,7 @@ __device__ void zero_padding(const ScatterArgs &a, int cta)
             return;
         }
         for (int c = threadIdx.x * VEC; c < a.H; c += blockDim.x * VEC)
-            store_raw<T, VEC>(rows + (int64_t)r * a.H + c, pack_raw<T, VEC>(zero));
+            store_raw<T, VEC>(rows + (int64_t)r * a.H + c, zero);
     }
 }
 
@@ -269,18 +288,23 @@ int block_of(int64_t units)
     return (int)(((units + passes - 1) / passes + 31) / 32 * 32);
 }
 
+template <typename T, int VEC, int KCH> cudaError_t combine_slots(const LaunchCtx &c, const CombineArgs &a)
+{
+    const int64_t units = (a.H + VEC - 1) / VEC;
+    const int64_t shares = (units + units_in_flight<T, VEC, KCH>() - 1) / units_in_flight<T, VEC, KCH>();
+    const int block = block_of(shares);
+    const dim3 grid((unsigned)a.T, (unsigned)((shares + block - 1) / block));
+    return launch_pdl(combine_kernel<T, VEC, KCH>, grid, dim3(block), 0, c.stream, a);
+}
+
 template <typename T, int VEC> cudaError_t combine_vec(const LaunchCtx &c, const CombineArgs &a)
 {
-    const int64_t units = a.H / VEC;
-    const int block = block_of(units);
-    const dim3 grid((unsigned)a.T, (unsigned)((units + block - 1) / block));
-    return a.k <= 2 ? launch_pdl(combine_kernel<T, VEC, 2>, grid, dim3(block), 0, c.stream, a)
-                    : launch_pdl(combine_kernel<T, VEC, 8>, grid, dim3(block), 0, c.stream, a);
+    return a.k <= 2 ? combine_slots<T, VEC, 2>(c, a) : combine_slots<T, VEC, 8>(c, a);
 }
 
 template <typename T, int VEC, bool DOT> cudaError_t scatter_vec(const LaunchCtx &c, ScatterArgs a)
 {
-    const int64_t units = a.H / VEC;
+    const int64_t units = (a.H + VEC - 1) / VEC;
     const int block = (int)(units >= kThreads ? kThreads : (units + 31) / 32 * 32);
     a.pad_split = a.E >= 256 ? 8 : 32;
     const dim3 grid((unsigned)(a.T + a.E * a.pad_split));

@@ -15,10 +15,10 @@
 //    applied to the finished sum.
 //  - x is BF16; a slot's elements are scaled by one power of two that brings
 //    its largest to [2^14, 2^15) and taken to f16: exact for every element
-//    within 2^-28 of the largest, and off by at most 2^-40 of the largest
+//    within 2^-31 of the largest, and off by at most 2^-39 of the largest
 //    below that (FP32 accumulation loses more).  Infinities and NaN stay.
-//    (Hardware converts two codes in one instruction; taking them apart by
-//    shifts and masks instead costs 4.3 instructions a pair and twice the time.)
+//  - two codes are converted by one instruction; taking them apart by shifts
+//    and masks costs four times the instructions and twice the time.
 //  - the summation index is free to be permuted: lane (g, t) of a warp takes
 //    64 consecutive elements of rows g and g + 8, so no fragment shuffle is
 //    needed, and x is brought into the order in which the lanes want it.
