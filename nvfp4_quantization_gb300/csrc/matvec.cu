@@ -27,10 +27,11 @@
 // What bounds it: with the rows at HBM's rate the conversion and the matrix
 // instruction take about 60 % of the issue slots, so a step's bookkeeping has
 // to be small beside its 32 matrix instructions.
-//  - up to four warps share a tile, each taking every fourth step of its rows;
-//    one of them adds the partial sums up.  A tile of one warp's own would take
-//    it a sixth of a large call's time, and that is what the warps would wait
-//    for each other where the group of slots (and so x) changes.
+//  - two warps share a tile, each taking every second step of its rows, and one
+//    of them adds the partial sums up.  The warps wait for each other where the
+//    group of slots (and so x) changes, for a tile's time at worst; but every
+//    tile costs two barriers (32 tokens x 8 of 64 experts of 4096 x 4096: 122 us
+//    with one warp a tile, 115 with two, 120 with four, 140 with eight).
 // The order of a row's sum depends on the shape (K, T, E), never on the
 // routing: a slot's result does not depend on where the other slots went.
 #include "epq_device.cuh"
@@ -48,7 +49,7 @@ constexpr int kMaxDepth = 6;     // steps in flight per warp, at most ...
 constexpr int kMinDepth = 2;     // ... and at least
 constexpr int kMaxE = 1024;
 constexpr int kIds = 512;        // slots whose expert is kept in shared memory
-constexpr int kMaxParts = 4;     // warps that share a tile, at most
+constexpr int kMaxParts = 2;     // warps that share a tile, at most
 
 // One word of eight E2M1 codes -> four f16 pairs (exact).
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4])
@@ -731,7 +732,9 @@ template <int G, int HALVES> cudaError_t launch_ring(const LaunchCtx &c, const M
         !make_map(&scales, a.w + a.K / 2, (uint64_t)a.K / 16, rows, (uint64_t)a.S, P::scale_pitch, kTile))
         return cudaErrorInvalidValue;
     const int steps = (a.K + HALVES * kHalf - 1) / (HALVES * kHalf);
-    const int parts = steps >= kMaxParts ? kMaxParts : steps >= 2 ? 2 : 1;
+    int parts = 1;
+    while (2 * parts <= kMaxParts && 2 * parts <= steps)
+        parts *= 2;
     return launch_pdl(matvec_kernel<G, HALVES>, dim3((unsigned)c.num_sms), dim3(kThreads),
                       (size_t)kWarps * depth * P::bytes + x_bytes + sizeof(int) * (size_t)(a.E + 1), c.stream, codes,
                       scales, a, depth, parts);
