@@ -315,11 +315,12 @@ def _stream_of(stream, device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _need_dense(t: torch.Tensor, name: str, shape: tuple, dtype, device):
-    """A contiguous operand of exactly this shape, on this device."""
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+def _need_dense(t: torch.Tensor, name: str, shape: tuple, dtype):
+    """A contiguous operand of exactly this shape and type.  (That it is on the
+    input's device is the library's own check, on the addresses.)"""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
 def _need_rows(t: torch.Tensor, name: str, dtypes) -> int:
@@ -341,13 +342,18 @@ def _need_rows(t: torch.Tensor, name: str, dtypes) -> int:
     return pitch
 
 
-def _need_plan(plan: RoutePlan, T: int, device):
+def _need_int32(t: torch.Tensor, name: str, n: int):
+    if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor with at least {n} entries")
+
+
+def _need_plan(plan: RoutePlan, T: int):
     if plan.T != T:
         raise ValueError(f"the plan is for {plan.T} tokens, got {T}")
-    for t, name, n in ((plan.dest, "plan.dest", T * plan.k), (plan.offsets, "plan.offsets", plan.E + 1),
-                       (plan.counts, "plan.counts", plan.E), (plan.status, "plan.status", 1)):
-        if t.dtype != torch.int32 or t.device != device or t.numel() < n or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor with at least {n} entries on {device}")
+    _need_int32(plan.dest, "plan.dest", T * plan.k)
+    _need_int32(plan.offsets, "plan.offsets", plan.E + 1)
+    _need_int32(plan.counts, "plan.counts", plan.E)
+    _need_int32(plan.status, "plan.status", 1)
 
 
 def _empty(shape, dtype, device, stream):
@@ -364,8 +370,7 @@ def _status_or_new(status, device, stream):
             return new_status(device)
         with torch.cuda.stream(stream):
             return new_status(device)
-    if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
-        raise ValueError(f"status must be an int32 tensor on {device}")
+    _need_int32(status, "status", 1)
     return status
 
 
@@ -374,14 +379,15 @@ def ep_pack(tokens: torch.Tensor, plan: RoutePlan, rows: torch.Tensor | None = N
     are; padding rows are zeroed.  The gradient is ``ep_combine(d_rows, plan)``."""
     ld = _need_rows(tokens, "tokens", _DTYPE)
     T, H = tokens.shape
-    _need_plan(plan, T, tokens.device)
+    _need_plan(plan, T)
     if rows is None:
         rows = _empty((plan.R_cap, H), tokens.dtype, tokens.device, stream)
     else:
-        _need_dense(rows, "rows", (plan.R_cap, H), tokens.dtype, tokens.device)
+        _need_dense(rows, "rows", (plan.R_cap, H), tokens.dtype)
     st = _lib.lib().ep_pack(_at(tokens), _DTYPE[tokens.dtype], T, H, ld, _at(plan.dest), plan.k, _at(plan.offsets),
                             _at(plan.counts), plan.E, _at(rows), plan.R_cap, _at(plan.status), _stream_of(stream, tokens.device))
-    check("ep_pack", st)
+    if st:
+        check("ep_pack", st)
     return rows
 
 
@@ -401,27 +407,28 @@ def ep_combine(rows: torch.Tensor, plan: RoutePlan | None = None, weights: torch
         raise ValueError("ep_combine takes either plan or topk_idx")
     if plan is not None:
         T, k, index = plan.T, plan.k, plan.dest
-        _need_plan(plan, T, dev)
+        _need_plan(plan, T)
         if status is None:
             status = plan.status
     else:
         if topk_idx.dim() != 2:
             raise ValueError("topk_idx must have two dimensions")
         T, k = topk_idx.shape
-        _need_dense(topk_idx, "topk_idx", (T, k), torch.int32, dev)
+        _need_dense(topk_idx, "topk_idx", (T, k), torch.int32)
         if n != T * k:
             raise ValueError(f"rows in slot order must be {T * k}, got {n}")
         index = topk_idx
     status = _status_or_new(status, dev, stream)
     if weights is not None:
-        _need_dense(weights, "weights", (T, k), torch.float32, dev)
+        _need_dense(weights, "weights", (T, k), torch.float32)
     if out is None:
         out = _empty((T, H), rows.dtype, dev, stream)
     else:
-        _need_dense(out, "out", (T, H), rows.dtype, dev)
+        _need_dense(out, "out", (T, H), rows.dtype)
     st = _lib.lib().ep_combine(_at(rows), _DTYPE[rows.dtype], n, H, ld, _at(index), int(plan is None),
                                _at(weights), T, k, _at(out), _at(status), _stream_of(stream, dev))
-    check("ep_combine", st)
+    if st:
+        check("ep_combine", st)
     return out
 
 
@@ -435,29 +442,30 @@ def ep_combine_backward(d_out: torch.Tensor, plan: RoutePlan, weights: torch.Ten
     ld = _need_rows(d_out, "d_out", _DTYPE)
     T, H = d_out.shape
     dev, dt = d_out.device, d_out.dtype
-    _need_plan(plan, T, dev)
+    _need_plan(plan, T)
     k, R_cap = plan.k, plan.R_cap
     ld_rows = H
     if weights is not None:
-        _need_dense(weights, "weights", (T, k), torch.float32, dev)
+        _need_dense(weights, "weights", (T, k), torch.float32)
     if rows is not None:
         ld_rows = _need_rows(rows, "rows", (dt,))
-        if rows.shape != (R_cap, H) or rows.device != dev:
-            raise ValueError(f"rows must have shape {(R_cap, H)} on {dev}, got {tuple(rows.shape)} on {rows.device}")
+        if rows.shape != (R_cap, H):
+            raise ValueError(f"rows must have shape {(R_cap, H)}, got {tuple(rows.shape)}")
         if d_weights is None:
             d_weights = _empty((T, k), torch.float32, dev, stream)
         else:
-            _need_dense(d_weights, "d_weights", (T, k), torch.float32, dev)
+            _need_dense(d_weights, "d_weights", (T, k), torch.float32)
     elif d_weights is not None:
         raise ValueError("d_weights needs rows")
     if d_rows is None:
         d_rows = _empty((R_cap, H), dt, dev, stream)
     else:
-        _need_dense(d_rows, "d_rows", (R_cap, H), dt, dev)
+        _need_dense(d_rows, "d_rows", (R_cap, H), dt)
     st = _lib.lib().ep_combine_backward(_at(d_out), _DTYPE[dt], T, H, ld, _at(rows), ld_rows, _at(plan.dest),
                                         _at(weights), k, _at(plan.offsets), _at(plan.counts), plan.E,
                                         _at(d_rows), R_cap, _at(d_weights), _at(plan.status), _stream_of(stream, dev))
-    check("ep_combine_backward", st)
+    if st:
+        check("ep_combine_backward", st)
     return d_rows, d_weights
 
 
@@ -466,13 +474,11 @@ def swiglu_checkpoint_bytes(R_cap: int, I: int) -> int:
     return R_cap * 2 * I + R_cap * (2 * I // 32)
 
 
-def _need_offsets(offsets, E: int, device):
-    if offsets is None:
-        if E != 1:
-            raise ValueError("E must be 1 without offsets")
-    elif offsets.dtype != torch.int32 or offsets.device != device or offsets.numel() < E + 1 or \
-            not offsets.is_contiguous():
-        raise ValueError(f"offsets must be a contiguous int32 tensor with at least {E + 1} entries on {device}")
+def _need_offsets(offsets, E: int):
+    if offsets is not None:
+        _need_int32(offsets, "offsets", E + 1)
+    elif E != 1:
+        raise ValueError("E must be 1 without offsets")
 
 
 def ep_swiglu(x: torch.Tensor, offsets: torch.Tensor | None = None, E: int = 1, act: torch.Tensor | None = None,
@@ -488,19 +494,20 @@ def ep_swiglu(x: torch.Tensor, offsets: torch.Tensor | None = None, E: int = 1, 
     if width % 64:
         raise ValueError(f"x needs two halves of a multiple of 32 columns, got {width}")
     I, dev = width // 2, x.device
-    _need_offsets(offsets, E, dev)
+    _need_offsets(offsets, E)
     if act is None:
         act = _empty((R_cap, I), torch.bfloat16, dev, stream)
     else:
-        _need_dense(act, "act", (R_cap, I), torch.bfloat16, dev)
+        _need_dense(act, "act", (R_cap, I), torch.bfloat16)
     if ckpt is not None:
-        _need_dense(ckpt, "ckpt", (swiglu_checkpoint_bytes(R_cap, I),), torch.uint8, dev)
+        _need_dense(ckpt, "ckpt", (swiglu_checkpoint_bytes(R_cap, I),), torch.uint8)
     elif checkpoint:
         ckpt = _empty((swiglu_checkpoint_bytes(R_cap, I),), torch.uint8, dev, stream)
     status = _status_or_new(status, dev, stream)
     st = _lib.lib().ep_swiglu(_at(x), ld, R_cap, I, _at(offsets), E, _at(act), _at(ckpt), _at(status),
                               _stream_of(stream, dev))
-    check("ep_swiglu", st)
+    if st:
+        check("ep_swiglu", st)
     return act, ckpt
 
 
@@ -518,22 +525,23 @@ def ep_swiglu_backward(d_act: torch.Tensor, ckpt: torch.Tensor, offsets: torch.T
     dev = d_act.device
     if I % 32:
         raise ValueError(f"d_act needs a multiple of 32 columns, got {I}")
-    _need_offsets(offsets, E, dev)
-    _need_dense(ckpt, "ckpt", (swiglu_checkpoint_bytes(R_cap, I),), torch.uint8, dev)
+    _need_offsets(offsets, E)
+    _need_dense(ckpt, "ckpt", (swiglu_checkpoint_bytes(R_cap, I),), torch.uint8)
     if d_x is None:
         d_x = _empty((R_cap, 2 * I), torch.bfloat16, dev, stream)
     else:
-        _need_dense(d_x, "d_x", (R_cap, 2 * I), torch.bfloat16, dev)
+        _need_dense(d_x, "d_x", (R_cap, 2 * I), torch.bfloat16)
     if act is not None:
-        _need_dense(act, "act", (R_cap, I), torch.bfloat16, dev)
+        _need_dense(act, "act", (R_cap, I), torch.bfloat16)
     elif recompute:
         act = _empty((R_cap, I), torch.bfloat16, dev, stream)
     if expert_amax is not None:
-        _need_dense(expert_amax, "expert_amax", (E,), torch.float32, dev)
+        _need_dense(expert_amax, "expert_amax", (E,), torch.float32)
     status = _status_or_new(status, dev, stream)
     st = _lib.lib().ep_swiglu_backward(_at(d_act), ld, _at(ckpt), R_cap, I, _at(offsets), E, _at(d_x), _at(act),
                                        _at(expert_amax), _at(status), _stream_of(stream, dev))
-    check("ep_swiglu_backward", st)
+    if st:
+        check("ep_swiglu_backward", st)
     return d_x, act
 
 
@@ -575,7 +583,7 @@ def ep_nvfp4_matvec(x: torch.Tensor, w_rows: torch.Tensor, topk_idx: torch.Tenso
     if w_rows.dim() != 3:
         raise ValueError("w_rows must have three dimensions [E, N, row_bytes(K)]")
     E, N, S = w_rows.shape
-    _need_dense(w_rows, "w_rows", (E, N, row_bytes(K)), torch.uint8, dev)
+    _need_dense(w_rows, "w_rows", (E, N, (9 * K // 16 + 31) // 16 * 16), torch.uint8)   # row_bytes(K)
     if topk_idx is None:
         if E != 1:
             raise ValueError("w_rows of several experts needs topk_idx")
@@ -584,15 +592,16 @@ def ep_nvfp4_matvec(x: torch.Tensor, w_rows: torch.Tensor, topk_idx: torch.Tenso
         if topk_idx.dim() != 2:
             raise ValueError("topk_idx must have two dimensions")
         T, k = topk_idx.shape
-        _need_dense(topk_idx, "topk_idx", (T, k), torch.int32, dev)
+        _need_dense(topk_idx, "topk_idx", (T, k), torch.int32)
         if n != T and n != T * k:
             raise ValueError(f"x must have {T} or {T * k} rows, got {n}")
     if y is None:
         y = _empty((T * k, N), torch.bfloat16, dev, stream)
     else:
-        _need_dense(y, "y", (T * k, N), torch.bfloat16, dev)
+        _need_dense(y, "y", (T * k, N), torch.bfloat16)
     status = _status_or_new(status, dev, stream)
     st = _lib.lib().ep_nvfp4_matvec(_at(x), T, K, ld, int(n != T), _at(w_rows), E, N, _at(topk_idx), k, _at(y),
                                     _at(status), _stream_of(stream, dev))
-    check("ep_nvfp4_matvec", st)
+    if st:
+        check("ep_nvfp4_matvec", st)
     return y
