@@ -45,7 +45,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;        // weight rows of a warp's tile
 constexpr int kHalf = 256;       // elements of a row that a warp multiplies at a time
-constexpr int kMaxDepth = 6;     // steps in flight per warp, at most ...
+constexpr int kMaxDepth = 3;     // steps in flight per warp, at most ...
 constexpr int kMinDepth = 2;     // ... and at least
 constexpr int kMaxE = 1024;
 constexpr int kIds = 512;        // slots whose expert is kept in shared memory
@@ -187,13 +187,37 @@ __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap *
                  " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"((uint64_t)m), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
-// Bounded wait of a whole warp on its barrier (as mbar_wait_bounded, the first
-// attempt in line).
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+__device__ __forceinline__ void mbar_arrive_expect_tx_at(uint32_t bar, uint32_t bytes)
 {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+                 "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+__device__ __noinline__ bool mbar_wait_bounded_at(uint32_t bar, uint32_t parity)
+{
+    for (uint32_t i = 0; i < (1u << 22); ++i) {
+        if (mbar_try_wait_at(bar, parity))
+            return true;
+        if (i > 64)
+            __nanosleep(256);
+    }
+    return false;
+}
+
+// Bounded wait of a whole warp on its barrier (the first attempt in line).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait_at(bar, parity)))
         return true;
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+    return __all_sync(0xffffffffu, mbar_wait_bounded_at(bar, parity));
 }
 
 struct Shared {
@@ -559,43 +583,51 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
     const int64_t end = quotient(total * (blockIdx.x + 1), gridDim.x);
 
     // the step to load next: step p_step of the tile at row p_row, into place p_at
+    const uint32_t ring_bytes = (uint32_t)(depth * P::bytes), bars = smem_u32(full);
     int64_t p_item = at + team;
-    int p_tile = 0, p_row = 0, p_step = part, p_at = 0, in_flight = 0;
+    int p_tile = 0, p_row = 0, p_step = part, in_flight = 0;
+    uint32_t p_at = 0, p_bar = bars;
+    bool p_more = p_item < end;
     auto locate = [&]() {
-        if (p_item >= end)
-            return;
         const int group = (int)quotient(p_item, tiles);
         p_tile = (int)(p_item - (int64_t)group * tiles);
         p_row = expert(group) * a.N + p_tile * kTile;
     };
     auto load = [&]() {
-        if (p_item >= end)
+        if (!p_more)
             return;
         if (lane == 0) {
-            const uint32_t to = ring + (uint32_t)(p_at * P::bytes);
-            mbar_arrive_expect_tx(full + p_at, P::bytes);
-            tma_load_2d_at(to, &codes_map, p_step * (HALVES * kHalf / 4), p_row, smem_u32(full + p_at));
-            tma_load_2d_at(to + P::codes, &scales_map, p_step * (HALVES * kHalf / 16), p_row, smem_u32(full + p_at));
+            const uint32_t to = ring + p_at;
+            mbar_arrive_expect_tx_at(p_bar, P::bytes);
+            tma_load_2d_at(to, &codes_map, p_step * (HALVES * kHalf / 4), p_row, p_bar);
+            tma_load_2d_at(to + P::codes, &scales_map, p_step * (HALVES * kHalf / 16), p_row, p_bar);
         }
         ++in_flight;
-        p_at = p_at + 1 == depth ? 0 : p_at + 1;
+        p_at += P::bytes;
+        p_bar += sizeof(uint64_t);
+        if (p_at == ring_bytes) {
+            p_at = 0;
+            p_bar = bars;
+        }
         p_step += parts;
         if (p_step >= steps) {
             p_step = part;
             p_item += teams;
             p_tile += teams;
             p_row += teams * kTile;
-            if (p_tile >= tiles)
+            p_more = p_item < end;
+            if (p_tile >= tiles && p_more)
                 locate();
         }
     };
-    locate();
+    if (p_more)
+        locate();
     for (int i = 0; i < depth; ++i)
         load();
 
     int64_t item = at + team;
-    int c_at = 0, turn = 0;             // turn: whose it is to add a tile's parts up
-    uint32_t parity = 0;
+    int turn = 0;                       // whose it is to add a tile's parts up
+    uint32_t c_at = 0, c_bar = bars, parity = 0;
     bool lost = false;                  // a wait gave up: no more loads, no more waits
     const uint32_t c_lane = ring + (uint32_t)(g * P::code_pitch + t * 32);
     const uint32_t s_lane = ring + (uint32_t)(P::codes + g * P::scale_pitch + t * 4);
@@ -632,12 +664,12 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
             float acc[2][4] = {};
             float2 one = make_float2(0.0f, 0.0f);
             for (int left = halves - part * HALVES; left > 0 && !lost; left -= parts * HALVES) {
-                if (!warp_wait(full + c_at, parity)) {
+                if (!warp_wait(c_bar, parity)) {
                     lost = true;
                     break;
                 }
                 --in_flight;
-                const uint32_t place = (uint32_t)(c_at * P::bytes), c = c_lane + place;
+                const uint32_t place = c_at, c = c_lane + place;
                 const uint32_t x_even = even ? x : smem_u32(zeros), x_odd = odd ? x : smem_u32(zeros);
 #pragma unroll
                 for (int h = 0; h < HALVES; ++h) {
@@ -657,8 +689,11 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
                     }
                 }
                 x += (uint32_t)(parts * HALVES * 32 * G * 16);
-                if (++c_at == depth) {
+                c_at += P::bytes;
+                c_bar += sizeof(uint64_t);
+                if (c_at == ring_bytes) {
                     c_at = 0;
+                    c_bar = bars;
                     parity ^= 1u;
                 }
                 __syncwarp();           // every lane has read the place that is loaded next
@@ -698,9 +733,10 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
         raise_status(a.status, kDevErrTimeout);
         // never leave with a load in flight
         for (; in_flight > 0; --in_flight) {
-            (void)mbar_wait_bounded(full + c_at, parity);
-            if (++c_at == depth) {
-                c_at = 0;
+            (void)mbar_wait_bounded_at(c_bar, parity);
+            c_bar += sizeof(uint64_t);
+            if (c_bar == bars + depth * sizeof(uint64_t)) {
+                c_bar = bars;
                 parity ^= 1u;
             }
         }
