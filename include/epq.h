@@ -422,7 +422,8 @@ ep_status ep_pack(const void *tokens, int dtype, int64_t T, int64_t H,
 /*
  * ep_combine -- expert rows back to tokens, weighted by the router:
  *   out[t] = sum over j of weights(t, j) * rows[r(t, j)], live slots only.
- *   rows            device [R_cap, H] of `dtype`, row pitch ld_rows elements.
+ *   rows            device [R_cap, H] of `dtype`, row pitch ld_rows elements;
+ *                   must not overlap `out`.
  *   index           slot_order = 0: device int32 [T*k], r(t, j) = index(t, j)
  *                   (the plan's dest); a negative entry is a dropped slot, one
  *                   >= R_cap raises EP_DEV_ERR_CAPACITY and is dropped.
@@ -430,8 +431,8 @@ ep_status ep_pack(const void *tokens, int dtype, int64_t T, int64_t H,
  *                   ep_nvfp4_matvec writes, R_cap >= T*k); a negative entry
  *                   (topk_idx) is a dropped slot; NULL: none is dropped.
  *   weights         device f32 [T*k] or NULL (all 1).  Weights and rows of
- *                   dropped slots are not read: whatever they hold does not
- *                   reach the output.
+ *                   dropped slots do not reach the output, whatever they
+ *                   hold.
  *   out             device [T, H] of `dtype`; a token without a live slot gets
  *                   zeros.
  * FP32 fused multiply-adds in slot order, rounded once.
@@ -524,8 +525,12 @@ ep_status ep_swiglu_backward(const void *d_act_bf16, int64_t ld_act,
  *                   repeat within a token.
  *   y_bf16          device bf16 [T*k, N].
  * Any T is accepted; the call is made for batches whose time is the reading
- * of the weights.  FP32 accumulation in a fixed order, the row scale applied
- * to the sum, one rounding.
+ * of the weights (up to 8 slots of an expert share one pass over its rows, fewer
+ * where K is above about 8000).  Weights and block scales enter exactly, x within
+ * 2^-39 of its row's largest element; FP32 accumulation, the row scale applied
+ * to the sum, one rounding.  A slot's result does not depend on the routing of
+ * the other slots (it may differ in the last bits between batch sizes).
+ * An infinity or NaN in x shows in its slot's outputs alone.
  */
 ep_status ep_nvfp4_matvec(const void *x_bf16, int64_t T, int64_t K,
                           int64_t ld_x, int x_per_slot, const uint8_t *w_rows,

@@ -18,8 +18,9 @@ from .api import (DEFAULT_ALIGNMENT, DEFAULT_SIGN_MASK, RoutePlan, alloc_grouped
                   new_route_workspace, new_status, row_bytes, rows_capacity, swiglu_checkpoint_bytes)
 
 __all__ = ["EP_DEV_ERR_BAD_EXPERT", "EP_DEV_ERR_CAPACITY", "EP_DEV_ERR_DUP_EXPERT", "EP_DEV_ERR_TIMEOUT",
-           "EP_DTYPE_BF16", "EP_DTYPE_F32", "EP_ROUND_RNE", "EP_ROUND_SR", "EpError", "library_path", "lib", "DEFAULT_ALIGNMENT",
-           "DEFAULT_SIGN_MASK", "RoutePlan", "alloc_grouped", "ep_combine", "ep_combine_backward", "ep_mxfp8_colwise", "ep_mxfp8_pack",
+           "EP_DTYPE_BF16", "EP_DTYPE_F32", "EP_ROUND_RNE", "EP_ROUND_SR", "EpError", "library_path", "lib",
+           "DEFAULT_ALIGNMENT", "DEFAULT_SIGN_MASK", "RoutePlan", "alloc_grouped", "ep_combine",
+           "ep_combine_backward", "ep_mxfp8_colwise", "ep_mxfp8_pack",
            "ep_nvfp4_colwise_rht_bf16",
            "ep_nvfp4_direct_receive",
            "ep_nvfp4_dispatch", "ep_nvfp4_matvec", "ep_nvfp4_pack", "ep_nvfp4_pack_weights", "ep_nvfp4_unpack",

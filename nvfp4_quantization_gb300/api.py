@@ -384,8 +384,9 @@ def ep_pack(tokens: torch.Tensor, plan: RoutePlan, rows: torch.Tensor | None = N
         rows = _empty((plan.R_cap, H), tokens.dtype, tokens.device, stream)
     else:
         _need_dense(rows, "rows", (plan.R_cap, H), tokens.dtype)
-    st = _lib.lib().ep_pack(_at(tokens), _DTYPE[tokens.dtype], T, H, ld, _at(plan.dest), plan.k, _at(plan.offsets),
-                            _at(plan.counts), plan.E, _at(rows), plan.R_cap, _at(plan.status), _stream_of(stream, tokens.device))
+    st = _lib.lib().ep_pack(tokens.data_ptr(), _DTYPE[tokens.dtype], T, H, ld, plan.dest.data_ptr(), plan.k,
+                            plan.offsets.data_ptr(), plan.counts.data_ptr(), plan.E, rows.data_ptr(), plan.R_cap,
+                            plan.status.data_ptr(), _stream_of(stream, tokens.device))
     if st:
         check("ep_pack", st)
     return rows
@@ -425,8 +426,8 @@ def ep_combine(rows: torch.Tensor, plan: RoutePlan | None = None, weights: torch
         out = _empty((T, H), rows.dtype, dev, stream)
     else:
         _need_dense(out, "out", (T, H), rows.dtype)
-    st = _lib.lib().ep_combine(_at(rows), _DTYPE[rows.dtype], n, H, ld, _at(index), int(plan is None),
-                               _at(weights), T, k, _at(out), _at(status), _stream_of(stream, dev))
+    st = _lib.lib().ep_combine(rows.data_ptr(), _DTYPE[rows.dtype], n, H, ld, index.data_ptr(), int(plan is None),
+                               _at(weights), T, k, out.data_ptr(), status.data_ptr(), _stream_of(stream, dev))
     if st:
         check("ep_combine", st)
     return out
@@ -461,9 +462,10 @@ def ep_combine_backward(d_out: torch.Tensor, plan: RoutePlan, weights: torch.Ten
         d_rows = _empty((R_cap, H), dt, dev, stream)
     else:
         _need_dense(d_rows, "d_rows", (R_cap, H), dt)
-    st = _lib.lib().ep_combine_backward(_at(d_out), _DTYPE[dt], T, H, ld, _at(rows), ld_rows, _at(plan.dest),
-                                        _at(weights), k, _at(plan.offsets), _at(plan.counts), plan.E,
-                                        _at(d_rows), R_cap, _at(d_weights), _at(plan.status), _stream_of(stream, dev))
+    st = _lib.lib().ep_combine_backward(d_out.data_ptr(), _DTYPE[dt], T, H, ld, _at(rows), ld_rows,
+                                        plan.dest.data_ptr(), _at(weights), k, plan.offsets.data_ptr(),
+                                        plan.counts.data_ptr(), plan.E, d_rows.data_ptr(), R_cap, _at(d_weights), plan.status.data_ptr(),
+                                        _stream_of(stream, dev))
     if st:
         check("ep_combine_backward", st)
     return d_rows, d_weights
@@ -504,8 +506,8 @@ def ep_swiglu(x: torch.Tensor, offsets: torch.Tensor | None = None, E: int = 1, 
     elif checkpoint:
         ckpt = _empty((swiglu_checkpoint_bytes(R_cap, I),), torch.uint8, dev, stream)
     status = _status_or_new(status, dev, stream)
-    st = _lib.lib().ep_swiglu(_at(x), ld, R_cap, I, _at(offsets), E, _at(act), _at(ckpt), _at(status),
-                              _stream_of(stream, dev))
+    st = _lib.lib().ep_swiglu(x.data_ptr(), ld, R_cap, I, _at(offsets), E, act.data_ptr(), _at(ckpt),
+                              status.data_ptr(), _stream_of(stream, dev))
     if st:
         check("ep_swiglu", st)
     return act, ckpt
@@ -538,8 +540,9 @@ def ep_swiglu_backward(d_act: torch.Tensor, ckpt: torch.Tensor, offsets: torch.T
     if expert_amax is not None:
         _need_dense(expert_amax, "expert_amax", (E,), torch.float32)
     status = _status_or_new(status, dev, stream)
-    st = _lib.lib().ep_swiglu_backward(_at(d_act), ld, _at(ckpt), R_cap, I, _at(offsets), E, _at(d_x), _at(act),
-                                       _at(expert_amax), _at(status), _stream_of(stream, dev))
+    st = _lib.lib().ep_swiglu_backward(d_act.data_ptr(), ld, ckpt.data_ptr(), R_cap, I, _at(offsets), E,
+                                       d_x.data_ptr(), _at(act), _at(expert_amax), status.data_ptr(),
+                                       _stream_of(stream, dev))
     if st:
         check("ep_swiglu_backward", st)
     return d_x, act
@@ -600,8 +603,8 @@ def ep_nvfp4_matvec(x: torch.Tensor, w_rows: torch.Tensor, topk_idx: torch.Tenso
     else:
         _need_dense(y, "y", (T * k, N), torch.bfloat16)
     status = _status_or_new(status, dev, stream)
-    st = _lib.lib().ep_nvfp4_matvec(_at(x), T, K, ld, int(n != T), _at(w_rows), E, N, _at(topk_idx), k, _at(y),
-                                    _at(status), _stream_of(stream, dev))
+    st = _lib.lib().ep_nvfp4_matvec(x.data_ptr(), T, K, ld, int(n != T), w_rows.data_ptr(), E, N, _at(topk_idx), k,
+                                    y.data_ptr(), status.data_ptr(), _stream_of(stream, dev))
     if st:
         check("ep_nvfp4_matvec", st)
     return y

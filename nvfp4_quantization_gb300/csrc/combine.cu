@@ -10,6 +10,13 @@
 // slot was dropped).  Every product and sum is FP32 and is rounded once, on
 // the way out; the sum over slots is in slot order and the dot products are
 // reduced in a fixed tree, so results do not depend on scheduling.
+//
+// Bound: HBM; each row, token and gradient passes once, in 16-byte units where
+// the rows allow it, with the loads of all of a token's slots in flight together.
+// Measured on GB300 at 16384 tokens x 7168, BF16: pack, 64 experts top-6 255 us
+// (6.4 TB/s, padding rows not counted), combine, 256 experts top-8 335 us (6.3
+// TB/s), its gradient with the weights' 631 us (6.3 TB/s, 6.7 with the padding
+// rows).
 #include "epq_device.cuh"
 #include "epq_internal.h"
 

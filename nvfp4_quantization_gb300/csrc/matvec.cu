@@ -24,14 +24,23 @@
 //    needed, and x is brought into the order in which the lanes want it.
 //  - the rows come by TMA, 16 rows x 512 elements at a time, into a ring of
 //    each warp's own: a warp waits for nobody but its own copies.
-// What bounds it: with the rows at HBM's rate the conversion and the matrix
-// instruction take about 60 % of the issue slots, so a step's bookkeeping has
-// to be small beside its 32 matrix instructions.
+// What bounds it: HBM, with the conversion, the scaling and the matrix
+// instructions close behind (57 % of the issue slots; without the copies the
+// arithmetic alone takes 0.8 of the time), so a step's bookkeeping has to be
+// small beside its 32 matrix instructions.
 //  - two warps share a tile, each taking every second step of its rows, and one
 //    of them adds the partial sums up.  The warps wait for each other where the
 //    group of slots (and so x) changes, for a tile's time at worst; but every
 //    tile costs two barriers (32 tokens x 8 of 64 experts of 4096 x 4096: 122 us
 //    with one warp a tile, 115 with two, 120 with four, 140 with eight).
+//  - measured and dropped: fragments loaded straight to registers (8 cache
+//    lines a request held the L1 at 80 %: 202 us for the batch above); whole row
+//    blocks by one bulk copy with x in registers and a row split over 16 warps
+//    (their hand-over of partial sums: 159 us); the copies issued by a warp of
+//    their own (17 warps leave 96 registers: 127 us).
+// Measured on GB300, 4096 x 4096 per expert, 64 experts top-8: one token 17.4 us
+// (76 MB, 4.4 TB/s, of which 4 us are the launch, the ids and x), 8 tokens 66 us
+// (5.5 TB/s of the rows in use), 32 tokens 113 us (5.3 TB/s).
 // The order of a row's sum depends on the shape (K, T, E), never on the
 // routing: a slot's result does not depend on where the other slots went.
 #include "epq_device.cuh"
@@ -679,8 +688,9 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
                         const uint4 wh[2] = {lds128(ch + 8 * P::code_pitch), lds128(ch + 8 * P::code_pitch + 16)};
                         if (G == 1) {
                             const uint32_t s = s_one + place + h * (kHalf / 16);
-                            multiply_one(one, wl, wh, lds64(s), lds64(s + 8 * P::scale_pitch), pick,
-                                         [&](int j, int o) { return lds128((o ? x_odd : x_even) + (h * 32 + j * 4) * 16); });
+                            multiply_one(one, wl, wh, lds64(s), lds64(s + 8 * P::scale_pitch), pick, [&](int j, int o) {
+                                return lds128((o ? x_odd : x_even) + (h * 32 + j * 4) * 16);
+                            });
                         } else {
                             const uint32_t s = s_lane + place + h * (kHalf / 16);
                             multiply(acc, wl, wh, lds32(s), lds32(s + 8 * P::scale_pitch),
