@@ -524,11 +524,11 @@ ep_status ep_swiglu_backward(const void *d_act_bf16, int64_t ld_act,
  *                   k = 1, a dense layer.  Unlike in a routing plan, an id may
  *                   repeat within a token.
  *   y_bf16          device bf16 [T*k, N].
- * Any T is accepted; the call is made for batches whose time is the reading
- * of the weights (up to 8 slots of an expert share one pass over its rows, fewer
- * where K is above about 8000).  Weights and block scales enter exactly, x within
- * 2^-39 of its row's largest element; FP32 accumulation, the row scale applied
- * to the sum, one rounding.  A slot's result does not depend on the routing of
+ * T*k up to 2^20 (EP_ERR_CAPACITY above); the call is made for batches whose
+ * time is the reading of the weights (up to 8 slots of an expert share one
+ * pass over its rows, fewer where K is above about 8000).  Weights and block
+ * scales enter exactly, x within 2^-39 of its row's largest element; FP32
+ * accumulation, the row scale applied to the sum, one rounding.  A slot's result does not depend on the routing of
  * the other slots (it may differ in the last bits between batch sizes).
  * An infinity or NaN in x shows in its slot's outputs alone.
  */

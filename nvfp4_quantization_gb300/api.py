@@ -296,6 +296,9 @@ def ep_mxfp8_pack(tokens: torch.Tensor, plan: RoutePlan, buf: torch.Tensor | Non
 # around the expert products: rows without quantisation, combine, activation,
 # products of a few tokens
 # ---------------------------------------------------------------------------
+# With `stream`, outputs and scratch made here belong to that stream; inputs made
+# on another one are the caller's to order (wait_stream) and keep (record_stream).
+#
 # These calls are made for single tokens too, where a call's host time is its
 # time: operands go to the library as plain addresses, and the current stream's
 # handle is read without building a Stream object (3 us of a 10 us call).

@@ -583,6 +583,10 @@ ep_status ep_nvfp4_matvec(const void *x_bf16, int64_t T, int64_t K, int64_t ld_x
     if (!shape_ok(T, K, k, E) || K > 32768 || N < 1 || N > (1 << 20) || !pitch_ok(ld_x, K) ||
         (T > 0 && !topk_idx && (E != 1 || k != 1)))
         return EP_ERR_SHAPE;
+    // every group of slots is looked for among all of them: past this the call
+    // would take seconds, and it is not the call for such batches
+    if (T * (int64_t)k > (1 << 20))
+        return EP_ERR_CAPACITY;
     if (!aligned16(x_bf16) || ld_x % 8 != 0 || !aligned16(w_rows) || !aligned_to(y_bf16, 2))
         return EP_ERR_ALIGN;
     const int dev = device_of(w_rows);

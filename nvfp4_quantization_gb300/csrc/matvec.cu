@@ -244,7 +244,6 @@ struct Shared {
 constexpr int kZeros = 2 * kHalf * 2;
 constexpr int kMaxSmem = 227 * 1024 - (int)sizeof(Shared);
 
-
 // Expert of a slot as the caller gave it, with ids outside [-1, E) as -2.
 __device__ __forceinline__ int read_id(const MatvecArgs &a, int s)
 {
@@ -455,8 +454,8 @@ __device__ __forceinline__ const uint16_t *x_row(const MatvecArgs &a, int s)
 
 // v * scale * 2^-shift, rounded once to FP32 in its normal range: the two
 // scales together may pass that range where the result does not, so the
-// exponents are added as integers and applied in two factors.  (In 64-bit
-// arithmetic this costs the kernel a third of its time.)
+// exponents are added as integers and applied in two factors.  (64-bit
+// arithmetic would say it shorter and is slow here.)
 __device__ __forceinline__ float rescale(float v, float scale, int shift)
 {
     const uint32_t b = f2u(scale);
@@ -788,8 +787,10 @@ template <int G, int HALVES> cudaError_t launch_ring(const LaunchCtx &c, const M
 
 template <int G> cudaError_t launch_group(const LaunchCtx &c, const MatvecArgs &a, size_t x_bytes)
 {
+    // whole steps where two of them fit beside x; half steps, which copy 18 bytes
+    // for 16, take longer (the 32-token batch above: 130 us against 120)
     return ring_depth<2>(G * x_bytes, a.E) >= kMinDepth ? launch_ring<G, 2>(c, a, G * x_bytes)
-                                                   : launch_ring<G, 1>(c, a, G * x_bytes);
+                                                        : launch_ring<G, 1>(c, a, G * x_bytes);
 }
 
 } // namespace

@@ -177,7 +177,7 @@ struct Walk {
         : nu(a.I / 8), cols(cols_), tx(threadIdx.x % cols_), ty(threadIdx.x / cols_), step(kThreads / cols_)
     {
         blocks = (nu + cols - 1) / cols;
-        const int64_t total = (int64_t)((R + step - 1) / step) * blocks;
+        const int64_t total = ((int64_t)R + step - 1) / step * blocks;
         const int64_t from = total * blockIdx.x / gridDim.x;
         left = total * (blockIdx.x + 1) / gridDim.x - from;
         r = (int)(from / blocks) * step + ty;

@@ -157,10 +157,14 @@ def test_combine_backward(T, k, E, H, dt, drop, extra):
     within(d_rows, want, (ulp(d_rows.dtype) + 2 * U) * want.abs() + 2.0 ** -133)
     within(d_w, want_w, 2 * H * U * mag_w)
     assert int(plan.status) == 0
+    # the weights' gradient does not depend on the weights
+    again, d_w2 = nq.ep_combine_backward(d_out, plan, rows=rows, d_rows=torch.full_like(d_rows, 7.0))
+    assert torch.equal(d_w2, d_w)
     # without weights, without the weights' gradient
     ones, none = nq.ep_combine_backward(d_out, plan, d_rows=torch.full_like(d_rows, 7.0))
     assert none is None
     assert torch.equal(ones, nq.ep_pack(d_out, plan, rows=torch.full_like(d_rows, 7.0)))
+    assert torch.equal(again, ones)
 
 
 def test_combine_gradient_against_differences():

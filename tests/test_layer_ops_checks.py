@@ -101,7 +101,7 @@ def _matvec(**kw):
 @pytest.mark.parametrize("kw, status", [
     (dict(x=None), -1), (dict(w=None), -1), (dict(y=None), -1), (dict(st=None), -1), (dict(K=48, ld=48), -2), (dict(K=32800, ld=32800), -2),
     (dict(ld=56), -2), (dict(N=0), -2), (dict(N=(1 << 20) + 1), -2), (dict(tk=None), -2), (dict(tk=None, E=1), -2),
-    (dict(E=0), -2), (dict(k=33), -2), (dict(T=-1), -2), (dict(x=HALF), -3), (dict(w=HALF), -3), (dict(ld=66), -3),
+    (dict(E=0), -2), (dict(k=33), -2), (dict(T=-1), -2), (dict(T=(1 << 19) + 1), -4), (dict(x=HALF), -3), (dict(w=HALF), -3), (dict(ld=66), -3),
     (dict(y=ODD), -3)])
 def test_matvec_refusals(kw, status):
     assert _matvec(**kw) == status
