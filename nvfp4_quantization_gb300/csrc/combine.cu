@@ -11,8 +11,8 @@
 // the way out; the sum over slots is in slot order and the dot products are
 // reduced in a fixed tree, so results do not depend on scheduling.
 //
-// Bound: HBM; each row, token and gradient passes once, in 16-byte units where
-// the rows allow it, with the loads of all of a token's slots in flight together.
+// Bound: HBM; each row, token and gradient passes once, in 16-byte blocks, with
+// the loads of a token's slots in flight together.
 // Measured on GB300 at 16384 tokens x 7168, BF16: pack, 64 experts top-6 255 us
 // (6.4 TB/s, padding rows not counted), combine, 256 experts top-8 335 us (6.3
 // TB/s), its gradient with the weights' 631 us (6.3 TB/s, 6.7 with the padding
@@ -26,73 +26,119 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// What a thread loads and stores at a time, a unit: VEC consecutive elements of
-// type T, 16 bytes where every row starts on 16 bytes and is a whole number of
-// them, else 4, else (BF16 rows of odd length) one element.
-template <int BYTES> struct Raw;
-template <> struct Raw<16> { using type = uint4; };
-template <> struct Raw<4> { using type = uint32_t; };
-template <> struct Raw<2> { using type = uint16_t; };
+// Everything moves in blocks of 16 bytes of a row, E elements of type T.
+template <typename T> constexpr int E = 16 / (int)sizeof(T);
 
-template <typename T, int VEC> using RawOf = typename Raw<(int)sizeof(T) * VEC>::type;
-
-template <typename T, int VEC>
-__device__ __forceinline__ RawOf<T, VEC> load_raw(const T *p)
-{
-    return __ldg(reinterpret_cast<const RawOf<T, VEC> *>(p));
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_raw(T *p, RawOf<T, VEC> v)
-{
-    *reinterpret_cast<RawOf<T, VEC> *>(p) = v;
-}
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return u2f(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return u2f(w & 0xffff0000u); }
-
-__device__ __forceinline__ void unpack_raw(uint4 r, float (&f)[8])
+__device__ __forceinline__ void unpack(uint4 r, float (&f)[8])
 {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
+        f[2 * i] = u2f(w[i] << 16);
+        f[2 * i + 1] = u2f(w[i] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void unpack_raw(uint32_t r, float (&f)[2])
-{
-    f[0] = bf16_lo(r);
-    f[1] = bf16_hi(r);
-}
-__device__ __forceinline__ void unpack_raw(uint16_t r, float (&f)[1]) { f[0] = u2f((uint32_t)r << 16); }
-__device__ __forceinline__ void unpack_raw(uint4 r, float (&f)[4])
+__device__ __forceinline__ void unpack(uint4 r, float (&f)[4])
 {
     f[0] = u2f(r.x);
     f[1] = u2f(r.y);
     f[2] = u2f(r.z);
     f[3] = u2f(r.w);
 }
-__device__ __forceinline__ void unpack_raw(uint32_t r, float (&f)[1]) { f[0] = u2f(r); }
-
-template <typename T, int VEC> __device__ __forceinline__ RawOf<T, VEC> pack_raw(const float (&f)[VEC]);
-template <> __device__ __forceinline__ uint4 pack_raw<uint16_t, 8>(const float (&f)[8])
+__device__ __forceinline__ uint4 pack(const float (&f)[8])
 {
     return make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
 }
-template <> __device__ __forceinline__ uint32_t pack_raw<uint16_t, 2>(const float (&f)[2])
-{
-    return cvt_bf16x2(f[0], f[1]);
-}
-template <> __device__ __forceinline__ uint16_t pack_raw<uint16_t, 1>(const float (&f)[1])
-{
-    return (uint16_t)cvt_bf16x2(f[0], 0.0f);
-}
-template <> __device__ __forceinline__ uint4 pack_raw<float, 4>(const float (&f)[4])
+__device__ __forceinline__ uint4 pack(const float (&f)[4])
 {
     return make_uint4(f2u(f[0]), f2u(f[1]), f2u(f[2]), f2u(f[3]));
 }
-template <> __device__ __forceinline__ uint32_t pack_raw<float, 1>(const float (&f)[1]) { return f2u(f[0]); }
+
+__device__ __forceinline__ uint4 load16(const void *p) { return __ldg(static_cast<const uint4 *>(p)); }
+
+// ---------------------------------------------------------------- rows that start anywhere
+// E elements from any element's address, as the two aligned 16-byte words that
+// hold them (the second is the neighbouring thread's first: it comes from L1)
+// and a shift by a number of bytes that is the same all along a row.  For the
+// blocks at a row's ends the words reach up to 28 bytes before it and 32 after
+// it, into its neighbours; rows that have less of the buffer there (its first
+// and last) are read element by element.
+template <typename T> __device__ __forceinline__ bool inner_row(int64_t row, int64_t rows, int64_t ld)
+{
+    return row * ld * (int)sizeof(T) >= 32 && (rows - 1 - row) * ld * (int)sizeof(T) >= 32;
+}
+
+struct Window {
+    uint4 lo, hi;
+    uint32_t shift;
+};
+
+template <typename T>
+__device__ __forceinline__ Window load_window(const T *p, bool inner, int first, int n)
+{
+    Window w;
+    if (inner) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        w.shift = (uint32_t)at & 15u;
+        const uint4 *q = reinterpret_cast<const uint4 *>(at - w.shift);
+        w.lo = __ldg(q);
+        w.hi = __ldg(q + (w.shift ? 1 : 0));
+    } else {
+        uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < E<T>; ++i)
+            if (i >= first && i < n) {
+                if constexpr (sizeof(T) == 2)
+                    v[i / 2] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+                else
+                    v[i] = f2u(__ldg(p + i));
+            }
+        w.lo = w.hi = make_uint4(v[0], v[1], v[2], v[3]);
+        w.shift = 0;
+    }
+    return w;
+}
+
+__device__ __forceinline__ uint4 value(const Window &w)
+{
+    const uint32_t r = 8 * (w.shift & 3u);
+    auto at = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e) {
+        return make_uint4(__funnelshift_r(a, b, r), __funnelshift_r(b, c, r), __funnelshift_r(c, d, r),
+                          __funnelshift_r(d, e, r));
+    };
+    switch (w.shift >> 2) {
+    case 0: return at(w.lo.x, w.lo.y, w.lo.z, w.lo.w, w.hi.x);
+    case 1: return at(w.lo.y, w.lo.z, w.lo.w, w.hi.x, w.hi.y);
+    case 2: return at(w.lo.z, w.lo.w, w.hi.x, w.hi.y, w.hi.z);
+    default: return at(w.lo.w, w.hi.x, w.hi.y, w.hi.z, w.hi.w);
+    }
+}
+
+// Elements [first, n) of a block to p, which is 16-byte aligned where all of
+// them are there.
+template <typename T>
+__device__ __forceinline__ void store_part(T *p, uint4 v, int first, int n)
+{
+    if (first == 0 && n == E<T>) {
+        *reinterpret_cast<uint4 *>(p) = v;
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < E<T>; ++i)
+        if (i >= first && i < n) {
+            if constexpr (sizeof(T) == 2)
+                p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+            else
+                p[i] = u2f(w[i]);
+        }
+}
+
+// Elements between p and the 16-byte boundary before it.
+template <typename T> __device__ __forceinline__ int before(const T *p)
+{
+    return (int)(reinterpret_cast<uintptr_t>(p) & 15u) / (int)sizeof(T);
+}
 
 // Row of a slot, or -1 for a dropped one; a row outside the buffer is
 // reported and dropped.
@@ -106,45 +152,46 @@ __device__ __forceinline__ int live_row(int d, int R_cap, uint32_t *status)
 }
 
 // ---------------------------------------------------------------- combine
-// One thread per UNR units of a token, a CTA's share of the row side by side;
-// the rows of KCH slots are in flight at once.  Narrow units come several to a
-// thread: with one, too few bytes are in flight (4096 tokens x 4097, top-4,
-// FP32: 115 us; with two 83 us).
-template <typename T, int VEC, int KCH> constexpr int units_in_flight()
+// Rows (as they are given) and weights of KCH slots of a token from slot j0 on.
+template <int KCH>
+__device__ __forceinline__ void read_slots(const CombineArgs &a, int64_t slot0, int j0, int (&d)[KCH], float (&w)[KCH])
 {
-    return sizeof(T) * VEC >= 16 ? (KCH > 2 ? 1 : 2) : sizeof(T) * VEC >= 4 && KCH > 2 ? 2 : 4;
+#pragma unroll
+    for (int j = 0; j < KCH; ++j) {
+        d[j] = -1;
+        w[j] = 1.0f;
+        if (j0 + j < a.k) {
+            const int64_t s = slot0 + j0 + j;
+            d[j] = a.index ? __ldg(a.index + s) : 0;
+            if (a.slot_order && d[j] >= 0)
+                d[j] = (int)s;
+            if (a.weights)
+                w[j] = __ldg(a.weights + s);
+        }
+    }
 }
 
-template <typename T, int VEC, int KCH>
+// Rows of whole 16-byte blocks.  One thread per UNR blocks of a token, a CTA's
+// share of the row side by side; the rows of KCH slots are in flight at once.
+// With two slots, two blocks: one leaves too few bytes in flight (8192 x 4096
+// FP32 top-2: 71 us, with two 59 us; with eight slots two cost 3 %).
+template <typename T, int KCH>
 __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a)
 {
-    constexpr int UNR = units_in_flight<T, VEC, KCH>();
+    constexpr int UNR = KCH > 2 ? 1 : 2;
     pdl_launch_dependents();
     pdl_wait();
     const int64_t t = blockIdx.x;
-    const int c0 = (blockIdx.y * UNR * blockDim.x + threadIdx.x) * VEC, step = blockDim.x * VEC;
+    const int c0 = (blockIdx.y * UNR * blockDim.x + threadIdx.x) * E<T>, step = blockDim.x * E<T>;
     if (c0 >= a.H)
         return;
     const T *rows = static_cast<const T *>(a.rows);
-    const int64_t slot0 = t * a.k;
-    float acc[UNR][VEC] = {};
+    float acc[UNR][E<T>] = {};
     for (int j0 = 0; j0 < a.k; j0 += KCH) {
         int d[KCH];
         float w[KCH];
-#pragma unroll
-        for (int j = 0; j < KCH; ++j) {
-            d[j] = -1;
-            w[j] = 1.0f;
-            if (j0 + j < a.k) {
-                const int64_t s = slot0 + j0 + j;
-                d[j] = a.index ? __ldg(a.index + s) : 0;
-                if (a.slot_order && d[j] >= 0)
-                    d[j] = (int)s;
-                if (a.weights)
-                    w[j] = __ldg(a.weights + s);
-            }
-        }
-        RawOf<T, VEC> raw[KCH][UNR];
+        read_slots<KCH>(a, t * a.k, j0, d, w);
+        uint4 raw[KCH][UNR];
 #pragma unroll
         for (int j = 0; j < KCH; ++j) {
             d[j] = live_row(d[j], a.R_cap, a.status);
@@ -152,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a)
 #pragma unroll
                 for (int u = 0; u < UNR; ++u)
                     if (c0 + u * step < a.H)
-                        raw[j][u] = load_raw<T, VEC>(rows + (int64_t)d[j] * a.ld_rows + c0 + u * step);
+                        raw[j][u] = load16(rows + (int64_t)d[j] * a.ld_rows + c0 + u * step);
             }
         }
 #pragma unroll
@@ -161,10 +208,10 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a)
                 continue;
 #pragma unroll
             for (int u = 0; u < UNR; ++u) {
-                float f[VEC];
-                unpack_raw(raw[j][u], f);
+                float f[E<T>];
+                unpack(raw[j][u], f);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
+                for (int i = 0; i < E<T>; ++i)
                     acc[u][i] = fmaf(w[j], f[i], acc[u][i]);
             }
         }
@@ -172,39 +219,81 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a)
 #pragma unroll
     for (int u = 0; u < UNR; ++u)
         if (c0 + u * step < a.H)
-            store_raw<T, VEC>(static_cast<T *>(a.out) + t * a.H + c0 + u * step, pack_raw<T, VEC>(acc[u]));
+            *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + t * a.H + c0 + u * step) = pack(acc[u]);
+}
+
+// Rows that start anywhere: a thread has one aligned block of the output (part
+// of one at the row's ends) and a window of each row (8192 x 7001 BF16 top-8: 203
+// us; with loads of single elements, four a thread, 356).
+template <typename T, int KCH>
+__global__ void __launch_bounds__(kThreads) combine_any_kernel(CombineArgs a)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t t = blockIdx.x;
+    T *out = static_cast<T *>(a.out) + t * a.H;
+    const int c = (int)(blockIdx.y * blockDim.x + threadIdx.x) * E<T> - before(out);
+    if (c >= a.H)
+        return;
+    const int first = c < 0 ? -c : 0, n = min(E<T>, a.H - c);
+    const T *rows = static_cast<const T *>(a.rows);
+    float acc[E<T>] = {};
+    for (int j0 = 0; j0 < a.k; j0 += KCH) {
+        int d[KCH];
+        float w[KCH];
+        read_slots<KCH>(a, t * a.k, j0, d, w);
+        Window raw[KCH];
+#pragma unroll
+        for (int j = 0; j < KCH; ++j) {
+            d[j] = live_row(d[j], a.R_cap, a.status);
+            if (d[j] >= 0)
+                raw[j] = load_window<T>(rows + (int64_t)d[j] * a.ld_rows + c, inner_row<T>(d[j], a.R_cap, a.ld_rows),
+                                        first, n);
+        }
+#pragma unroll
+        for (int j = 0; j < KCH; ++j) {
+            if (d[j] < 0)
+                continue;
+            float f[E<T>];
+            unpack(value(raw[j]), f);
+#pragma unroll
+            for (int i = 0; i < E<T>; ++i)
+                acc[i] = fmaf(w[j], f[i], acc[i]);
+        }
+    }
+    store_part<T>(out + c, pack(acc), first, n);
 }
 
 // ---------------------------------------------------------------- scatter
 // Zero the padding rows [offsets[e] + counts[e], offsets[e + 1]) of expert
 // e = cta / a.pad_split, every a.pad_split-th row of them.
-template <typename T, int VEC>
+template <typename T>
 __device__ void zero_padding(const ScatterArgs &a, int cta)
 {
     const int e = cta / a.pad_split;
     const int end = __ldg(a.offsets + e + 1);
     T *rows = static_cast<T *>(a.rows_out);
-    const RawOf<T, VEC> zero = {};
     for (int r = __ldg(a.offsets + e) + __ldg(a.counts + e) + cta % a.pad_split; r < end; r += a.pad_split) {
         if (r < 0 || r >= a.R_cap) {
             if (threadIdx.x == 0)
                 raise_status(a.status, kDevErrCapacity);
             return;
         }
-        for (int c = threadIdx.x * VEC; c < a.H; c += blockDim.x * VEC)
-            store_raw<T, VEC>(rows + (int64_t)r * a.H + c, zero);
+        for (int c = threadIdx.x * E<T>; c < a.H; c += blockDim.x * E<T>)
+            *reinterpret_cast<uint4 *>(rows + (int64_t)r * a.H + c) = make_uint4(0, 0, 0, 0);
     }
 }
 
-// One CTA per token; CTAs past the tokens write the padding rows.
-template <typename T, int VEC, int KCH, bool DOT>
+// Rows of whole 16-byte blocks: one CTA per token, which is read once; CTAs
+// past the tokens write the padding rows.
+template <typename T, int KCH, bool DOT>
 __global__ void __launch_bounds__(kThreads) scatter_kernel(ScatterArgs a)
 {
     __shared__ float part[kThreads / 32][KCH];
     pdl_launch_dependents();
     pdl_wait();
     if ((int)blockIdx.x >= a.T) {
-        zero_padding<T, VEC>(a, blockIdx.x - a.T);
+        zero_padding<T>(a, blockIdx.x - a.T);
         return;
     }
     const int64_t t = blockIdx.x;
@@ -226,36 +315,36 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(ScatterArgs a)
                     w[j] = __ldg(a.weights + slot0 + j0 + j);
             }
         }
-        for (int c = threadIdx.x * VEC; c < a.H; c += blockDim.x * VEC) {
-            const RawOf<T, VEC> raw = load_raw<T, VEC>(src + c);
-            RawOf<T, VEC> in[KCH];
+        for (int c = threadIdx.x * E<T>; c < a.H; c += blockDim.x * E<T>) {
+            const uint4 raw = load16(src + c);
+            uint4 in[KCH];
             if (DOT) {
 #pragma unroll
                 for (int j = 0; j < KCH; ++j)
                     if (d[j] >= 0)
-                        in[j] = load_raw<T, VEC>(rows_in + (int64_t)d[j] * a.ld_in + c);
+                        in[j] = load16(rows_in + (int64_t)d[j] * a.ld_in + c);
             }
-            float f[VEC];
-            unpack_raw(raw, f);
+            float f[E<T>];
+            unpack(raw, f);
 #pragma unroll
             for (int j = 0; j < KCH; ++j) {
                 if (d[j] < 0)
                     continue;
-                T *to = rows_out + (int64_t)d[j] * a.H + c;
+                uint4 *to = reinterpret_cast<uint4 *>(rows_out + (int64_t)d[j] * a.H + c);
                 if (a.weights) {
-                    float o[VEC];
+                    float o[E<T>];
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
+                    for (int i = 0; i < E<T>; ++i)
                         o[i] = w[j] * f[i];
-                    store_raw<T, VEC>(to, pack_raw<T, VEC>(o));
+                    *to = pack(o);
                 } else {
-                    store_raw<T, VEC>(to, raw);
+                    *to = raw;
                 }
                 if (DOT) {
-                    float g[VEC];
-                    unpack_raw(in[j], g);
+                    float g[E<T>];
+                    unpack(in[j], g);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
+                    for (int i = 0; i < E<T>; ++i)
                         dot[j] = fmaf(f[i], g[i], dot[j]);
                 }
             }
@@ -282,46 +371,165 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(ScatterArgs a)
     }
 }
 
-bool multiple_of(const void *p, int64_t ld, int64_t H, int elem, int bytes)
+// The same for rows that start anywhere: an expert's padding rows lie together,
+// and a CTA zeroes a share of their elements.
+template <typename T>
+__device__ void zero_padding_any(const ScatterArgs &a, int cta)
 {
-    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * elem) % bytes == 0 && (H * elem) % bytes == 0;
+    const int e = cta / a.pad_split, part = cta % a.pad_split;
+    const int64_t row0 = (int64_t)__ldg(a.offsets + e) + __ldg(a.counts + e);
+    int64_t row1 = __ldg(a.offsets + e + 1);
+    if (row1 > a.R_cap || row0 < 0) {
+        if (threadIdx.x == 0)
+            raise_status(a.status, kDevErrCapacity);
+        row1 = min(row1, (int64_t)a.R_cap);
+    }
+    if (row0 < 0 || row0 >= row1)
+        return;
+    const int64_t all = (row1 - row0) * a.H;
+    T *p = static_cast<T *>(a.rows_out) + row0 * a.H + all * part / a.pad_split;
+    T *end = static_cast<T *>(a.rows_out) + row0 * a.H + all * (part + 1) / a.pad_split;
+    const int head = (int)min((int64_t)((E<T> - before(p)) % E<T>), (int64_t)(end - p));
+    if ((int)threadIdx.x < head)
+        p[threadIdx.x] = T(0);
+    p += head;
+    const int64_t blocks = (end - p) / E<T>;
+    for (int64_t b = threadIdx.x; b < blocks; b += blockDim.x)
+        reinterpret_cast<uint4 *>(p)[b] = make_uint4(0, 0, 0, 0);
+    p += blocks * E<T>;
+    if (p + threadIdx.x < end)
+        p[threadIdx.x] = T(0);
 }
 
-// Threads for a row of `units` loads: the fewest whole warps that take it in
-// the same number of passes as kThreads would.
+// Rows that start anywhere: one warp per slot, because each of a token's rows
+// wants the token at another shift; the token is read k times, from L1 and L2
+// after the first.  A lane has U aligned blocks of the row (parts of one at its
+// ends) and the windows that belong to them in flight (with two windows a block,
+// two blocks of BF16: 8192 x 7001 top-6 296 us, with one 314; one of FP32: 1021
+// x 1001 top-5 14.9 us, with two 18.1).
+template <typename T, bool DOT>
+__global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
+{
+    constexpr int U = !DOT ? 4 : sizeof(T) == 2 ? 2 : 1, kWarps = kThreads / 32;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t slots = (int64_t)a.T * a.k;
+    const int slot_ctas = (int)((slots + kWarps - 1) / kWarps);
+    if ((int)blockIdx.x >= slot_ctas) {
+        zero_padding_any<T>(a, blockIdx.x - slot_ctas);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const int64_t s = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (s >= slots)
+        return;
+    const int d = live_row(__ldg(a.dest + s), a.R_cap, a.status);
+    float dot = 0.0f;
+    if (d >= 0) {
+        const int64_t t = s / a.k;
+        const float w = a.weights ? __ldg(a.weights + s) : 1.0f;
+        const T *src = static_cast<const T *>(a.src) + t * a.ld_src;
+        const T *in = DOT ? static_cast<const T *>(a.rows_in) + (int64_t)d * a.ld_in : nullptr;
+        T *to = static_cast<T *>(a.rows_out) + (int64_t)d * a.H;
+        const bool src_inner = inner_row<T>(t, a.T, a.ld_src), in_inner = DOT && inner_row<T>(d, a.R_cap, a.ld_in);
+        for (int c0 = lane * E<T> - before(to); c0 < a.H; c0 += 32 * U * E<T>) {
+            Window x[U], y[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * 32 * E<T>;
+                if (c >= a.H)
+                    break;
+                const int first = c < 0 ? -c : 0, n = min(E<T>, a.H - c);
+                x[u] = load_window<T>(src + c, src_inner, first, n);
+                if (DOT)
+                    y[u] = load_window<T>(in + c, in_inner, first, n);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * 32 * E<T>;
+                if (c >= a.H)
+                    break;
+                const int first = c < 0 ? -c : 0, n = min(E<T>, a.H - c);
+                const uint4 raw = value(x[u]);
+                float f[E<T>];
+                unpack(raw, f);
+                if (a.weights) {
+                    float o[E<T>];
+#pragma unroll
+                    for (int i = 0; i < E<T>; ++i)
+                        o[i] = w * f[i];
+                    store_part<T>(to + c, pack(o), first, n);
+                } else {
+                    store_part<T>(to + c, raw, first, n);
+                }
+                if (DOT) {
+                    float g[E<T>];
+                    unpack(value(y[u]), g);
+#pragma unroll
+                    for (int i = 0; i < E<T>; ++i)
+                        if (i >= first && i < n)
+                            dot = fmaf(f[i], g[i], dot);
+                }
+            }
+        }
+    }
+    if (DOT) {
+        for (int o = 16; o; o >>= 1)
+            dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0)
+            a.d_weights[s] = dot;
+    }
+}
+
+// Every row starts on 16 bytes and is a whole number of them.
+bool in_blocks(const void *p, int64_t ld, int64_t H, int elem)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * elem) % 16 == 0 && (H * elem) % 16 == 0;
+}
+
+// Threads for `units` of work side by side: the fewest whole warps that take
+// them in the same number of CTAs as kThreads would.
 int block_of(int64_t units)
 {
     const int64_t passes = (units + kThreads - 1) / kThreads;
     return (int)(((units + passes - 1) / passes + 31) / 32 * 32);
 }
 
-template <typename T, int VEC, int KCH> cudaError_t combine_slots(const LaunchCtx &c, const CombineArgs &a)
+template <typename T, int KCH> cudaError_t combine_slots(const LaunchCtx &c, const CombineArgs &a, bool blocks)
 {
-    const int64_t units = (a.H + VEC - 1) / VEC;
-    const int64_t shares = (units + units_in_flight<T, VEC, KCH>() - 1) / units_in_flight<T, VEC, KCH>();
-    const int block = block_of(shares);
-    const dim3 grid((unsigned)a.T, (unsigned)((shares + block - 1) / block));
-    return launch_pdl(combine_kernel<T, VEC, KCH>, grid, dim3(block), 0, c.stream, a);
+    constexpr int UNR = KCH > 2 ? 1 : 2;
+    // (a row that starts inside a block has up to one block more)
+    const int64_t n = blocks ? (a.H / E<T> + UNR - 1) / UNR : (a.H + 2 * E<T> - 2) / E<T>;
+    const int block = block_of(n);
+    const dim3 grid((unsigned)a.T, (unsigned)((n + block - 1) / block));
+    return blocks ? launch_pdl(combine_kernel<T, KCH>, grid, dim3(block), 0, c.stream, a)
+                  : launch_pdl(combine_any_kernel<T, KCH == 8 ? E<T> / 2 : KCH>, grid, dim3(block), 0, c.stream, a);
 }
 
-template <typename T, int VEC> cudaError_t combine_vec(const LaunchCtx &c, const CombineArgs &a)
+template <typename T> cudaError_t combine_type(const LaunchCtx &c, const CombineArgs &a)
 {
-    return a.k <= 2 ? combine_slots<T, VEC, 2>(c, a) : combine_slots<T, VEC, 8>(c, a);
+    const bool blocks = in_blocks(a.rows, a.ld_rows, a.H, sizeof(T)) && in_blocks(a.out, a.H, a.H, sizeof(T));
+    return a.k <= 2 ? combine_slots<T, 2>(c, a, blocks) : combine_slots<T, 8>(c, a, blocks);
 }
 
-template <typename T, int VEC, bool DOT> cudaError_t scatter_vec(const LaunchCtx &c, ScatterArgs a)
+template <typename T, bool DOT> cudaError_t scatter_type(const LaunchCtx &c, ScatterArgs a)
 {
-    const int64_t units = (a.H + VEC - 1) / VEC;
-    const int block = (int)(units >= kThreads ? kThreads : (units + 31) / 32 * 32);
     a.pad_split = a.E >= 256 ? 8 : 32;
-    const dim3 grid((unsigned)(a.T + a.E * a.pad_split));
-    return a.k <= 2 ? launch_pdl(scatter_kernel<T, VEC, 2, DOT>, grid, dim3(block), 0, c.stream, a)
-                    : launch_pdl(scatter_kernel<T, VEC, 8, DOT>, grid, dim3(block), 0, c.stream, a);
+    const unsigned pad = (unsigned)(a.E * a.pad_split);
+    if (!(in_blocks(a.src, a.ld_src, a.H, sizeof(T)) && in_blocks(a.rows_out, a.H, a.H, sizeof(T)) &&
+          in_blocks(a.rows_in, a.rows_in ? a.ld_in : 0, a.H, sizeof(T)))) {
+        const unsigned ctas = (unsigned)(((int64_t)a.T * a.k + kThreads / 32 - 1) / (kThreads / 32));
+        return launch_pdl(scatter_any_kernel<T, DOT>, dim3(ctas + pad), dim3(kThreads), 0, c.stream, a);
+    }
+    const int64_t units = a.H / E<T>;
+    const int block = (int)(units >= kThreads ? kThreads : (units + 31) / 32 * 32);
+    return a.k <= 2 ? launch_pdl(scatter_kernel<T, 2, DOT>, dim3((unsigned)a.T + pad), dim3(block), 0, c.stream, a)
+                    : launch_pdl(scatter_kernel<T, 8, DOT>, dim3((unsigned)a.T + pad), dim3(block), 0, c.stream, a);
 }
 
-template <typename T, int VEC> cudaError_t scatter_dot(const LaunchCtx &c, const ScatterArgs &a)
+template <typename T> cudaError_t scatter_dot(const LaunchCtx &c, const ScatterArgs &a)
 {
-    return a.d_weights ? scatter_vec<T, VEC, true>(c, a) : scatter_vec<T, VEC, false>(c, a);
+    return a.d_weights ? scatter_type<T, true>(c, a) : scatter_type<T, false>(c, a);
 }
 
 } // namespace
@@ -330,29 +538,12 @@ cudaError_t launch_combine(const LaunchCtx &c, const CombineArgs &a, int dtype)
 {
     if (a.T == 0)
         return cudaSuccess;
-    const int elem = dtype == kF32 ? 4 : 2;
-    auto fits = [&](int bytes) {
-        return multiple_of(a.rows, a.ld_rows, a.H, elem, bytes) && multiple_of(a.out, a.H, a.H, elem, bytes);
-    };
-    if (dtype == kF32)
-        return fits(16) ? combine_vec<float, 4>(c, a) : combine_vec<float, 1>(c, a);
-    return fits(16)  ? combine_vec<uint16_t, 8>(c, a)
-           : fits(4) ? combine_vec<uint16_t, 2>(c, a)
-                     : combine_vec<uint16_t, 1>(c, a);
+    return dtype == kF32 ? combine_type<float>(c, a) : combine_type<uint16_t>(c, a);
 }
 
 cudaError_t launch_scatter(const LaunchCtx &c, const ScatterArgs &a, int dtype)
 {
-    const int elem = dtype == kF32 ? 4 : 2;
-    auto fits = [&](int bytes) {
-        return multiple_of(a.src, a.ld_src, a.H, elem, bytes) && multiple_of(a.rows_out, a.H, a.H, elem, bytes) &&
-               multiple_of(a.rows_in, a.rows_in ? a.ld_in : 0, a.H, elem, bytes);
-    };
-    if (dtype == kF32)
-        return fits(16) ? scatter_dot<float, 4>(c, a) : scatter_dot<float, 1>(c, a);
-    return fits(16)  ? scatter_dot<uint16_t, 8>(c, a)
-           : fits(4) ? scatter_dot<uint16_t, 2>(c, a)
-                     : scatter_dot<uint16_t, 1>(c, a);
+    return dtype == kF32 ? scatter_dot<float>(c, a) : scatter_dot<uint16_t>(c, a);
 }
 
 } // namespace epq
