@@ -401,26 +401,28 @@ __device__ void zero_padding_any(const ScatterArgs &a, int cta)
         p[threadIdx.x] = T(0);
 }
 
-// Rows that start anywhere: one warp per slot, because each of a token's rows
+// Rows that start anywhere: one warp per slot (a CTA's W = 8 where slots are
+// few: 96 slots of 3993 FP32 took 20 us on one warp each), because each of a token's rows
 // wants the token at another shift; the token is read k times, from L1 and L2
 // after the first.  A lane has U aligned blocks of the row (parts of one at its
 // ends) and the windows that belong to them in flight (with two windows a block,
 // two blocks of BF16: 8192 x 7001 top-6 296 us, with one 314; one of FP32: 1021
 // x 1001 top-5 14.9 us, with two 18.1).
-template <typename T, bool DOT>
+template <typename T, bool DOT, int W>
 __global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
 {
-    constexpr int U = !DOT ? 4 : sizeof(T) == 2 ? 2 : 1, kWarps = kThreads / 32;
+    constexpr int U = !DOT ? 4 : sizeof(T) == 2 ? 2 : 1, kSlots = kThreads / 32 / W;
+    __shared__ float part[W];
     pdl_launch_dependents();
     pdl_wait();
     const int64_t slots = (int64_t)a.T * a.k;
-    const int slot_ctas = (int)((slots + kWarps - 1) / kWarps);
+    const int slot_ctas = (int)((slots + kSlots - 1) / kSlots);
     if ((int)blockIdx.x >= slot_ctas) {
         zero_padding_any<T>(a, blockIdx.x - slot_ctas);
         return;
     }
-    const int lane = threadIdx.x & 31;
-    const int64_t s = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x % (32 * W);
+    const int64_t s = (int64_t)blockIdx.x * kSlots + threadIdx.x / (32 * W);
     if (s >= slots)
         return;
     const int d = live_row(__ldg(a.dest + s), a.R_cap, a.status);
@@ -432,11 +434,11 @@ __global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
         const T *in = DOT ? static_cast<const T *>(a.rows_in) + (int64_t)d * a.ld_in : nullptr;
         T *to = static_cast<T *>(a.rows_out) + (int64_t)d * a.H;
         const bool src_inner = inner_row<T>(t, a.T, a.ld_src), in_inner = DOT && inner_row<T>(d, a.R_cap, a.ld_in);
-        for (int c0 = lane * E<T> - before(to); c0 < a.H; c0 += 32 * U * E<T>) {
+        for (int c0 = lane * E<T> - before(to); c0 < a.H; c0 += 32 * W * U * E<T>) {
             Window x[U], y[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * 32 * E<T>;
+                const int c = c0 + u * 32 * W * E<T>;
                 if (c >= a.H)
                     break;
                 const int first = c < 0 ? -c : 0, n = min(E<T>, a.H - c);
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * 32 * E<T>;
+                const int c = c0 + u * 32 * W * E<T>;
                 if (c >= a.H)
                     break;
                 const int first = c < 0 ? -c : 0, n = min(E<T>, a.H - c);
@@ -476,6 +478,14 @@ __global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
     if (DOT) {
         for (int o = 16; o; o >>= 1)
             dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (W > 1) {                    // (the whole CTA has this slot)
+            if ((lane & 31) == 0)
+                part[lane / 32] = dot;
+            __syncthreads();
+            dot = 0.0f;
+            for (int i = 0; i < W; ++i)
+                dot += part[i];
+        }
         if (lane == 0)
             a.d_weights[s] = dot;
     }
@@ -518,8 +528,13 @@ template <typename T, bool DOT> cudaError_t scatter_type(const LaunchCtx &c, Sca
     const unsigned pad = (unsigned)(a.E * a.pad_split);
     if (!(in_blocks(a.src, a.ld_src, a.H, sizeof(T)) && in_blocks(a.rows_out, a.H, a.H, sizeof(T)) &&
           in_blocks(a.rows_in, a.rows_in ? a.ld_in : 0, a.H, sizeof(T)))) {
-        const unsigned ctas = (unsigned)(((int64_t)a.T * a.k + kThreads / 32 - 1) / (kThreads / 32));
-        return launch_pdl(scatter_any_kernel<T, DOT>, dim3(ctas + pad), dim3(kThreads), 0, c.stream, a);
+        const int64_t slots = (int64_t)a.T * a.k;
+        const int warps = kThreads / 32;
+        if (slots < (int64_t)c.num_sms * 2 * warps)
+            return launch_pdl(scatter_any_kernel<T, DOT, kThreads / 32>, dim3((unsigned)slots + pad), dim3(kThreads), 0,
+                              c.stream, a);
+        return launch_pdl(scatter_any_kernel<T, DOT, 1>, dim3((unsigned)((slots + warps - 1) / warps) + pad),
+                          dim3(kThreads), 0, c.stream, a);
     }
     const int64_t units = a.H / E<T>;
     const int block = (int)(units >= kThreads ? kThreads : (units + 31) / 32 * 32);
