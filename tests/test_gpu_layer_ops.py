@@ -167,6 +167,59 @@ def test_combine_backward(T, k, E, H, dt, drop, extra):
     assert torch.equal(again, ones)
 
 
+def inside(rows, cols, dtype, offset, fill):
+    """A contiguous [rows, cols] view that starts `offset` elements into a buffer
+    of canaries, and that buffer."""
+    buf = torch.full((offset + rows * cols + 64,), fill, dtype=dtype, device="cuda")
+    return buf[offset: offset + rows * cols].view(rows, cols), buf
+
+
+@pytest.mark.parametrize("offset", [0, 1, 3, 5])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [1, 7, 8, 9, 24, 331, 1000, 4099])
+def test_rows_that_start_anywhere(H, dt, offset):
+    """Buffers at every alignment of an element: the values, and nothing written
+    beside the outputs."""
+    dtype, g = TYPES[dt], gen(20 + offset)
+    T, k, E = 21, 3, 5
+    topk = route(T, k, E, g, 0.2)
+    plan = nq.ep_route_plan(topk, E)
+    d = dest_of(plan)
+    live = d >= 0
+    R = int(plan.offsets[-1])
+    tok = inside(T, H, dtype, offset, 9.0)[0]
+    tok.copy_(torch.randn(T, H, generator=g, device="cuda"))
+    rows, buf = inside(plan.R_cap, H, dtype, (offset * 3) % 8, 7.0)
+    nq.ep_pack(tok, plan, rows=rows)
+    want = torch.full_like(rows, 7.0)
+    want[:R] = 0
+    for j in range(k):
+        want[d[live[:, j], j]] = tok[live[:, j]]
+    assert torch.equal(rows, want)
+    first = (offset * 3) % 8
+    assert (buf[:first] == 7.0).all() and (buf[first + rows.numel():] == 7.0).all()
+    rows[:R] = torch.randn(R, H, generator=g, device="cuda").to(dtype)
+    weights = torch.randn(T, k, generator=g, device="cuda")
+    out, buf = inside(T, H, dtype, (offset * 5) % 8, 7.0)
+    nq.ep_combine(rows, plan, weights, out=out)
+    sums, mag = combine64(rows, d, live, weights)
+    within(out, sums, ulp(dtype) * sums.abs() * (1 + B) + 2 * k * U * mag + 2.0 ** -133)
+    first = (offset * 5) % 8
+    assert (buf[:first] == 7.0).all() and (buf[first + out.numel():] == 7.0).all()
+    d_rows, buf = inside(plan.R_cap, H, dtype, (offset * 7) % 8, 7.0)
+    _, d_w = nq.ep_combine_backward(tok, plan, weights, rows=rows, d_rows=d_rows)
+    first = (offset * 7) % 8
+    assert (buf[:first] == 7.0).all() and (buf[first + d_rows.numel():] == 7.0).all()
+    assert (d_rows[R:] == 7.0).all()
+    for j in range(k):
+        t = live[:, j].nonzero().reshape(-1)
+        v = tok[t].double() * weights[t, j].double().unsqueeze(1)
+        within(d_rows[d[t, j]], v, (ulp(dtype) + 2 * U) * v.abs() + 2.0 ** -133)
+        p = tok[t].double() * rows[d[t, j]].double()
+        within(d_w[t, j], p.sum(1), 2 * H * U * p.abs().sum(1))
+    assert not d_w[~live].any()
+
+
 def test_combine_gradient_against_differences():
     """Central differences of L = <v, combine(rows, w)> in 64 bits along random
     directions; L is bilinear, so only the gradients' own rounding is left."""
