@@ -32,7 +32,13 @@
 //    of them adds the partial sums up.  The warps wait for each other where the
 //    group of slots (and so x) changes, for a tile's time at worst; but every
 //    tile costs two barriers (32 tokens x 8 of 64 experts of 4096 x 4096: 122 us
-//    with one warp a tile, 115 with two, 120 with four, 140 with eight).
+//    with one warp a tile, 115 with two, 120 with four, 140 with eight).  Where
+//    there are not enough tiles for all teams, up to 16 share one (21 tokens x
+//    121 outputs of 3936: 11 -> 7 us).
+//  - x is staged with each thread on one slot, and in an order without bank
+//    conflicts: with every thread on all slots it held the group changes back
+//    (the batch above: 115 -> 110 us; 19 tokens x 6 of 13 experts of 404 x 128:
+//    15 -> 9 us).
 //  - measured and dropped: fragments loaded straight to registers (8 cache
 //    lines a request held the L1 at 80 %: 202 us for the batch above); whole row
 //    blocks by one bulk copy with x in registers and a row split over 16 warps
@@ -40,7 +46,7 @@
 //    their own (17 warps leave 96 registers: 127 us).
 // Measured on GB300, 4096 x 4096 per expert, 64 experts top-8: one token 17.4 us
 // (76 MB, 4.4 TB/s, of which 4 us are the launch, the ids and x), 8 tokens 66 us
-// (5.5 TB/s of the rows in use), 32 tokens 113 us (5.3 TB/s).
+// (5.5 TB/s of the rows in use), 32 tokens 110 us (5.5 TB/s).
 // The order of a row's sum depends on the shape (K, T, E), never on the
 // routing: a slot's result does not depend on where the other slots went.
 #include "epq_device.cuh"
@@ -58,7 +64,7 @@ constexpr int kMaxDepth = 3;     // steps in flight per warp, at most ...
 constexpr int kMinDepth = 2;     // ... and at least
 constexpr int kMaxE = 1024;
 constexpr int kIds = 512;        // slots whose expert is kept in shared memory
-constexpr int kMaxParts = 2;     // warps that share a tile, at most
+constexpr int kMaxParts = 2;     // warps that share a tile, where tiles are many
 
 // One word of eight E2M1 codes -> four f16 pairs (exact).
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4])
@@ -501,44 +507,54 @@ __device__ __forceinline__ int expert_of_group(const int *first, int E, int grou
 // x of the group's m slots -> f16 in shared memory: elements 8q .. 8q + 7 of
 // slot c at 16-byte place (((q / 32) * 8 + q % 8) * G + c) * 4 + (q / 8) % 4,
 // which is where lane (c, t) looks for word q % 8 of its 64 elements of half
-// step q / 32 (eight neighbouring lanes: 128 neighbouring bytes).
+// step q / 32 (eight neighbouring lanes: 128 neighbouring bytes).  kThreads / G
+// threads have a slot; a warp's lanes take the 32 places of a half step in an
+// order in which four neighbours write 64 neighbouring bytes.
 template <int G>
 __device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, uint4 *xs, int halves)
 {
-    const int nq = a.K / 8;
-    const uint4 *x[G];
-    uint32_t top[G];
+    constexpr int kSpan = kThreads / G, kKeep = G;
+    const int nq = a.K / 8, c = threadIdx.x / kSpan, l = threadIdx.x & 31;
+    const int q0 = (threadIdx.x % kSpan & ~31) + (l & 3) * 8 + (l >> 2);
+    const uint4 *x = reinterpret_cast<const uint4 *>(x_row(a, sh.slot[c < m ? c : 0]));
+    const bool here = c < m, once = nq <= kKeep * kSpan;    // once: what was read is kept
+    uint4 kept[kKeep];
+    uint32_t top = 0;
+    if (here) {
 #pragma unroll
-    for (int c = 0; c < G; ++c) {
-        x[c] = reinterpret_cast<const uint4 *>(x_row(a, sh.slot[c < m ? c : 0]));
-        top[c] = 0;
-    }
-    const bool once = nq <= kThreads;   // a thread has eight elements of a slot, and keeps them
-    uint4 kept[G];
-    for (int q = threadIdx.x; q < nq; q += kThreads) {
-#pragma unroll
-        for (int c = 0; c < G; ++c) {
-            if (c < m) {
-                kept[c] = __ldg(x[c] + q);
-                top[c] = finite_absmax(top[c], kept[c]);
-            }
+        for (int i = 0; i < kKeep; ++i) {
+            kept[i] = make_uint4(0, 0, 0, 0);
+            if (i * kSpan < nq && q0 + i * kSpan < nq)
+                kept[i] = __ldg(x + q0 + i * kSpan);
         }
-    }
 #pragma unroll
-    for (int c = 0; c < G; ++c) {
-        const uint32_t w = __reduce_max_sync(0xffffffffu, top[c]);
-        if (c < m && (threadIdx.x & 31) == 0 && w)
-            atomicMax(&sh.top[c], w);
+        for (int i = 0; i < kKeep; ++i) {
+            if (i * kSpan >= nq)
+                break;
+            top = finite_absmax(top, kept[i]);
+        }
+        for (int q = q0 + kKeep * kSpan; q < nq; q += kSpan)
+            top = finite_absmax(top, __ldg(x + q));
     }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (l == 0 && top)
+        atomicMax(&sh.top[c], top);
     __syncthreads();
-#pragma unroll
-    for (int c = 0; c < G; ++c) {
-        if (c >= m)
-            break;
+    if (here) {
         const int shift = x_shift(sh.top[c]);
-        for (int q = threadIdx.x; q < halves * 32; q += kThreads)
-            xs[(((q >> 5) * 8 + (q & 7)) * G + c) * 4 + ((q >> 3) & 3)] =
-                q < nq ? to_f16(once ? kept[c] : __ldg(x[c] + q), shift) : make_uint4(0, 0, 0, 0);
+        auto put = [&](int q, uint4 v) {
+            xs[(((q >> 5) * 8 + (q & 7)) * G + c) * 4 + ((q >> 3) & 3)] = to_f16(v, shift);
+        };
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            if (i * kSpan >= halves * 32)
+                break;
+            if (q0 + i * kSpan < halves * 32)
+                put(q0 + i * kSpan, kept[i]);               // (zeros past K)
+        }
+        if (!once)
+            for (int q = q0 + kKeep * kSpan; q < halves * 32; q += kSpan)
+                put(q, q < nq ? __ldg(x + q) : make_uint4(0, 0, 0, 0));
     }
 }
 
@@ -777,8 +793,13 @@ template <int G, int HALVES> cudaError_t launch_ring(const LaunchCtx &c, const M
         !make_map(&scales, a.w + a.K / 2, (uint64_t)a.K / 16, rows, (uint64_t)a.S, P::scale_pitch, kTile))
         return cudaErrorInvalidValue;
     const int steps = (a.K + HALVES * kHalf - 1) / (HALVES * kHalf);
+    // more warps a tile where there is less than a tile for every team at most
+    const int64_t slots = (int64_t)a.T * a.k;
+    const int64_t groups = slots < a.E + slots / G ? slots : a.E + slots / G;
+    const int64_t tiles = groups * ((a.N + kTile - 1) / kTile);
     int parts = 1;
-    while (2 * parts <= kMaxParts && 2 * parts <= steps)
+    while (2 * parts <= steps && (2 * parts <= kMaxParts ||
+                                  (2 * parts <= kWarps && tiles * 2 * parts <= (int64_t)c.num_sms * kWarps)))
         parts *= 2;
     return launch_pdl(matvec_kernel<G, HALVES>, dim3((unsigned)c.num_sms), dim3(kThreads),
                       (size_t)kWarps * depth * P::bytes + x_bytes + sizeof(int) * (size_t)(a.E + 1), c.stream, codes,
