@@ -140,6 +140,15 @@ template <typename T> __device__ __forceinline__ int before(const T *p)
     return (int)(reinterpret_cast<uintptr_t>(p) & 15u) / (int)sizeof(T);
 }
 
+// A CTA's token.  SHORT: blockDim.y tokens a CTA, for rows that leave most of
+// one's threads idle (16121 tokens x 192, top-1: 19 us with a CTA of a warp each,
+// 6 with eight tokens a CTA).  Kept apart because a token that is the same for
+// the whole CTA costs a fifth of the registers less.
+template <bool SHORT> __device__ __forceinline__ int64_t token_of()
+{
+    return SHORT ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : (int64_t)blockIdx.x;
+}
+
 // Row of a slot, or -1 for a dropped one; a row outside the buffer is
 // reported and dropped.
 __device__ __forceinline__ int live_row(int d, int R_cap, uint32_t *status)
@@ -175,15 +184,15 @@ __device__ __forceinline__ void read_slots(const CombineArgs &a, int64_t slot0, 
 // share of the row side by side; the rows of KCH slots are in flight at once.
 // With two slots, two blocks: one leaves too few bytes in flight (8192 x 4096
 // FP32 top-2: 71 us, with two 59 us; with eight slots two cost 3 %).
-template <typename T, int KCH>
+template <typename T, int KCH, bool SHORT>
 __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a)
 {
     constexpr int UNR = KCH > 2 ? 1 : 2;
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t t = blockIdx.x;
+    const int64_t t = token_of<SHORT>();
     const int c0 = (blockIdx.y * UNR * blockDim.x + threadIdx.x) * E<T>, step = blockDim.x * E<T>;
-    if (c0 >= a.H)
+    if ((SHORT && t >= a.T) || c0 >= a.H)
         return;
     const T *rows = static_cast<const T *>(a.rows);
     float acc[UNR][E<T>] = {};
@@ -225,12 +234,14 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a)
 // Rows that start anywhere: a thread has one aligned block of the output (part
 // of one at the row's ends) and a window of each row (8192 x 7001 BF16 top-8: 203
 // us; with loads of single elements, four a thread, 356).
-template <typename T, int KCH>
+template <typename T, int KCH, bool SHORT>
 __global__ void __launch_bounds__(kThreads) combine_any_kernel(CombineArgs a)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t t = blockIdx.x;
+    const int64_t t = token_of<SHORT>();
+    if (SHORT && t >= a.T)
+        return;
     T *out = static_cast<T *>(a.out) + t * a.H;
     const int c = (int)(blockIdx.y * blockDim.x + threadIdx.x) * E<T> - before(out);
     if (c >= a.H)
@@ -266,14 +277,16 @@ __global__ void __launch_bounds__(kThreads) combine_any_kernel(CombineArgs a)
 
 // ---------------------------------------------------------------- scatter
 // Zero the padding rows [offsets[e] + counts[e], offsets[e + 1]) of expert
-// e = cta / a.pad_split, every a.pad_split-th row of them.
-template <typename T>
+// e = cta / a.pad_split, every a.pad_split-th row of them (and of those, if
+// SHORT, this threadIdx.y's).
+template <typename T, bool SHORT>
 __device__ void zero_padding(const ScatterArgs &a, int cta)
 {
     const int e = cta / a.pad_split;
     const int end = __ldg(a.offsets + e + 1);
     T *rows = static_cast<T *>(a.rows_out);
-    for (int r = __ldg(a.offsets + e) + __ldg(a.counts + e) + cta % a.pad_split; r < end; r += a.pad_split) {
+    const int first = __ldg(a.offsets + e) + __ldg(a.counts + e) + (SHORT ? (int)threadIdx.y * a.pad_split : 0);
+    for (int r = first + cta % a.pad_split; r < end; r += SHORT ? a.pad_split * (int)blockDim.y : a.pad_split) {
         if (r < 0 || r >= a.R_cap) {
             if (threadIdx.x == 0)
                 raise_status(a.status, kDevErrCapacity);
@@ -284,19 +297,21 @@ __device__ void zero_padding(const ScatterArgs &a, int cta)
     }
 }
 
-// Rows of whole 16-byte blocks: one CTA per token, which is read once; CTAs
-// past the tokens write the padding rows.
-template <typename T, int KCH, bool DOT>
+// Rows of whole 16-byte blocks: a token (SHORT: blockDim.y of them) a CTA, read
+// once by its blockDim.x threads; CTAs past the tokens write the padding rows.
+template <typename T, int KCH, bool DOT, bool SHORT>
 __global__ void __launch_bounds__(kThreads) scatter_kernel(ScatterArgs a)
 {
     __shared__ float part[kThreads / 32][KCH];
     pdl_launch_dependents();
     pdl_wait();
-    if ((int)blockIdx.x >= a.T) {
-        zero_padding<T>(a, blockIdx.x - a.T);
+    const int token_ctas = SHORT ? (a.T + (int)blockDim.y - 1) / (int)blockDim.y : a.T;
+    if ((int)blockIdx.x >= token_ctas) {
+        zero_padding<T, SHORT>(a, blockIdx.x - token_ctas);
         return;
     }
-    const int64_t t = blockIdx.x;
+    const int64_t t = token_of<SHORT>();
+    const bool here = !SHORT || t < a.T;    // (the last CTA's may not be)
     const int64_t slot0 = t * a.k;
     const T *src = static_cast<const T *>(a.src) + t * a.ld_src;
     const T *rows_in = static_cast<const T *>(a.rows_in);
@@ -309,13 +324,13 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(ScatterArgs a)
             d[j] = -1;
             w[j] = 1.0f;
             dot[j] = 0.0f;
-            if (j0 + j < a.k) {
+            if (here && j0 + j < a.k) {
                 d[j] = live_row(__ldg(a.dest + slot0 + j0 + j), a.R_cap, a.status);
                 if (a.weights)
                     w[j] = __ldg(a.weights + slot0 + j0 + j);
             }
         }
-        for (int c = threadIdx.x * E<T>; c < a.H; c += blockDim.x * E<T>) {
+        for (int c = here ? threadIdx.x * E<T> : a.H; c < a.H; c += blockDim.x * E<T>) {
             const uint4 raw = load16(src + c);
             uint4 in[KCH];
             if (DOT) {
@@ -350,7 +365,8 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(ScatterArgs a)
             }
         }
         if (DOT) {
-            const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+            const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+            const int warp0 = SHORT ? threadIdx.y * warps : 0, warp = warp0 + (threadIdx.x >> 5);
 #pragma unroll
             for (int j = 0; j < KCH; ++j) {
                 float v = dot[j];
@@ -360,10 +376,10 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(ScatterArgs a)
                     part[warp][j] = v;
             }
             __syncthreads();
-            if ((int)threadIdx.x < KCH && j0 + (int)threadIdx.x < a.k) {
+            if (here && (int)threadIdx.x < KCH && j0 + (int)threadIdx.x < a.k) {
                 float v = 0.0f;
                 for (int i = 0; i < warps; ++i)
-                    v += part[i][threadIdx.x];
+                    v += part[warp0 + i][threadIdx.x];
                 a.d_weights[slot0 + j0 + threadIdx.x] = v;
             }
             __syncthreads();
@@ -498,11 +514,13 @@ bool in_blocks(const void *p, int64_t ld, int64_t H, int elem)
 }
 
 // Threads for `units` of work side by side: the fewest whole warps that take
-// them in the same number of CTAs as kThreads would.
-int block_of(int64_t units)
+// them in the same number of CTAs as kThreads would; short rows several to a
+// CTA.
+dim3 block_of(int64_t units)
 {
     const int64_t passes = (units + kThreads - 1) / kThreads;
-    return (int)(((units + passes - 1) / passes + 31) / 32 * 32);
+    const int x = (int)(((units + passes - 1) / passes + 31) / 32 * 32);
+    return dim3(x, kThreads / x);
 }
 
 template <typename T, int KCH> cudaError_t combine_slots(const LaunchCtx &c, const CombineArgs &a, bool blocks)
@@ -510,10 +528,14 @@ template <typename T, int KCH> cudaError_t combine_slots(const LaunchCtx &c, con
     constexpr int UNR = KCH > 2 ? 1 : 2;
     // (a row that starts inside a block has up to one block more)
     const int64_t n = blocks ? (a.H / E<T> + UNR - 1) / UNR : (a.H + 2 * E<T> - 2) / E<T>;
-    const int block = block_of(n);
-    const dim3 grid((unsigned)a.T, (unsigned)((n + block - 1) / block));
-    return blocks ? launch_pdl(combine_kernel<T, KCH>, grid, dim3(block), 0, c.stream, a)
-                  : launch_pdl(combine_any_kernel<T, KCH == 8 ? E<T> / 2 : KCH>, grid, dim3(block), 0, c.stream, a);
+    const dim3 block = block_of(n);
+    const dim3 grid((unsigned)((a.T + block.y - 1) / block.y), (unsigned)((n + block.x - 1) / block.x));
+    constexpr int K2 = KCH == 8 ? E<T> / 2 : KCH;
+    if (block.y > 1)
+        return blocks ? launch_pdl(combine_kernel<T, KCH, true>, grid, block, 0, c.stream, a)
+                      : launch_pdl(combine_any_kernel<T, K2, true>, grid, block, 0, c.stream, a);
+    return blocks ? launch_pdl(combine_kernel<T, KCH, false>, grid, block, 0, c.stream, a)
+                  : launch_pdl(combine_any_kernel<T, K2, false>, grid, block, 0, c.stream, a);
 }
 
 template <typename T> cudaError_t combine_type(const LaunchCtx &c, const CombineArgs &a)
@@ -537,9 +559,14 @@ template <typename T, bool DOT> cudaError_t scatter_type(const LaunchCtx &c, Sca
                           dim3(kThreads), 0, c.stream, a);
     }
     const int64_t units = a.H / E<T>;
-    const int block = (int)(units >= kThreads ? kThreads : (units + 31) / 32 * 32);
-    return a.k <= 2 ? launch_pdl(scatter_kernel<T, 2, DOT>, dim3((unsigned)a.T + pad), dim3(block), 0, c.stream, a)
-                    : launch_pdl(scatter_kernel<T, 8, DOT>, dim3((unsigned)a.T + pad), dim3(block), 0, c.stream, a);
+    const int x = (int)(units >= kThreads ? kThreads : (units + 31) / 32 * 32);
+    const dim3 block(x, kThreads / x);
+    const dim3 grid((a.T + block.y - 1) / block.y + pad);
+    if (block.y > 1)
+        return a.k <= 2 ? launch_pdl(scatter_kernel<T, 2, DOT, true>, grid, block, 0, c.stream, a)
+                        : launch_pdl(scatter_kernel<T, 8, DOT, true>, grid, block, 0, c.stream, a);
+    return a.k <= 2 ? launch_pdl(scatter_kernel<T, 2, DOT, false>, grid, block, 0, c.stream, a)
+                    : launch_pdl(scatter_kernel<T, 8, DOT, false>, grid, block, 0, c.stream, a);
 }
 
 template <typename T> cudaError_t scatter_dot(const LaunchCtx &c, const ScatterArgs &a)
