@@ -168,7 +168,7 @@ __device__ __forceinline__ int used_rows(const SwigluArgs &a)
 }
 
 // A CTA's walk over blocks of (256 / cols) rows x cols units of 8 columns, in
-// row order; a warp stays within one row.
+// row order; the four lanes of a block of 32 elements stay together.
 struct Walk {
     int nu, cols, tx, ty, step, blocks, r, qb;
     int64_t left;
@@ -269,13 +269,17 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluArgs a,
             rsu = __ldg(sr + a.I / 32);
         }
     };
-    int cur = -1;         // expert whose rows `top` covers (the same in all lanes of a warp) ...
+    int cur = -1;         // expert whose rows `top` covers ...
     int cur_end = 0;      // ... and where they end
     float top = 0.0f;     // its largest |dg|, |du| so far
     auto flush = [&]() {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, f2u(top));
-        if (cur >= 0 && (threadIdx.x & 31) == 0 && m)
-            red_max_nonneg(a.expert_amax + cur, u2f(m));
+        if (__all_sync(0xffffffffu, cur == __shfl_sync(0xffffffffu, cur, 0))) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, f2u(top));
+            if (cur >= 0 && (threadIdx.x & 31) == 0 && m)
+                red_max_nonneg(a.expert_amax + cur, u2f(m));
+        } else if (cur >= 0 && f2u(top)) {      // short rows: the warp's rows lie on both sides of a boundary
+            red_max_nonneg(a.expert_amax + cur, top);
+        }
         top = 0.0f;
     };
     fetch();
@@ -287,10 +291,13 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluArgs a,
         const bool on = r < R && q < at.nu;
         at.next();
         fetch();
-        if (a.expert_amax && r < R && (cur < 0 || r >= cur_end)) {
+        const bool turn = r < R && (cur < 0 || r >= cur_end);
+        if (a.expert_amax && __any_sync(0xffffffffu, turn)) {
             flush();
-            cur = a.offsets ? expert_of_dest(a.offsets, a.E, r) : 0;
-            cur_end = a.offsets ? __ldg(a.offsets + cur + 1) : R;
+            if (turn) {
+                cur = a.offsets ? expert_of_dest(a.offsets, a.E, r) : 0;
+                cur_end = a.offsets ? __ldg(a.offsets + cur + 1) : R;
+            }
         }
         if (on) {
             const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
@@ -322,10 +329,15 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluArgs a,
         flush();
 }
 
+// Threads side by side along a row: the least power of two that covers it, 4
+// (one block of 32) to 256.  (With no fewer than a warp, 6022 x 6 rows of I = 96
+// took 29 us.)
 int column_threads(int I)
 {
-    const int nu = I / 8;
-    return nu <= 32 ? 32 : nu <= 64 ? 64 : nu <= 128 ? 128 : 256;
+    int n = 4;
+    while (n < I / 8 && n < kThreads)
+        n *= 2;
+    return n;
 }
 
 // One wave of resident CTAs (or fewer, if there is less work).

@@ -416,6 +416,25 @@ def test_swiglu_extremes():
     assert amax[2] == torch.tensor(1e30)
 
 
+@pytest.mark.parametrize("I", [32, 64, 96, 256])
+def test_swiglu_experts_of_any_length(I):
+    """Experts that begin and end inside a warp's rows, and empty ones."""
+    g = gen(30)
+    off = torch.tensor([0, 3, 3, 4, 11, 11, 30, 37], dtype=torch.int32, device="cuda")
+    E, R_cap = 7, 40
+    x = torch.randn(R_cap, 2 * I, generator=g, device="cuda").to(torch.bfloat16)
+    d = torch.randn(R_cap, I, generator=g, device="cuda").to(torch.bfloat16)
+    _, ckpt = nq.ep_swiglu(x, off, E)
+    amax = torch.zeros(E, device="cuda")
+    d_x, _ = nq.ep_swiglu_backward(d, ckpt, off, E, expert_amax=amax)
+    o = off.tolist()
+    for e in range(E):
+        if o[e] == o[e + 1]:
+            assert amax[e] == 0
+        else:
+            assert amax[e].to(torch.bfloat16) == d_x[o[e]: o[e + 1]].abs().max()
+
+
 def test_swiglu_reports_rows_past_the_buffer():
     x = torch.ones(128, 64, dtype=torch.bfloat16, device="cuda")
     off = torch.tensor([0, 256], dtype=torch.int32, device="cuda")
