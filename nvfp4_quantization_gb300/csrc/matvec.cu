@@ -793,12 +793,14 @@ template <int G, int HALVES> cudaError_t launch_ring(const LaunchCtx &c, const M
         !make_map(&scales, a.w + a.K / 2, (uint64_t)a.K / 16, rows, (uint64_t)a.S, P::scale_pitch, kTile))
         return cudaErrorInvalidValue;
     const int steps = (a.K + HALVES * kHalf - 1) / (HALVES * kHalf);
-    // more warps a tile where there is less than a tile for every team at most
+    // two warps a tile if each has two steps of it (one step a warp, rows of
+    // 1024: 43 us where a warp a tile takes 38); more where there is less than a
+    // tile for every team at most
     const int64_t slots = (int64_t)a.T * a.k;
     const int64_t groups = slots < a.E + slots / G ? slots : a.E + slots / G;
     const int64_t tiles = groups * ((a.N + kTile - 1) / kTile);
     int parts = 1;
-    while (2 * parts <= steps && (2 * parts <= kMaxParts ||
+    while (2 * parts <= steps && ((2 * parts <= kMaxParts && 4 * parts <= steps) ||
                                   (2 * parts <= kWarps && tiles * 2 * parts <= (int64_t)c.num_sms * kWarps)))
         parts *= 2;
     return launch_pdl(matvec_kernel<G, HALVES>, dim3((unsigned)c.num_sms), dim3(kThreads),
