@@ -20,7 +20,7 @@
 // in flight while the current one is computed.
 //
 // Measured on GB300, 64 experts top-6, 16384 tokens, I = 2048: forward and
-// backward with the activation again 603 us (6.1 TB/s, 6.3 with the padding
+// backward with the activation again 600 us (6.1 TB/s, 6.3 with the padding
 // rows); 8 experts top-2, 8192 tokens, I = 4096: 183 us (5.9 TB/s, 6.1).
 #include "epq_device.cuh"
 #include "epq_internal.h"
