@@ -417,18 +417,19 @@ __device__ void zero_padding_any(const ScatterArgs &a, int cta)
         p[threadIdx.x] = T(0);
 }
 
-// Rows that start anywhere: one warp per slot (a CTA's W = 8 where slots are
-// few: 96 slots of 3993 FP32 took 20 us on one warp each), because each of a token's rows
+// Rows that start anywhere: L threads per slot, a warp (a CTA where slots are
+// few: 96 slots of 3993 FP32 took 20 us on one warp each; a quarter of a warp
+// for short rows without a sum along them: 25032 slots of 117 took 18), because each of a token's rows
 // wants the token at another shift; the token is read k times, from L1 and L2
 // after the first.  A lane has U aligned blocks of the row (parts of one at its
 // ends) and the windows that belong to them in flight (with two windows a block,
 // two blocks of BF16: 8192 x 7001 top-6 296 us, with one 314; one of FP32: 1021
 // x 1001 top-5 14.9 us, with two 18.1).
-template <typename T, bool DOT, int W>
+template <typename T, bool DOT, int L>
 __global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
 {
-    constexpr int U = !DOT ? 4 : sizeof(T) == 2 ? 2 : 1, kSlots = kThreads / 32 / W;
-    __shared__ float part[W];
+    constexpr int U = !DOT ? 4 : sizeof(T) == 2 ? 2 : 1, kSlots = kThreads / L;
+    __shared__ float part[kThreads / 32];
     pdl_launch_dependents();
     pdl_wait();
     const int64_t slots = (int64_t)a.T * a.k;
@@ -437,11 +438,9 @@ __global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
         zero_padding_any<T>(a, blockIdx.x - slot_ctas);
         return;
     }
-    const int lane = threadIdx.x % (32 * W);
-    const int64_t s = (int64_t)blockIdx.x * kSlots + threadIdx.x / (32 * W);
-    if (s >= slots)
-        return;
-    const int d = live_row(__ldg(a.dest + s), a.R_cap, a.status);
+    const int lane = threadIdx.x % L;
+    const int64_t s = (int64_t)blockIdx.x * kSlots + threadIdx.x / L;
+    const int d = s < slots ? live_row(__ldg(a.dest + s), a.R_cap, a.status) : -1;
     float dot = 0.0f;
     if (d >= 0) {
         const int64_t t = s / a.k;
@@ -450,11 +449,11 @@ __global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
         const T *in = DOT ? static_cast<const T *>(a.rows_in) + (int64_t)d * a.ld_in : nullptr;
         T *to = static_cast<T *>(a.rows_out) + (int64_t)d * a.H;
         const bool src_inner = inner_row<T>(t, a.T, a.ld_src), in_inner = DOT && inner_row<T>(d, a.R_cap, a.ld_in);
-        for (int c0 = lane * E<T> - before(to); c0 < a.H; c0 += 32 * W * U * E<T>) {
+        for (int c0 = lane * E<T> - before(to); c0 < a.H; c0 += L * U * E<T>) {
             Window x[U], y[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * 32 * W * E<T>;
+                const int c = c0 + u * L * E<T>;
                 if (c >= a.H)
                     break;
                 const int first = c < 0 ? -c : 0, n = min(E<T>, a.H - c);
@@ -464,7 +463,7 @@ __global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * 32 * W * E<T>;
+                const int c = c0 + u * L * E<T>;
                 if (c >= a.H)
                     break;
                 const int first = c < 0 ? -c : 0, n = min(E<T>, a.H - c);
@@ -492,17 +491,17 @@ __global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
         }
     }
     if (DOT) {
-        for (int o = 16; o; o >>= 1)
+        for (int o = L < 32 ? L / 2 : 16; o; o >>= 1)
             dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (W > 1) {                    // (the whole CTA has this slot)
+        if (L > 32) {
             if ((lane & 31) == 0)
                 part[lane / 32] = dot;
             __syncthreads();
             dot = 0.0f;
-            for (int i = 0; i < W; ++i)
+            for (int i = 0; i < L / 32; ++i)
                 dot += part[i];
         }
-        if (lane == 0)
+        if (lane == 0 && s < slots)
             a.d_weights[s] = dot;
     }
 }
@@ -551,12 +550,12 @@ template <typename T, bool DOT> cudaError_t scatter_type(const LaunchCtx &c, Sca
     if (!(in_blocks(a.src, a.ld_src, a.H, sizeof(T)) && in_blocks(a.rows_out, a.H, a.H, sizeof(T)) &&
           in_blocks(a.rows_in, a.rows_in ? a.ld_in : 0, a.H, sizeof(T)))) {
         const int64_t slots = (int64_t)a.T * a.k;
-        const int warps = kThreads / 32;
-        if (slots < (int64_t)c.num_sms * 2 * warps)
-            return launch_pdl(scatter_any_kernel<T, DOT, kThreads / 32>, dim3((unsigned)slots + pad), dim3(kThreads), 0,
-                              c.stream, a);
-        return launch_pdl(scatter_any_kernel<T, DOT, 1>, dim3((unsigned)((slots + warps - 1) / warps) + pad),
-                          dim3(kThreads), 0, c.stream, a);
+        auto grid = [&](int per_cta) { return dim3((unsigned)((slots + per_cta - 1) / per_cta) + pad); };
+        if (!DOT && a.H <= 16 * E<T>)
+            return launch_pdl(scatter_any_kernel<T, false, 8>, grid(kThreads / 8), dim3(kThreads), 0, c.stream, a);
+        if (slots < (int64_t)c.num_sms * 2 * (kThreads / 32))
+            return launch_pdl(scatter_any_kernel<T, DOT, kThreads>, grid(1), dim3(kThreads), 0, c.stream, a);
+        return launch_pdl(scatter_any_kernel<T, DOT, 32>, grid(kThreads / 32), dim3(kThreads), 0, c.stream, a);
     }
     const int64_t units = a.H / E<T>;
     const int x = (int)(units >= kThreads ? kThreads : (units + 31) / 32 * 32);
