@@ -474,7 +474,8 @@ ep_status ep_combine_backward(const void *d_out, int dtype, int64_t T,
  *   expert_offsets  device int32 [E+1] or NULL.  With it, rows [0, R) are
  *                   processed, R = expert_offsets[E]; NULL (E = 1): all R_cap.
  *   act_bf16        device bf16 [R_cap, I]: g / (1 + exp(-g)) * u, FP32 from
- *                   the BF16 input, rounded once.
+ *                   the BF16 input, rounded once.  A sigmoid below FP32's range
+ *                   still counts where its product with u does not lie there.
  *   ckpt            device u8 or NULL: MXFP8 of x in ep_mxfp8_pack's layout
  *                   (data [R_cap, 2I], then scales [R_cap, 2I/32]; same
  *                   exponent rule).  An infinity or NaN is stored as E4M3's
@@ -490,7 +491,9 @@ ep_status ep_swiglu(const void *x_bf16, int64_t ld_x, int64_t R_cap, int64_t I,
  * g, u the values ckpt holds and s = 1 / (1 + exp(-g)):
  *   d_x_bf16        device bf16 [R_cap, 2I]: dg = d_act * u * s * (1 + g (1 - s))
  *                   in [0, I), du = d_act * g * s in [I, 2I); FP32, rounded
- *                   once.
+ *                   once.  d_act * u is formed first and can overflow alone.
+ *                   Elements that E4M3 rounds up to 2^128 count as the largest
+ *                   FP32 number.
  *   act_bf16        device bf16 [R_cap, I] or NULL: g * s * u again (the second
  *                   product's weight gradient reads it).
  *   expert_amax     device f32 [E] or NULL: max-reduced with |dg|, |du| of each

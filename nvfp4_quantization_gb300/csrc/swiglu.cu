@@ -48,18 +48,22 @@ __device__ __forceinline__ float rcp_approx(float x)
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// 1 / (1 + exp(-g)) of two finite values.  exp(-g) = 2^t (1 + r ln 2) with
-// t = RN(-g log2 e) and r what the product lost: its rounding error (exact by
-// a fused multiply-add; Dekker, "A floating-point technique for extending the
-// available precision", 1971) and the part of log2 e below FP32.  Without r
-// the result would lose as many bits as |t| has.
+// log2 e as the sum of two FP32 numbers.
+constexpr float kLog2eHi = 1.44269504088896340736f;
+constexpr float kLog2eLo = (float)(1.44269504088896340736 - (double)kLog2eHi);
+
+// 1 / (1 + exp(-g)) of two values up to 2^127 in size, so that g log2 e stays
+// finite.  exp(-g) = 2^t (1 + r ln 2) with t = RN(-g log2 e) and r what the
+// product lost: its rounding error (exact by a fused multiply-add; Dekker, "A
+// floating-point technique for extending the available precision", 1971) and
+// the part of log2 e below FP32.  Without r the result would lose as many bits
+// as |t| has.  Below g = -87.3 the result, under 2^-126, is taken to 0: a far
+// gate, which the kernels look for and hand to the functions below.
 __device__ __forceinline__ float2 sigmoid2(float2 g)
 {
-    const float hi = -1.44269504088896340736f;
-    const float lo = (float)(-1.44269504088896340736 - (double)hi);
-    const float2 t = mul2(g, both(hi));
-    float2 r = fma2(g, both(hi), make_float2(-t.x, -t.y));
-    r = fma2(g, both(lo), r);
+    const float2 t = mul2(g, both(-kLog2eHi));
+    float2 r = fma2(g, both(-kLog2eHi), make_float2(-t.x, -t.y));
+    r = fma2(g, both(-kLog2eLo), r);
     const float2 c = fma2(r, both(0.69314718055994530942f), both(1.0f));
     const float2 e = mul2(make_float2(ex2_approx(t.x), ex2_approx(t.y)), c);
     const float2 d = add2(e, both(1.0f));
@@ -69,6 +73,59 @@ __device__ __forceinline__ float2 sigmoid2(float2 g)
 __device__ __forceinline__ float2 bf16_pair(uint32_t w) { return make_float2(u2f(w << 16), u2f(w & 0xffff0000u)); }
 
 __device__ __forceinline__ uint32_t to_bf16_pair(float2 v) { return cvt_bf16x2(v.x, v.y); }
+
+// ---------------------------------------------------------------- far gates
+// Below kFar the sigmoid leaves FP32's normal range, but its products with a
+// large u or gradient need not: there s = exp(g) = p 2^n to well below a
+// rounding, and the products are taken apart into fractions and exponents.
+constexpr float kFar = -86.0f;
+constexpr uint32_t kFarBits = 0x42acu;      // |kFar| as BF16
+
+// p and n for g in [-1024, kFar]; p is about 2^-1/2 to 2^1/2.
+__device__ __forceinline__ float exp_parts(float g, int &n)
+{
+    const float k = rintf(g * kLog2eHi);
+    n = (int)k;
+    return ex2_approx(fmaf(g, kLog2eLo, fmaf(g, kLog2eHi, -k)));
+}
+
+// a b c 2^n, rounded to FP32's range at the end alone; c is of ordinary size.
+__device__ __forceinline__ float product(float a, float b, float c, int n)
+{
+    int ea, eb;
+    const float m = frexpf(a, &ea) * frexpf(b, &eb) * c;
+    return ldexpf(m, n + ea + eb);
+}
+
+// The products of the backward pass, in the order in which the interface
+// states them; c: the sigmoid's argument.
+__device__ __forceinline__ void gradients(float2 d, float2 g, float2 c, float2 u, float2 &dg, float2 &du, float2 &act)
+{
+    const float2 s = sigmoid2(c);
+    const float2 silu = mul2(g, s);
+    const float2 slope = fma2(silu, fma2(s, both(-1.0f), both(1.0f)), s);
+    du = mul2(d, silu);
+    dg = mul2(mul2(d, u), slope);
+    act = mul2(silu, u);
+}
+
+// The same for one far gate.  Beyond -1024 every result is 0.
+__device__ __forceinline__ void gradients_far(float d, float g, float u, float &dg, float &du, float &act)
+{
+    g = fmaxf(g, -1024.0f);
+    int n;
+    const float p = exp_parts(g, n);
+    dg = product(d, u, (1.0f + g) * p, n);
+    du = product(d, 1.0f, g * p, n);
+    act = product(u, 1.0f, g * p, n);
+}
+
+// E4M3 times 2^120 reaches 2^128, which passes for FLT_MAX.
+__device__ __forceinline__ float finite(float v) { return fabsf(v) > FLT_MAX ? copysignf(FLT_MAX, v) : v; }
+__device__ __forceinline__ float2 finite2(float2 v) { return make_float2(finite(v.x), finite(v.y)); }
+
+// The sigmoid of +-256 is that of +-infinity; a NaN comes back with the product.
+__device__ __forceinline__ float near(float g) { return fminf(fmaxf(g, -256.0f), 256.0f); }
 
 // max(|a|, |b|) per BF16 half; a NaN in either wins (signs are meaningless).
 __device__ __forceinline__ uint32_t absmax_pair(uint32_t a, uint32_t b)
@@ -157,6 +214,63 @@ __device__ __forceinline__ float2 scale_of(uint32_t sbyte)
     return both(sbyte ? u2f(sbyte << 23) : u2f(0x00400000u));
 }
 
+// Whether a gate of a block with this scale can lie below kFar (448 * 2^-3 = 56
+// is the largest element of the scale before), or an element of either at 2^128.
+__device__ __forceinline__ bool has_far(uint32_t sbyte_g, uint32_t sbyte_u) { return sbyte_g >= 125u || sbyte_u >= 247u; }
+
+// The results of 8 columns with far gates or elements of 2^128 among them.
+// Kept out of line: it is rare.
+struct Results {
+    uint4 dg, du, act;
+    float top;
+};
+
+__device__ __noinline__ Results backward8_far(uint4 d, uint2 cg, uint2 cu, uint32_t sbyte_g, uint32_t sbyte_u, float top)
+{
+    const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+    const uint32_t gw[4] = {cg.x & 0xffffu, cg.x >> 16, cg.y & 0xffffu, cg.y >> 16};
+    const uint32_t uw[4] = {cu.x & 0xffffu, cu.x >> 16, cu.y & 0xffffu, cu.y >> 16};
+    uint32_t og[4], ou[4], oa[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 dv = bf16_pair(dw[i]);
+        const float2 g = finite2(decode2(gw[i], scale_of(sbyte_g))), u = finite2(decode2(uw[i], scale_of(sbyte_u)));
+        float2 dg, du, act;
+        gradients(dv, g, make_float2(near(g.x), near(g.y)), u, dg, du, act);
+        if (g.x < kFar)
+            gradients_far(dv.x, g.x, u.x, dg.x, du.x, act.x);
+        if (g.y < kFar)
+            gradients_far(dv.y, g.y, u.y, dg.y, du.y, act.y);
+        top = max_abs_nan(max_abs_nan(top, dg), du);
+        og[i] = to_bf16_pair(dg);
+        ou[i] = to_bf16_pair(du);
+        oa[i] = to_bf16_pair(act);
+    }
+    return {make_uint4(og[0], og[1], og[2], og[3]), make_uint4(ou[0], ou[1], ou[2], ou[3]),
+            make_uint4(oa[0], oa[1], oa[2], oa[3]), top};
+}
+
+// Activations `o` of 8 gates with those of far gates put right (beyond -256
+// they are 0 as they stand, and an infinity's is NaN).  Out of line like the
+// one above.
+__device__ __noinline__ uint4 forward8_far(uint4 g, uint4 u, uint4 o)
+{
+    const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+    uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int up = 16 * (i & 1);
+        const float gv = u2f(gw[i >> 1] >> up << 16);
+        if (!(gv >= -256.0f && gv < kFar))
+            continue;
+        int n;
+        const float p = exp_parts(gv, n);
+        const uint32_t v = cvt_bf16x2(product(u2f(uw[i >> 1] >> up << 16), 1.0f, gv * p, n), 0.0f);
+        ow[i >> 1] = (ow[i >> 1] & 0xffff0000u >> up) | (v & 0xffffu) << up;
+    }
+    return make_uint4(ow[0], ow[1], ow[2], ow[3]);
+}
+
 __device__ __forceinline__ int used_rows(const SwigluArgs &a)
 {
     if (!a.offsets)
@@ -221,14 +335,17 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluArgs a, int cols
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // the sigmoid of +-256 is that of +-infinity; a NaN comes back with the product
-            uint32_t c;
+            uint32_t c;                 // what near() makes of the pair
             asm("{\n\t.reg .b32 m;\n\tmin.bf16x2 m, %1, %2;\n\tmax.bf16x2 %0, m, %3;\n\t}"
                 : "=r"(c) : "r"(gw[i]), "r"(0x43804380u), "r"(0xc380c380u));
             o[i] = to_bf16_pair(mul2(mul2(bf16_pair(gw[i]), sigmoid2(bf16_pair(c))), bf16_pair(uw[i])));
         }
+        uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
+        const uint32_t m = absmax_pair(absmax_pair(g.x, g.y), absmax_pair(g.z, g.w)) & 0x7fff7fffu;
+        if (max(m & 0xffffu, m >> 16) > kFarBits)
+            out = forward8_far(g, u, out);
         if (on)
-            *reinterpret_cast<uint4 *>(a.act + (int64_t)r * a.I + q * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(a.act + (int64_t)r * a.I + q * 8) = out;
         if (CKPT) {
             uint32_t sg, su;
             const uint2 cg = encode8(g, sg), cu = encode8(u, su);
@@ -286,7 +403,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluArgs a,
     while (at.left > 0) {
         const uint4 d = rd;
         const uint2 cg = rg, cu = ru;
-        const float2 sg = scale_of(rsg), su = scale_of(rsu);
+        const uint32_t sbyte_g = rsg, sbyte_u = rsu;
         const int r = at.r, q = at.unit();
         const bool on = r < R && q < at.nu;
         at.next();
@@ -300,29 +417,35 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluArgs a,
             }
         }
         if (on) {
-            const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
-            const uint32_t gw[4] = {cg.x & 0xffffu, cg.x >> 16, cg.y & 0xffffu, cg.y >> 16};
-            const uint32_t uw[4] = {cu.x & 0xffffu, cu.x >> 16, cu.y & 0xffffu, cu.y >> 16};
-            uint32_t og[4], ou[4], oa[4];
+            Results o;
+            if (has_far(sbyte_g, sbyte_u)) {
+                o = backward8_far(d, cg, cu, sbyte_g, sbyte_u, top);
+                top = o.top;
+            } else {
+                const float2 sg = scale_of(sbyte_g), su = scale_of(sbyte_u);
+                const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+                const uint32_t gw[4] = {cg.x & 0xffffu, cg.x >> 16, cg.y & 0xffffu, cg.y >> 16};
+                const uint32_t uw[4] = {cu.x & 0xffffu, cu.x >> 16, cu.y & 0xffffu, cu.y >> 16};
+                uint32_t og[4], ou[4], oa[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 dv = bf16_pair(dw[i]), g = decode2(gw[i], sg), u = decode2(uw[i], su);
-                const float2 s = sigmoid2(g);
-                const float2 silu = mul2(g, s);
-                const float2 du = mul2(dv, silu);
-                const float2 slope = fma2(silu, fma2(s, both(-1.0f), both(1.0f)), s);
-                const float2 dg = mul2(mul2(dv, u), slope);
-                top = max_abs_nan(max_abs_nan(top, dg), du);
-                og[i] = to_bf16_pair(dg);
-                ou[i] = to_bf16_pair(du);
-                if (ACT)
-                    oa[i] = to_bf16_pair(mul2(silu, u));
+                for (int i = 0; i < 4; ++i) {
+                    const float2 g = decode2(gw[i], sg);
+                    float2 dg, du, act;
+                    gradients(bf16_pair(dw[i]), g, g, decode2(uw[i], su), dg, du, act);
+                    top = max_abs_nan(max_abs_nan(top, dg), du);
+                    og[i] = to_bf16_pair(dg);
+                    ou[i] = to_bf16_pair(du);
+                    oa[i] = to_bf16_pair(act);
+                }
+                o.dg = make_uint4(og[0], og[1], og[2], og[3]);
+                o.du = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+                o.act = make_uint4(oa[0], oa[1], oa[2], oa[3]);
             }
             uint16_t *dx = a.d_x + (int64_t)r * 2 * a.I + q * 8;
-            *reinterpret_cast<uint4 *>(dx) = make_uint4(og[0], og[1], og[2], og[3]);
-            *reinterpret_cast<uint4 *>(dx + a.I) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+            *reinterpret_cast<uint4 *>(dx) = o.dg;
+            *reinterpret_cast<uint4 *>(dx + a.I) = o.du;
             if (ACT)
-                *reinterpret_cast<uint4 *>(a.act + (int64_t)r * a.I + q * 8) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+                *reinterpret_cast<uint4 *>(a.act + (int64_t)r * a.I + q * 8) = o.act;
         }
     }
     if (a.expert_amax)
