@@ -7,7 +7,7 @@ activation's backward also leaves each expert's amax, with which d_h goes
 straight into the columnwise NVFP4 operand of the weight-gradient product.
 
 Decode (NVFP4 weights): the same layer for a few tokens, straight from the
-packed rows: products, activation, products, combine, five calls in all with
+packed rows: products, activation, products, combine, four calls in all with
 the routing left as ids.
 
 The expert products of the training step are torch.matmul per expert: the
@@ -45,6 +45,7 @@ class Layer:
     def __init__(self, w1, w2):
         self.w1, self.w2, self.E = w1, w2, w1.shape[0]
         self.w1_rows, self.w2_rows = nq.ep_nvfp4_pack_weights(w1), nq.ep_nvfp4_pack_weights(w2)
+        self.status = nq.new_status(w1.device)   # what the decode steps report: EP_DEV_ERR_* bits
 
     def forward(self, x, topk, weights):
         """Output [T, H] and what the backward pass keeps."""
@@ -76,11 +77,13 @@ class Layer:
         return d_x, d_weights, d_w1, d_w2, colwise
 
     def decode(self, x, topk, weights):
-        """Output [T, H] for a few tokens, from the packed weights."""
-        h = nq.ep_nvfp4_matvec(x, self.w1_rows, topk)
-        act, _ = nq.ep_swiglu(h, checkpoint=False)
-        y = nq.ep_nvfp4_matvec(act, self.w2_rows, topk)
-        return nq.ep_combine(y, topk_idx=topk, weights=weights)
+        """Output [T, H] for a few tokens, from the packed weights.  A bad id, or
+        anything else that the kernels find wrong, shows in self.status, which is
+        read when the host waits for the GPU anyway."""
+        h = nq.ep_nvfp4_matvec(x, self.w1_rows, topk, status=self.status)
+        act, _ = nq.ep_swiglu(h, checkpoint=False, status=self.status)
+        y = nq.ep_nvfp4_matvec(act, self.w2_rows, topk, status=self.status)
+        return nq.ep_combine(y, topk_idx=topk, weights=weights, status=self.status)
 
 
 def plain_layer(x, topk, weights, w1, w2):
@@ -120,7 +123,7 @@ def main(T=2048, H=1024, I=512, E=8, k=2, seed=0):
 
     few = slice(0, 4)                            # decoding: the weights' 4 bits are what is left of an error
     err["decode"] = relative(layer.decode(x[few], topk[few].contiguous(), weights[few].contiguous()), want[few])
-    assert int(kept[0].status) == 0
+    assert int(kept[0].status) == 0 and int(layer.status) == 0
     return err
 
 

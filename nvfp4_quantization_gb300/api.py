@@ -299,6 +299,10 @@ def ep_mxfp8_pack(tokens: torch.Tensor, plan: RoutePlan, buf: torch.Tensor | Non
 # With `stream`, outputs and scratch made here belong to that stream; inputs made
 # on another one are the caller's to order (wait_stream) and keep (record_stream).
 #
+# What a kernel finds wrong it reports in `status` (new_status; EP_DEV_ERR_* bits)
+# or in the plan's word.  A call without either makes a word of its own, which
+# costs a fill and which nobody sees.
+#
 # These calls are made for single tokens too, where a call's host time is its
 # time: operands go to the library as plain addresses, and the current stream's
 # handle is read without building a Stream object (3 us of a 10 us call).
@@ -403,7 +407,7 @@ def ep_combine(rows: torch.Tensor, plan: RoutePlan | None = None, weights: torch
     With ``plan`` the rows are in its order ([R_cap, H]); with ``topk_idx``
     (int32 [T, k]) they are in slot order ([T*k, H], as ep_nvfp4_matvec writes
     them) and slots whose id is negative are left out.  ``weights`` f32 [T, k],
-    None = 1."""
+    None = 1.  Errors are reported in ``status``, or in the plan's word."""
     ld = _need_rows(rows, "rows", _DTYPE)
     n, H = rows.shape
     dev = rows.device
@@ -493,7 +497,8 @@ def ep_swiglu(x: torch.Tensor, offsets: torch.Tensor | None = None, E: int = 1, 
     (act [R_cap, I], checkpoint).  The checkpoint (uint8,
     swiglu_checkpoint_bytes) holds x in MXFP8 for ep_swiglu_backward;
     ``checkpoint=False`` leaves it out (None).  With ``offsets`` (int32 [E+1])
-    only rows [0, offsets[E]) are processed."""
+    only rows [0, offsets[E]) are processed; more than R_cap of them are
+    reported in ``status`` (not seen without it)."""
     ld = _need_rows(x, "x", (torch.bfloat16,))
     R_cap, width = x.shape
     if width % 64:
@@ -524,7 +529,8 @@ def ep_swiglu_backward(d_act: torch.Tensor, ckpt: torch.Tensor, offsets: torch.T
     activation is written again (from the checkpoint's values) into ``act``, or
     into a new tensor with ``recompute=True``; else None.  ``expert_amax`` (f32
     [E], filled by the caller, e.g. with zeros) receives the max of each
-    expert's |d_x| before rounding: the amax of ep_nvfp4_colwise_rht_bf16."""
+    expert's |d_x| before rounding: the amax of ep_nvfp4_colwise_rht_bf16.
+    ``status`` as in ep_swiglu."""
     ld = _need_rows(d_act, "d_act", (torch.bfloat16,))
     R_cap, I = d_act.shape
     dev = d_act.device
@@ -582,7 +588,9 @@ def ep_nvfp4_matvec(x: torch.Tensor, w_rows: torch.Tensor, topk_idx: torch.Tenso
     ``w_rows`` uint8 [E, N, row_bytes(K)] (ep_nvfp4_pack_weights); ``x`` BF16
     [T, K] (one row for all slots of a token) or [T*k, K] (one per slot).
     Slots whose id is -1 give zero rows.  Without ``topk_idx`` E must be 1 and
-    the call is a dense layer on x [T, K]."""
+    the call is a dense layer on x [T, K].  An id out of range (its rows are
+    zero too) and a wait that gave up (rows of y left as they were) are reported
+    in ``status`` and not seen without it."""
     ld = _need_rows(x, "x", (torch.bfloat16,))
     n, K = x.shape
     dev = x.device
