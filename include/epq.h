@@ -531,8 +531,10 @@ ep_status ep_swiglu_backward(const void *d_act_bf16, int64_t ld_act,
  * time is the reading of the weights (up to 8 slots of an expert share one
  * pass over its rows, fewer where K is above about 8000).  Weights and block
  * scales enter exactly, x within 2^-39 of its row's largest element; FP32
- * accumulation, the row scale applied to the sum, one rounding.  A slot's result does not depend on the routing of
- * the other slots (it may differ in the last bits between batch sizes).
+ * accumulation, the row scale applied to the sum, one rounding.  A slot's
+ * result does not depend on the routing of the other slots.  The order of its
+ * sum, and with it the last bits, depends on T, k, K, N, E and the device's
+ * number of SMs: the same weights split over N may give other last bits.
  * An infinity or NaN in x shows in its slot's outputs alone.
  */
 ep_status ep_nvfp4_matvec(const void *x_bf16, int64_t T, int64_t K,

@@ -47,8 +47,10 @@
 // Measured on GB300, 4096 x 4096 per expert, 64 experts top-8: one token 17.4 us
 // (76 MB, 4.4 TB/s, of which 4 us are the launch, the ids and x), 8 tokens 66 us
 // (5.5 TB/s of the rows in use), 32 tokens 110 us (5.5 TB/s).
-// The order of a row's sum depends on the shape (K, T, E), never on the
-// routing: a slot's result does not depend on where the other slots went.
+// The order of a row's sum depends on the call's shape (T, k, K, N, E) and the
+// number of SMs, by which the launcher chooses how many warps share a tile,
+// never on the routing: a slot's result does not depend on where the other
+// slots went.
 #include "epq_device.cuh"
 #include "epq_internal.h"
 
