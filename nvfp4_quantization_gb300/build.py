@@ -19,7 +19,7 @@ CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = BUILD / "libepq.so"
 SOURCES = ["api.cu", "route.cu", "route_noalloc.cu", "pack.cu", "unpack.cu", "receive.cu", "colwise_bf16.cu",
-           "combine.cu", "swiglu.cu", "matvec.cu"]
+           "combine.cu", "swiglu.cu", "matvec.cu", "tensor_map.cu"]
 HEADERS = ["epq_device.cuh", "epq_internal.h"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
