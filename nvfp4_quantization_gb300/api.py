@@ -471,8 +471,8 @@ def ep_combine_backward(d_out: torch.Tensor, plan: RoutePlan, weights: torch.Ten
         _need_dense(d_rows, "d_rows", (R_cap, H), dt)
     st = _lib.lib().ep_combine_backward(d_out.data_ptr(), _DTYPE[dt], T, H, ld, _at(rows), ld_rows,
                                         plan.dest.data_ptr(), _at(weights), k, plan.offsets.data_ptr(),
-                                        plan.counts.data_ptr(), plan.E, d_rows.data_ptr(), R_cap, _at(d_weights), plan.status.data_ptr(),
-                                        _stream_of(stream, dev))
+                                        plan.counts.data_ptr(), plan.E, d_rows.data_ptr(), R_cap, _at(d_weights),
+                                        plan.status.data_ptr(), _stream_of(stream, dev))
     if st:
         check("ep_combine_backward", st)
     return d_rows, d_weights

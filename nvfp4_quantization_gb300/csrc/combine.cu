@@ -13,9 +13,9 @@
 //
 // Bound: HBM; each row, token and gradient passes once, in 16-byte blocks, with
 // the loads of a token's slots in flight together.
-// Measured on GB300 at 16384 tokens x 7168, BF16: pack, 64 experts top-6 255 us
-// (6.4 TB/s, padding rows not counted), combine, 256 experts top-8 335 us (6.3
-// TB/s), its gradient with the weights' 631 us (6.3 TB/s, 6.7 with the padding
+// Measured on GB300 at 16384 tokens x 7168, BF16: pack, 64 experts top-6 254 us
+// (6.5 TB/s, padding rows not counted), combine, 256 experts top-8 336 us (6.3
+// TB/s), its gradient with the weights' 629 us (6.3 TB/s, 6.7 with the padding
 // rows).
 #include "epq_device.cuh"
 #include "epq_internal.h"
@@ -419,9 +419,9 @@ __device__ void zero_padding_any(const ScatterArgs &a, int cta)
 
 // Rows that start anywhere: L threads per slot, a warp (a CTA where slots are
 // few: 96 slots of 3993 FP32 took 20 us on one warp each; a quarter of a warp
-// for short rows without a sum along them: 25032 slots of 117 took 18), because each of a token's rows
-// wants the token at another shift; the token is read k times, from L1 and L2
-// after the first.  A lane has U aligned blocks of the row (parts of one at its
+// for short rows without a sum along them: 25032 slots of 117 took 18), because
+// each of a token's rows wants the token at another shift; the token is read k
+// times, from L1 and L2 after the first.  A lane has U aligned blocks of the row (parts of one at its
 // ends) and the windows that belong to them in flight (with two windows a block,
 // two blocks of BF16: 8192 x 7001 top-6 296 us, with one 314; one of FP32: 1021
 // x 1001 top-5 14.9 us, with two 18.1).
@@ -545,6 +545,10 @@ template <typename T> cudaError_t combine_type(const LaunchCtx &c, const Combine
 
 template <typename T, bool DOT> cudaError_t scatter_type(const LaunchCtx &c, ScatterArgs a)
 {
+    // CTAs an expert's padding rows are shared by.  Few leave a long tail where
+    // rows are long, many are mostly idle where they are short (pack, 8 against
+    // 32: 64 experts, 4096 x 4096 top-6 43.7, 41.5 us, 2048 x 1001 12.4, 14.0; 256
+    // experts top-8, 65.6, 63.1 and 18.9, 30.6).
     a.pad_split = a.E >= 256 ? 8 : 32;
     const unsigned pad = (unsigned)(a.E * a.pad_split);
     if (!(in_blocks(a.src, a.ld_src, a.H, sizeof(T)) && in_blocks(a.rows_out, a.H, a.H, sizeof(T)) &&
@@ -553,6 +557,11 @@ template <typename T, bool DOT> cudaError_t scatter_type(const LaunchCtx &c, Sca
         auto grid = [&](int per_cta) { return dim3((unsigned)((slots + per_cta - 1) / per_cta) + pad); };
         if (!DOT && a.H <= 16 * E<T>)
             return launch_pdl(scatter_any_kernel<T, false, 8>, grid(kThreads / 8), dim3(kThreads), 0, c.stream, a);
+        // A CTA a slot where a warp a slot would leave the SMs with less than two
+        // CTAs each.  That is where rows of a warp's many turns gain (gradient, 600
+        // slots of 3993: FP32 10.7 us on CTAs, 38.0 on warps, BF16 5.6, 16.2; 2432
+        // slots 21.0, 41.1 and 15.3, 20.5); rows of one or two turns lose a little
+        // (1200 slots of BF16: 1001 5.2, 4.7 us; 331 5.0, 3.2).
         if (slots < (int64_t)c.num_sms * 2 * (kThreads / 32))
             return launch_pdl(scatter_any_kernel<T, DOT, kThreads>, grid(1), dim3(kThreads), 0, c.stream, a);
         return launch_pdl(scatter_any_kernel<T, DOT, 32>, grid(kThreads / 32), dim3(kThreads), 0, c.stream, a);

@@ -46,7 +46,12 @@
 //    their own (17 warps leave 96 registers: 127 us).
 // Measured on GB300, 4096 x 4096 per expert, 64 experts top-8: one token 17.4 us
 // (76 MB, 4.4 TB/s, of which 4 us are the launch, the ids and x), 8 tokens 66 us
-// (5.5 TB/s of the rows in use), 32 tokens 110 us (5.5 TB/s).
+// (5.5 TB/s of the rows in use), 32 tokens 109 us (5.4 TB/s).  7168 x 4096: one
+// token 26.7 us (5.0 TB/s), 32 tokens 198 us (5.2 TB/s).
+// Every further 8 slots of an expert are another pass over its rows, which L2
+// may hold by then but which are converted and scaled again: one expert of 4096
+// x 16384 (floor 5.6 us) takes 13.7 us for 8 tokens, 18.9 for 16, 30.4 for 32 and
+// 97 for 128; 32 tokens top-2 of 8 experts of 4096 x 4096 30.8 us (floor 11.2).
 // The order of a row's sum depends on the call's shape (T, k, K, N, E) and the
 // number of SMs, by which the launcher chooses how many warps share a tile,
 // never on the routing: a slot's result does not depend on where the other
@@ -198,6 +203,9 @@ __device__ __forceinline__ uint2 lds64(uint32_t at)
     return v;
 }
 
+// The copy and barrier helpers on shared-memory addresses: a warp's place and
+// barrier move from step to step, and as generic pointers they would be converted
+// at every use.
 __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar)
 {
     asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes"

@@ -20,8 +20,13 @@
 // in flight while the current one is computed.
 //
 // Measured on GB300, 64 experts top-6, 16384 tokens, I = 2048: forward and
-// backward with the activation again 600 us (6.1 TB/s, 6.3 with the padding
-// rows); 8 experts top-2, 8192 tokens, I = 4096: 183 us (5.9 TB/s, 6.1).
+// backward with the activation again 599 us (6.1 TB/s, 6.3 with the padding
+// rows); 8 experts top-2, 8192 tokens, I = 4096: 183 us (5.9 TB/s, 6.1).  Where
+// I / 8 does not fill the threads side by side, those past the row's end compute
+// along with the others: I = 1536 5.2 TB/s, 2560 4.9, 2112 4.3 (73 % of the issue
+// slots in the forward pass, nearly half of them for nothing).  Far gates (below
+// -86) cost under 1 % up to one in 10^4; one in 100 takes the forward pass of 17000
+// x 4096 from 92 to 129 us and the backward pass from 91 to 194.
 #include "epq_device.cuh"
 #include "epq_internal.h"
 
@@ -216,7 +221,10 @@ __device__ __forceinline__ float2 scale_of(uint32_t sbyte)
 
 // Whether a gate of a block with this scale can lie below kFar (448 * 2^-3 = 56
 // is the largest element of the scale before), or an element of either at 2^128.
-__device__ __forceinline__ bool has_far(uint32_t sbyte_g, uint32_t sbyte_u) { return sbyte_g >= 125u || sbyte_u >= 247u; }
+__device__ __forceinline__ bool has_far(uint32_t sbyte_g, uint32_t sbyte_u)
+{
+    return sbyte_g >= 125u || sbyte_u >= 247u;
+}
 
 // The results of 8 columns with far gates or elements of 2^128 among them.
 // Kept out of line: it is rare.
@@ -225,7 +233,8 @@ struct Results {
     float top;
 };
 
-__device__ __noinline__ Results backward8_far(uint4 d, uint2 cg, uint2 cu, uint32_t sbyte_g, uint32_t sbyte_u, float top)
+__device__ __noinline__ Results backward8_far(uint4 d, uint2 cg, uint2 cu, uint32_t sbyte_g, uint32_t sbyte_u,
+                                              float top)
 {
     const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
     const uint32_t gw[4] = {cg.x & 0xffffu, cg.x >> 16, cg.y & 0xffffu, cg.y >> 16};

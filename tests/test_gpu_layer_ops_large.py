@@ -90,7 +90,8 @@ def test_one_token_with_long_rows(k, E, N, K):
     g = gen(70)
     topk = route(1, k, E, g)
     topk[0, 0] = E - 1
-    w_rows = nq.ep_nvfp4_pack_weights((torch.randn(E, N, K, generator=g, device="cuda") / math.sqrt(K)).to(torch.bfloat16))
+    w = torch.randn(E, N, K, generator=g, device="cuda") / math.sqrt(K)
+    w_rows = nq.ep_nvfp4_pack_weights(w.to(torch.bfloat16))
     x = torch.randn(1, K, generator=g, device="cuda")
     x[:, ::13] *= 2.0 ** -20
     x[:, K - 5:] *= 2.0 ** 6             # the last elements count
@@ -112,7 +113,8 @@ def test_weights_past_32_bit_offsets(T):
     assert (E - 1) * N * S > 1 << 32
     g = gen(71)
     w_rows = torch.zeros(E, N, S, dtype=torch.uint8, device="cuda")
-    w_rows[E - 1, N - last:] = nq.ep_nvfp4_pack_weights((torch.randn(1, last, K, generator=g, device="cuda") / 64).to(torch.bfloat16))[0]
+    w = torch.randn(1, last, K, generator=g, device="cuda") / 64
+    w_rows[E - 1, N - last:] = nq.ep_nvfp4_pack_weights(w.to(torch.bfloat16))[0]
     x = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
     topk = torch.tensor([[E - 1, 0]] * T, dtype=torch.int32, device="cuda")
     y = nq.ep_nvfp4_matvec(x, w_rows, topk).view(T, 2, N)

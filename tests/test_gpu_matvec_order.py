@@ -17,7 +17,8 @@ def test_a_slot_does_not_depend_on_the_others(T, k, E, N, K):
     """The same slot's row, bit for bit, wherever the other slots go (and with
     them its group, its column and the warps that compute it)."""
     g = gen(72)
-    w_rows = nq.ep_nvfp4_pack_weights((torch.randn(E, N, K, generator=g, device="cuda") / math.sqrt(K)).to(torch.bfloat16))
+    w = torch.randn(E, N, K, generator=g, device="cuda") / math.sqrt(K)
+    w_rows = nq.ep_nvfp4_pack_weights(w.to(torch.bfloat16))
     x = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
     t, j, e = T // 2, k - 1, E // 2
     kept = []
