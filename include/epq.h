@@ -360,6 +360,26 @@ ep_status ep_nvfp4_colwise_rht_bf16(const void *x_bf16, int64_t R_cap,
                                     uint32_t *dev_status, void *stream);
 
 /*
+ * ep_nvfp4_colwise_rht_bf16_swizzled -- ep_nvfp4_colwise_rht_bf16 with
+ * cw_scales in the tiled layout of block-scaled GEMM operands, as
+ * ep_nvfp4_direct_receive_swizzled writes them: expert e's [H, n_e/16] matrix
+ * at byte offsets[e]*H/16.  Everything else alike; H % 128 != 0 ->
+ * EP_ERR_SHAPE.
+ */
+ep_status ep_nvfp4_colwise_rht_bf16_swizzled(const void *x_bf16, int64_t R_cap,
+                                             int64_t H,
+                                             const int32_t *expert_offsets,
+                                             int E, const float *amax_in,
+                                             uint8_t *cw_codes,
+                                             uint8_t *cw_scales,
+                                             float *amax_row, float *amax_col,
+                                             float *cw_scale_enc, int rounding,
+                                             uint64_t seed,
+                                             uint16_t rht_sign_mask,
+                                             uint32_t *dev_status,
+                                             void *stream);
+
+/*
  * ep_mxfp8_pack -- MXFP8 variant of the pack with the same routing gather.
  * TE PR #3270, description: bfloat16 tokens are quantised to MXFP8 and
  * dispatched; sequence diagram: the quantisation step yields E4M3 data with
@@ -542,6 +562,150 @@ ep_status ep_nvfp4_matvec(const void *x_bf16, int64_t T, int64_t K,
                           int64_t ld_x, int x_per_slot, const uint8_t *w_rows,
                           int E, int64_t N, const int32_t *topk_idx, int k,
                           void *y_bf16, uint32_t *dev_status, void *stream);
+
+/*
+ * Matrix products grouped by expert, for batches.  Shared by the four calls:
+ *   expert_offsets  device int32 [E+1] as ep_route_plan makes them: expert e's
+ *                   rows are [offsets[e], offsets[e+1]), a whole number of
+ *                   128-row tiles.  A slot that is not raises
+ *                   EP_DEV_ERR_BAD_EXPERT and counts as empty; rows past R_cap
+ *                   raise EP_DEV_ERR_CAPACITY and are skipped.  NULL (E = 1):
+ *                   all R_cap rows, any number of them (a dense layer).
+ *   Sums in FP32 (tensor-core accumulators), each output rounded once.  An
+ *   output's sum runs over its K (or rows) in one order that depends on the
+ *   sizes alone.  No output overlaps an input.  Buffers and row pitches are
+ *   16-byte aligned.  R_cap = 0 is allowed.  Sizes: N, K <= 2^20, and fewer
+ *   than 2^31 output tiles of 128 x 256 (EP_ERR_CAPACITY).
+ *
+ * ep_grouped_gemm -- the expert products and the gradient of their rows:
+ *   transposed = 0:  out[r][n] = sum over k of w[e][n][k] * x[r][k]
+ *   transposed = 1:  out[r][n] = sum over k of w[e][k][n] * x[r][k]
+ * for the rows r of expert e.  With transposed = 1, x the gradient of the
+ * outputs and w the forward weights (so K and N trade places), it is the
+ * gradient of the rows.
+ *   x_bf16          device bf16 [R_cap, K], row pitch ld_x elements (a multiple
+ *                   of 8).  A row reaches its own output row only.
+ *   w_bf16          device bf16 [E, N, K], or [E, K, N] with transposed.
+ *   out_bf16        device bf16 [R_cap, N]; rows [0, R) are written, padding
+ *                   rows from what x holds there (zeros give zeros).
+ * N % 8 == 0, K % 8 == 0.
+ */
+ep_status ep_grouped_gemm(const void *x_bf16, int64_t R_cap, int64_t K,
+                          int64_t ld_x, const void *w_bf16, int E, int64_t N,
+                          int transposed, const int32_t *expert_offsets,
+                          void *out_bf16, uint32_t *dev_status, void *stream);
+
+/*
+ * ep_grouped_wgrad -- the gradient of the expert weights:
+ *   d_w[e][n][k] = sum over e's rows r of dy[r][n] * x[r][k].
+ *   dy_bf16, x_bf16 device bf16 [R_cap, N] and [R_cap, K], row pitches ld_dy,
+ *                   ld_x elements (multiples of 8).
+ *   expert_counts   device int32 [E] or NULL.  With it (as ep_route_plan makes
+ *                   it) only the first expert_counts[e] rows of a slot enter,
+ *                   whatever the padding rows hold; NULL: all rows of the
+ *                   slot, which is the same while padding rows are zero, as
+ *                   every call here leaves them.
+ *   d_w             device [E, N, K] of `dtype` (EP_DTYPE_F32 or EP_DTYPE_BF16).
+ *                   Written whole: an expert without rows gets zeros.
+ *   accumulate      EP_DTYPE_F32 only (EP_ERR_ARG): the sums are added to what
+ *                   d_w holds, one FP32 addition an element.
+ * N % 8 == 0, K % 8 == 0.
+ */
+ep_status ep_grouped_wgrad(const void *dy_bf16, int64_t ld_dy,
+                           const void *x_bf16, int64_t ld_x, int64_t R_cap,
+                           int64_t N, int64_t K, const int32_t *expert_offsets,
+                           const int32_t *expert_counts, int E, void *d_w,
+                           int dtype, int accumulate, uint32_t *dev_status,
+                           void *stream);
+
+/* Bytes of the tiled block scales of `rows` packed rows of H elements:
+ * ceil(rows / 128) * ceil(H / 64) tiles of 512. */
+size_t ep_nvfp4_scale_bytes(int64_t rows, int64_t H);
+
+/*
+ * ep_nvfp4_operand -- packed rows as an operand of ep_nvfp4_grouped_gemm
+ * without the columnwise half of a direct receive: the block scales in 128 x 4
+ * tiles and the row scales; the codes are read from the rows themselves (codes
+ * pointer = rows, pitch = ep_nvfp4_row_bytes(H)).  For weights, and for rows
+ * whose weight gradient is not wanted.
+ *   rows            device u8 [groups * rows_per_group, S] (ep_nvfp4_pack
+ *                   layout).
+ *   groups          1 for rows; E for weights [E, N, S], each expert's rows
+ *                   tiled for themselves (rows_per_group = N).
+ *   expert_offsets  device int32 [E+1] or NULL (E = 1).  With it (groups = 1)
+ *                   the rows [0, offsets[E]) are taken; NULL: all.
+ *   scales          device u8 [groups][ceil(rows_per_group / 128)]
+ *                   [ceil(H / 64)][512]: tiles as in
+ *                   ep_nvfp4_direct_receive_swizzled; what overhangs in a
+ *                   tile, along the rows or along H, is zero.
+ *   row_scale       device f32 [groups * rows_per_group].
+ */
+ep_status ep_nvfp4_operand(const uint8_t *rows, int64_t groups,
+                           int64_t rows_per_group, int64_t H,
+                           const int32_t *expert_offsets, int E,
+                           uint8_t *scales, float *row_scale,
+                           uint32_t *dev_status, void *stream);
+
+/*
+ * ep_nvfp4_grouped_gemm -- the expert products of NVFP4 rows with NVFP4
+ * weights:
+ *   out[r][n] = sx[r] * sw[e][n] * sum over k of x[r][k] * w[e][n][k],
+ * x and w the codes times their block scales, sx and sw the row scales.
+ *   x_codes         device u8, row r's K/2 bytes of codes at r * ld_x.
+ *   x_scales        device u8, tiled block scales of [R_cap, K/16].
+ *   x_row_scale     device f32 [R_cap].
+ *                   These are rw_codes (ld_x = K/2), rw_scales and
+ *                   rw_row_scale of ep_nvfp4_direct_receive_swizzled, or the
+ *                   packed rows and the outputs of ep_nvfp4_operand.
+ *   w_codes         device u8, output feature n of expert e at (e*N + n) * ld_w.
+ *   w_scales        device u8 [E][ceil(N/128)][ceil(K/64)][512].
+ *   w_row_scale     device f32 [E * N].
+ *   out_bf16        device bf16 [R_cap, N]; rows [0, R) are written.
+ * The data's gradient is the same call with the transposed weights packed.
+ * The sum times sw is formed first and can overflow alone.
+ * N % 8 == 0, K % 32 == 0; ld_x, ld_w multiples of 16.
+ */
+ep_status ep_nvfp4_grouped_gemm(const uint8_t *x_codes, int64_t ld_x,
+                                const uint8_t *x_scales,
+                                const float *x_row_scale, int64_t R_cap,
+                                int64_t K, const uint8_t *w_codes,
+                                int64_t ld_w, const uint8_t *w_scales,
+                                const float *w_row_scale, int E, int64_t N,
+                                const int32_t *expert_offsets, void *out_bf16,
+                                uint32_t *dev_status, void *stream);
+
+/* Device workspace of ep_nvfp4_grouped_wgrad: 512 bytes an expert. */
+size_t ep_nvfp4_wgrad_workspace_bytes(int E);
+
+/*
+ * ep_nvfp4_grouped_wgrad -- the weight gradient from the columnwise operands:
+ *   d_w[e][n][k] = sum over e's rows of dy[n][r] * x[k][r] / (Sdy[e] * Sx[e]),
+ * dy and x the columnwise codes times their block scales.  Both sides carry
+ * the same transform of every 16 rows (same sign mask), which is orthogonal,
+ * so the sum is that of the rows before it.
+ *   dy_codes, dy_scales, dy_scale_enc: cw_codes, cw_scales, cw_scale_enc of
+ *                   ep_nvfp4_direct_receive_swizzled or
+ *                   ep_nvfp4_colwise_rht_bf16_swizzled for H = N;
+ *   x_codes, x_scales, x_scale_enc: the same for H = K.
+ *                   Without expert_offsets R_cap is a multiple of 128.
+ *   workspace       device, 128-byte aligned, ws_bytes >=
+ *                   ep_nvfp4_wgrad_workspace_bytes(E); needs no filling.  Calls
+ *                   that may overlap need one each.
+ *   d_w, dtype, accumulate: as in ep_grouped_wgrad.  An expert whose rows go
+ *                   past R_cap counts as empty as a whole.
+ * N % 128 == 0, K % 128 == 0.
+ */
+ep_status ep_nvfp4_grouped_wgrad(const uint8_t *dy_codes,
+                                 const uint8_t *dy_scales,
+                                 const float *dy_scale_enc,
+                                 const uint8_t *x_codes,
+                                 const uint8_t *x_scales,
+                                 const float *x_scale_enc, int64_t R_cap,
+                                 int64_t N, int64_t K,
+                                 const int32_t *expert_offsets, int E,
+                                 void *workspace, size_t ws_bytes, void *d_w,
+                                 int dtype, int accumulate,
+                                 uint32_t *dev_status, void *stream);
 
 /* Human-readable name of a status code. */
 const char *ep_status_string(int status);

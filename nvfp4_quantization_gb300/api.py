@@ -239,10 +239,12 @@ def ep_nvfp4_direct_receive(rows: torch.Tensor, H: int, offsets: torch.Tensor, E
 def ep_nvfp4_colwise_rht_bf16(x: torch.Tensor, offsets: torch.Tensor, E: int, amax: torch.Tensor,
                               out: dict | None = None, rounding: int = EP_ROUND_RNE, seed: int = 0,
                               sign_mask: int = DEFAULT_SIGN_MASK, status: torch.Tensor | None = None,
-                              stream=None) -> dict:
+                              stream=None, swizzled: bool = False) -> dict:
     """Expert-grouped BF16 rows [R_cap, H] + supplied per-expert amax [E]
     (f32) -> the columnwise RHT operand and its metadata (keys cw_codes,
-    cw_scales, amax_row, amax_col, cw_scale_enc)."""
+    cw_scales, amax_row, amax_col, cw_scale_enc).  ``swizzled`` calls
+    ep_nvfp4_colwise_rht_bf16_swizzled: the scales in the tiled layout that
+    ep_nvfp4_grouped_wgrad reads (H % 128 == 0)."""
     _need_cuda(x, "x", torch.bfloat16)
     _need_cuda(amax, "amax", torch.float32)
     R_cap, H = x.shape
@@ -255,11 +257,12 @@ def ep_nvfp4_colwise_rht_bf16(x: torch.Tensor, offsets: torch.Tensor, E: int, am
                "cw_scale_enc": torch.empty(E, dtype=torch.float32, device=dev)}
     if status is None:
         status = new_status(dev)
-    st = _lib.lib().ep_nvfp4_colwise_rht_bf16(_ptr(x), R_cap, H, _ptr(offsets), E, _ptr(amax), _ptr(out["cw_codes"]),
-                                              _ptr(out["cw_scales"]), _ptr(out["amax_row"]), _ptr(out["amax_col"]),
-                                              _ptr(out["cw_scale_enc"]), int(rounding), int(seed) & ((1 << 64) - 1),
-                                              int(sign_mask) & 0xFFFF, _ptr(status), _stream(stream))
-    check("ep_nvfp4_colwise_rht_bf16", st)
+    name = "ep_nvfp4_colwise_rht_bf16_swizzled" if swizzled else "ep_nvfp4_colwise_rht_bf16"
+    st = getattr(_lib.lib(), name)(_ptr(x), R_cap, H, _ptr(offsets), E, _ptr(amax), _ptr(out["cw_codes"]),
+                                   _ptr(out["cw_scales"]), _ptr(out["amax_row"]), _ptr(out["amax_col"]),
+                                   _ptr(out["cw_scale_enc"]), int(rounding), int(seed) & ((1 << 64) - 1),
+                                   int(sign_mask) & 0xFFFF, _ptr(status), _stream(stream))
+    check(name, st)
     return out
 
 
@@ -619,3 +622,209 @@ def ep_nvfp4_matvec(x: torch.Tensor, w_rows: torch.Tensor, topk_idx: torch.Tenso
     if st:
         check("ep_nvfp4_matvec", st)
     return y
+
+
+# ---------------------------------------------------------------------------
+# the expert products of a batch
+# ---------------------------------------------------------------------------
+def ep_grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor | None = None, transpose: bool = False,
+                    out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows of expert e times its weights, BF16: ``out[r] = w[e] @ x[r]``,
+    [R_cap, N], for x [R_cap, K] and w [E, N, K].
+
+    ``transpose=True``: ``out[r] = w[e].T @ x[r]`` for w [E, K, N], the gradient
+    of the rows when x is the gradient of the outputs.  ``offsets`` (int32
+    [E+1]) as ep_route_plan makes them; without them E must be 1 and all rows
+    are taken (a dense layer).  Rows behind offsets[E] are left as they were."""
+    ld = _need_rows(x, "x", (torch.bfloat16,))
+    R_cap, K = x.shape
+    dev = x.device
+    if w.dim() != 3:
+        raise ValueError("w must have three dimensions")
+    E, N = w.shape[0], w.shape[2 if transpose else 1]
+    _need_dense(w, "w", (E, K, N) if transpose else (E, N, K), torch.bfloat16)
+    _need_offsets(offsets, E)
+    if out is None:
+        out = _empty((R_cap, N), torch.bfloat16, dev, stream)
+    else:
+        _need_dense(out, "out", (R_cap, N), torch.bfloat16)
+    status = _status_or_new(status, dev, stream)
+    st = _lib.lib().ep_grouped_gemm(x.data_ptr(), R_cap, K, ld, w.data_ptr(), E, N, int(transpose), _at(offsets),
+                                    out.data_ptr(), status.data_ptr(), _stream_of(stream, dev))
+    if st:
+        check("ep_grouped_gemm", st)
+    return out
+
+
+def _weight_gradient(d_w, shape: tuple, dtype, accumulate: bool, dev, stream):
+    if d_w is None:
+        if accumulate:
+            raise ValueError("accumulate needs d_w")
+        d_w = _empty(shape, dtype, dev, stream)
+    if d_w.dtype not in _DTYPE:
+        raise ValueError(f"d_w must be one of {', '.join(str(d) for d in _DTYPE)}, got {d_w.dtype}")
+    _need_dense(d_w, "d_w", shape, d_w.dtype)
+    return d_w
+
+
+def ep_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor | None = None, E: int = 1,
+                     counts: torch.Tensor | None = None, d_w: torch.Tensor | None = None,
+                     dtype: torch.dtype = torch.float32, accumulate: bool = False,
+                     status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of the expert weights, [E, N, K]: ``d_w[e] = dy[rows].T @ x[rows]``
+    over expert e's rows of dy [R_cap, N] and x [R_cap, K] (BF16).
+
+    FP32 or BF16, by ``d_w`` or ``dtype``; ``accumulate`` adds to an FP32
+    ``d_w``.  With ``counts`` (int32 [E], the plan's) padding rows do not enter,
+    whatever they hold; without it they have to be zero, as every call here
+    leaves them.  ``offsets`` and E as in ep_swiglu."""
+    ld_dy = _need_rows(dy, "dy", (torch.bfloat16,))
+    ld_x = _need_rows(x, "x", (torch.bfloat16,))
+    R_cap, N = dy.shape
+    K, dev = x.shape[1], dy.device
+    if x.shape[0] != R_cap:
+        raise ValueError(f"dy and x must have the same rows, got {R_cap} and {x.shape[0]}")
+    _need_offsets(offsets, E)
+    if counts is not None:
+        _need_int32(counts, "counts", E)
+    d_w = _weight_gradient(d_w, (E, N, K), dtype, accumulate, dev, stream)
+    status = _status_or_new(status, dev, stream)
+    st = _lib.lib().ep_grouped_wgrad(dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, R_cap, N, K, _at(offsets), _at(counts),
+                                     E, d_w.data_ptr(), _DTYPE[d_w.dtype], int(accumulate), status.data_ptr(),
+                                     _stream_of(stream, dev))
+    if st:
+        check("ep_grouped_wgrad", st)
+    return d_w
+
+
+def nvfp4_scale_bytes(rows: int, H: int) -> int:
+    """Bytes of the tiled block scales of ``rows`` packed rows of H elements."""
+    return -(-rows // 128) * -(-H // 64) * 512
+
+
+def ep_nvfp4_operand(rows: torch.Tensor, H: int, offsets: torch.Tensor | None = None, E: int = 1,
+                     scales: torch.Tensor | None = None, row_scale: torch.Tensor | None = None,
+                     status: torch.Tensor | None = None, stream=None) -> dict:
+    """Packed NVFP4 rows as an operand of ep_nvfp4_grouped_gemm: keys rw_codes (a
+    view of the rows), rw_scales (tiled) and rw_row_scale.
+
+    ``rows`` uint8 [R_cap, row_bytes(H)], of which [0, offsets[E]) are taken
+    (all without ``offsets``), or weights [E, N, row_bytes(H)] as
+    ep_nvfp4_pack_weights makes them (no ``offsets``)."""
+    if not rows.is_cuda:
+        raise ValueError("rows must be a CUDA tensor")
+    S = (9 * H // 16 + 31) // 16 * 16                          # row_bytes(H)
+    if rows.dim() not in (2, 3):
+        raise ValueError("rows must have two or three dimensions")
+    _need_dense(rows, "rows", tuple(rows.shape[:-1]) + (S,), torch.uint8)
+    groups, n = (1, rows.shape[0]) if rows.dim() == 2 else (rows.shape[0], rows.shape[1])
+    if rows.dim() == 3 and (offsets is not None or E != 1):
+        raise ValueError("weights take no offsets")
+    _need_offsets(offsets, E)
+    dev = rows.device
+    nbytes = groups * nvfp4_scale_bytes(n, H)
+    if scales is None:
+        scales = _empty((nbytes,), torch.uint8, dev, stream)
+    else:
+        _need_dense(scales, "scales", (nbytes,), torch.uint8)
+    shape = tuple(rows.shape[:-1])
+    if row_scale is None:
+        row_scale = _empty(shape, torch.float32, dev, stream)
+    else:
+        _need_dense(row_scale, "row_scale", shape, torch.float32)
+    status = _status_or_new(status, dev, stream)
+    st = _lib.lib().ep_nvfp4_operand(rows.data_ptr(), groups, n, H, _at(offsets), E, scales.data_ptr(),
+                                     row_scale.data_ptr(), status.data_ptr(), _stream_of(stream, dev))
+    if st:
+        check("ep_nvfp4_operand", st)
+    return {"rw_codes": rows[..., : H // 2], "rw_scales": scales, "rw_row_scale": row_scale}
+
+
+def _need_bytes(t: torch.Tensor, name: str, n: int):
+    if t.dtype != torch.uint8 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous uint8 tensor with at least {n} bytes")
+
+
+def _need_f32(t: torch.Tensor, name: str, n: int):
+    if t.dtype != torch.float32 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor with at least {n} entries")
+
+
+def ep_nvfp4_grouped_gemm(x: dict, w: dict, offsets: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                          status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows of expert e times its weights, both NVFP4: BF16 [R_cap, N].
+
+    ``x``: the rowwise operand of R_cap rows (keys rw_codes, rw_scales in tiles,
+    rw_row_scale), from ep_nvfp4_direct_receive(..., swizzled=True) or
+    ep_nvfp4_operand.  ``w``: the operand of weights [E, N, K], from
+    ep_nvfp4_operand.  The gradient of the rows is the same call with the packed
+    transposed weights.  ``offsets`` and the rows as in ep_grouped_gemm."""
+    xc, wc = x["rw_codes"], w["rw_codes"]
+    ld_x = _need_rows(xc, 'x["rw_codes"]', (torch.uint8,))
+    R_cap, K = xc.shape[0], 2 * xc.shape[1]
+    dev = xc.device
+    if wc.dim() != 3 or wc.dtype != torch.uint8 or wc.shape[2] != xc.shape[1]:
+        raise ValueError(f'w["rw_codes"] must be uint8 [E, N, {xc.shape[1]}], got {wc.dtype} {tuple(wc.shape)}')
+    E, N = wc.shape[:2]
+    ld_w = wc.stride(1) if N > 1 else wc.stride(0) if E > 1 else max(K // 2, 1)
+    if (K > 2 and wc.stride(2) != 1) or (E > 1 and wc.stride(0) != N * ld_w) or ld_w < K // 2:
+        raise ValueError('w["rw_codes"] must have contiguous rows at one distance')
+    # blocks of 128 rows that the call may read; without offsets the last may be cut
+    blocks = R_cap // 128 if offsets is not None else -(-R_cap // 128)
+    _need_bytes(x["rw_scales"], 'x["rw_scales"]', blocks * -(-K // 64) * 512)
+    _need_f32(x["rw_row_scale"], 'x["rw_row_scale"]', R_cap)
+    _need_bytes(w["rw_scales"], 'w["rw_scales"]', E * nvfp4_scale_bytes(N, K))
+    _need_f32(w["rw_row_scale"], 'w["rw_row_scale"]', E * N)
+    _need_offsets(offsets, E)
+    if out is None:
+        out = _empty((R_cap, N), torch.bfloat16, dev, stream)
+    else:
+        _need_dense(out, "out", (R_cap, N), torch.bfloat16)
+    status = _status_or_new(status, dev, stream)
+    st = _lib.lib().ep_nvfp4_grouped_gemm(xc.data_ptr(), ld_x, x["rw_scales"].data_ptr(), x["rw_row_scale"].data_ptr(),
+                                          R_cap, K, wc.data_ptr(), ld_w, w["rw_scales"].data_ptr(),
+                                          w["rw_row_scale"].data_ptr(), E, N, _at(offsets), out.data_ptr(),
+                                          status.data_ptr(), _stream_of(stream, dev))
+    if st:
+        check("ep_nvfp4_grouped_gemm", st)
+    return out
+
+
+def ep_nvfp4_grouped_wgrad(dy: dict, x: dict, N: int, K: int, offsets: torch.Tensor | None = None, E: int = 1,
+                           d_w: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+                           accumulate: bool = False, workspace: torch.Tensor | None = None,
+                           status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of the expert weights, [E, N, K], from the columnwise NVFP4
+    operands of dy (N columns) and x (K columns): keys cw_codes, cw_scales in
+    tiles, cw_scale_enc, as ep_nvfp4_direct_receive and
+    ep_nvfp4_colwise_rht_bf16 make them with ``swizzled=True`` and one sign
+    mask.
+
+    ``d_w``, ``dtype``, ``accumulate`` as in ep_grouped_wgrad.  ``workspace``
+    (uint8, 512 bytes an expert): calls that may overlap need one each; made
+    here without it."""
+    codes = dy["cw_codes"]
+    if not codes.is_cuda:
+        raise ValueError('dy["cw_codes"] must be a CUDA tensor')
+    if N < 1 or K < 1 or codes.numel() * 2 % N:
+        raise ValueError(f'dy["cw_codes"] does not hold rows of {N} columns')
+    R_cap, dev = codes.numel() * 2 // N, codes.device
+    for op, name, H in ((dy, "dy", N), (x, "x", K)):
+        _need_dense(op["cw_codes"], f'{name}["cw_codes"]', (R_cap * H // 2,), torch.uint8)
+        _need_bytes(op["cw_scales"], f'{name}["cw_scales"]', R_cap * H // 16)
+        _need_f32(op["cw_scale_enc"], f'{name}["cw_scale_enc"]', E)
+    _need_offsets(offsets, E)
+    d_w = _weight_gradient(d_w, (E, N, K), dtype, accumulate, dev, stream)
+    if workspace is None:
+        workspace = _empty((512 * E,), torch.uint8, dev, stream)
+    else:
+        _need_bytes(workspace, "workspace", 512 * E)
+    status = _status_or_new(status, dev, stream)
+    st = _lib.lib().ep_nvfp4_grouped_wgrad(codes.data_ptr(), dy["cw_scales"].data_ptr(), dy["cw_scale_enc"].data_ptr(),
+                                           x["cw_codes"].data_ptr(), x["cw_scales"].data_ptr(),
+                                           x["cw_scale_enc"].data_ptr(), R_cap, N, K, _at(offsets), E,
+                                           workspace.data_ptr(), workspace.numel(), d_w.data_ptr(), _DTYPE[d_w.dtype],
+                                           int(accumulate), status.data_ptr(), _stream_of(stream, dev))
+    if st:
+        check("ep_nvfp4_grouped_wgrad", st)
+    return d_w

@@ -19,8 +19,8 @@ CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = BUILD / "libepq.so"
 SOURCES = ["api.cu", "route.cu", "route_noalloc.cu", "pack.cu", "unpack.cu", "receive.cu", "colwise_bf16.cu",
-           "combine.cu", "swiglu.cu", "matvec.cu", "tensor_map.cu"]
-HEADERS = ["epq_device.cuh", "epq_internal.h"]
+           "combine.cu", "swiglu.cu", "matvec.cu", "grouped_bf16.cu", "grouped_nvfp4.cu", "tensor_map.cu"]
+HEADERS = ["epq_device.cuh", "epq_internal.h", "umma.cuh", "grouped.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

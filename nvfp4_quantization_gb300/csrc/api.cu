@@ -229,15 +229,16 @@ ep_status ep_nvfp4_dispatch(const int32_t *topk_idx, const void *tokens_bf16, in
     return cuda_status(err);
 }
 
-ep_status ep_nvfp4_colwise_rht_bf16(const void *x_bf16, int64_t R_cap, int64_t H, const int32_t *expert_offsets,
+static ep_status colwise_rht_bf16_common(const void *x_bf16, int64_t R_cap, int64_t H, const int32_t *expert_offsets,
                                     int E, const float *amax_in, uint8_t *cw_codes, uint8_t *cw_scales,
                                     float *amax_row, float *amax_col, float *cw_scale_enc, int rounding,
-                                    uint64_t seed, uint16_t rht_sign_mask, uint32_t *dev_status, void *stream)
+                                    uint64_t seed, uint16_t rht_sign_mask, uint32_t *dev_status, void *stream,
+                                    bool tiled)
 {
     if (!x_bf16 || !expert_offsets || !amax_in || !cw_codes || !cw_scales || !amax_row || !amax_col ||
         !cw_scale_enc || !dev_status)
         return EP_ERR_NULL;
-    if (!shape_ok(0, H, 1, E))
+    if (!shape_ok(0, H, 1, E) || (tiled && H % 128 != 0))
         return EP_ERR_SHAPE;
     if (R_cap < 0 || R_cap > (int64_t)INT32_MAX || R_cap * H / 2 > (int64_t)INT32_MAX * 16)
         return EP_ERR_CAPACITY;
@@ -256,7 +257,26 @@ ep_status ep_nvfp4_colwise_rht_bf16(const void *x_bf16, int64_t R_cap, int64_t H
     LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
     return cuda_status(epq::launch_colwise_rht_bf16(c, (const uint16_t *)x_bf16, (int)R_cap, (int)H, expert_offsets,
                                                     E, amax_in, cw_codes, cw_scales, amax_row, amax_col,
-                                                    cw_scale_enc, rounding, seed, rht_sign_mask, dev_status));
+                                                    cw_scale_enc, rounding, seed, rht_sign_mask, dev_status, tiled));
+}
+
+ep_status ep_nvfp4_colwise_rht_bf16(const void *x_bf16, int64_t R_cap, int64_t H, const int32_t *expert_offsets,
+                                    int E, const float *amax_in, uint8_t *cw_codes, uint8_t *cw_scales,
+                                    float *amax_row, float *amax_col, float *cw_scale_enc, int rounding,
+                                    uint64_t seed, uint16_t rht_sign_mask, uint32_t *dev_status, void *stream)
+{
+    return colwise_rht_bf16_common(x_bf16, R_cap, H, expert_offsets, E, amax_in, cw_codes, cw_scales, amax_row,
+                                   amax_col, cw_scale_enc, rounding, seed, rht_sign_mask, dev_status, stream, false);
+}
+
+ep_status ep_nvfp4_colwise_rht_bf16_swizzled(const void *x_bf16, int64_t R_cap, int64_t H,
+                                             const int32_t *expert_offsets, int E, const float *amax_in,
+                                             uint8_t *cw_codes, uint8_t *cw_scales, float *amax_row, float *amax_col,
+                                             float *cw_scale_enc, int rounding, uint64_t seed, uint16_t rht_sign_mask,
+                                             uint32_t *dev_status, void *stream)
+{
+    return colwise_rht_bf16_common(x_bf16, R_cap, H, expert_offsets, E, amax_in, cw_codes, cw_scales, amax_row,
+                                   amax_col, cw_scale_enc, rounding, seed, rht_sign_mask, dev_status, stream, true);
 }
 
 ep_status ep_mxfp8_colwise(const void *x_bf16, int64_t R_cap, int64_t H, const int32_t *expert_offsets, int E,
@@ -572,6 +592,242 @@ ep_status ep_swiglu_backward(const void *d_act_bf16, int64_t ld_act, const uint8
     a.expert_amax = expert_amax;
     a.status = dev_status;
     return cuda_status(epq::launch_swiglu_backward(c, a));
+}
+
+// Sizes of the grouped products: their row tiles and output tiles are counted
+// in 32 bits.
+static bool product_ok(int64_t N, int64_t K, int E, int unit_n, int unit_k)
+{
+    return N >= unit_n && N <= (1 << 20) && N % unit_n == 0 && K >= unit_k && K <= (1 << 20) && K % unit_k == 0 &&
+           E >= 1 && E <= 1024;
+}
+
+static bool tiles_ok(int64_t M, int64_t N_tiles) { return (M + 127) / 128 * N_tiles <= (int64_t)INT32_MAX; }
+
+ep_status ep_grouped_gemm(const void *x_bf16, int64_t R_cap, int64_t K, int64_t ld_x, const void *w_bf16, int E,
+                          int64_t N, int transposed, const int32_t *expert_offsets, void *out_bf16,
+                          uint32_t *dev_status, void *stream)
+{
+    if (!dev_status || (R_cap > 0 && (!x_bf16 || !w_bf16 || !out_bf16)))
+        return EP_ERR_NULL;
+    if (!product_ok(N, K, E, 8, 8) || !pitch_ok(ld_x, K) || (!expert_offsets && E != 1))
+        return EP_ERR_SHAPE;
+    if (R_cap < 0 || R_cap > (int64_t)INT32_MAX || !tiles_ok(N, (R_cap + 255) / 256 + E))
+        return EP_ERR_CAPACITY;
+    if (!aligned16(x_bf16) || ld_x % 8 != 0 || !aligned16(w_bf16) || !aligned16(out_bf16))
+        return EP_ERR_ALIGN;
+    const int dev = device_of(R_cap > 0 ? x_bf16 : (const void *)dev_status);
+    if (dev < 0 || !on_device(w_bf16, dev) || !on_device(expert_offsets, dev) || !on_device(out_bf16, dev) ||
+        !on_device(dev_status, dev))
+        return EP_ERR_DEVICE;
+    DeviceGuard g(dev);
+    if (!g.ok)
+        return EP_ERR_DEVICE;
+    LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
+    epq::GroupedGemmArgs a = {};
+    a.x = x_bf16;
+    a.ld_x = ld_x;
+    a.w = w_bf16;
+    a.transposed = transposed != 0;
+    a.offsets = expert_offsets;
+    a.out = out_bf16;
+    a.R_cap = (int)R_cap;
+    a.E = E;
+    a.K = (int)K;
+    a.N = (int)N;
+    a.status = dev_status;
+    return cuda_status(epq::launch_grouped_gemm(c, a));
+}
+
+// Checks that the weight gradients share.
+static ep_status wgrad_checks(int64_t R_cap, int64_t N, int64_t K, int E, int unit, const int32_t *offsets,
+                              const void *d_w, int dtype, int accumulate, const uint32_t *dev_status)
+{
+    if (!dev_status || !d_w)
+        return EP_ERR_NULL;
+    if (!product_ok(N, K, E, unit, unit) || (!offsets && E != 1))
+        return EP_ERR_SHAPE;
+    if (R_cap < 0 || R_cap > (int64_t)INT32_MAX || !tiles_ok(N, E * ((K + 255) / 256)))
+        return EP_ERR_CAPACITY;
+    if (!dtype_ok(dtype) || (accumulate && dtype != EP_DTYPE_F32))
+        return EP_ERR_ARG;
+    return aligned16(d_w) ? EP_OK : EP_ERR_ALIGN;
+}
+
+ep_status ep_grouped_wgrad(const void *dy_bf16, int64_t ld_dy, const void *x_bf16, int64_t ld_x, int64_t R_cap,
+                           int64_t N, int64_t K, const int32_t *expert_offsets, const int32_t *expert_counts, int E,
+                           void *d_w, int dtype, int accumulate, uint32_t *dev_status, void *stream)
+{
+    if (R_cap > 0 && (!dy_bf16 || !x_bf16))
+        return EP_ERR_NULL;
+    const ep_status st = wgrad_checks(R_cap, N, K, E, 8, expert_offsets, d_w, dtype, accumulate, dev_status);
+    if (st != EP_OK)
+        return st;
+    if (!pitch_ok(ld_dy, N) || !pitch_ok(ld_x, K))
+        return EP_ERR_SHAPE;
+    if (!aligned16(dy_bf16) || ld_dy % 8 != 0 || !aligned16(x_bf16) || ld_x % 8 != 0 || !aligned_to(expert_counts, 4))
+        return EP_ERR_ALIGN;
+    const int dev = device_of(d_w);
+    if (dev < 0 || !on_device(dy_bf16, dev) || !on_device(x_bf16, dev) || !on_device(expert_offsets, dev) ||
+        !on_device(expert_counts, dev) || !on_device(dev_status, dev))
+        return EP_ERR_DEVICE;
+    DeviceGuard g(dev);
+    if (!g.ok)
+        return EP_ERR_DEVICE;
+    LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
+    epq::GroupedWgradArgs a = {};
+    a.dy = dy_bf16;
+    a.ld_dy = ld_dy;
+    a.x = x_bf16;
+    a.ld_x = ld_x;
+    a.offsets = expert_offsets;
+    a.counts = expert_counts;
+    a.d_w = d_w;
+    a.R_cap = (int)R_cap;
+    a.E = E;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.f32 = dtype == EP_DTYPE_F32;
+    a.add = accumulate != 0;
+    a.status = dev_status;
+    return cuda_status(epq::launch_grouped_wgrad(c, a));
+}
+
+size_t ep_nvfp4_scale_bytes(int64_t rows, int64_t H)
+{
+    return rows > 0 && H > 0 ? (size_t)((rows + 127) / 128 * ((H + 63) / 64) * 512) : 0;
+}
+
+ep_status ep_nvfp4_operand(const uint8_t *rows, int64_t groups, int64_t rows_per_group, int64_t H,
+                           const int32_t *expert_offsets, int E, uint8_t *scales, float *row_scale,
+                           uint32_t *dev_status, void *stream)
+{
+    const bool any = groups > 0 && rows_per_group > 0;
+    if (!dev_status || (any && (!rows || !scales || !row_scale)))
+        return EP_ERR_NULL;
+    if (!shape_ok(0, H, 1, E) || (expert_offsets ? groups != 1 : E != 1))
+        return EP_ERR_SHAPE;
+    if (groups < 0 || rows_per_group < 0 || rows_per_group > (int64_t)INT32_MAX ||
+        (groups > 0 && rows_per_group > (int64_t)INT32_MAX / groups) ||
+        groups * ((rows_per_group + 127) / 128) > (int64_t)INT32_MAX)
+        return EP_ERR_CAPACITY;
+    if (!aligned16(rows) || !aligned16(scales) || !aligned_to(row_scale, 4))
+        return EP_ERR_ALIGN;
+    const int dev = device_of(any ? (const void *)rows : (const void *)dev_status);
+    if (dev < 0 || !on_device(expert_offsets, dev) || !on_device(scales, dev) || !on_device(row_scale, dev) ||
+        !on_device(dev_status, dev))
+        return EP_ERR_DEVICE;
+    DeviceGuard g(dev);
+    if (!g.ok)
+        return EP_ERR_DEVICE;
+    LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
+    epq::OperandArgs a = {};
+    a.rows = rows;
+    a.S = epq::row_bytes(H);
+    a.groups = groups;
+    a.per_group = rows_per_group;
+    a.offsets = expert_offsets;
+    a.E = E;
+    a.K = (int)H;
+    a.scales = scales;
+    a.row_scale = row_scale;
+    a.status = dev_status;
+    return cuda_status(epq::launch_operand(c, a));
+}
+
+ep_status ep_nvfp4_grouped_gemm(const uint8_t *x_codes, int64_t ld_x, const uint8_t *x_scales,
+                                const float *x_row_scale, int64_t R_cap, int64_t K, const uint8_t *w_codes,
+                                int64_t ld_w, const uint8_t *w_scales, const float *w_row_scale, int E, int64_t N,
+                                const int32_t *expert_offsets, void *out_bf16, uint32_t *dev_status, void *stream)
+{
+    if (!dev_status || (R_cap > 0 && (!x_codes || !x_scales || !x_row_scale || !w_codes || !w_scales || !w_row_scale ||
+                                      !out_bf16)))
+        return EP_ERR_NULL;
+    if (!product_ok(N, K, E, 8, 32) || !pitch_ok(ld_x, K / 2) || !pitch_ok(ld_w, K / 2) ||
+        (!expert_offsets && E != 1))
+        return EP_ERR_SHAPE;
+    if (R_cap < 0 || R_cap > (int64_t)INT32_MAX || !tiles_ok(N, (R_cap + 255) / 256 + E))
+        return EP_ERR_CAPACITY;
+    if (!aligned16(x_codes) || ld_x % 16 != 0 || !aligned16(x_scales) || !aligned_to(x_row_scale, 4) ||
+        !aligned16(w_codes) || ld_w % 16 != 0 || !aligned16(w_scales) || !aligned_to(w_row_scale, 4) ||
+        !aligned16(out_bf16))
+        return EP_ERR_ALIGN;
+    const int dev = device_of(R_cap > 0 ? (const void *)x_codes : (const void *)dev_status);
+    if (dev < 0 || !on_device(x_scales, dev) || !on_device(x_row_scale, dev) || !on_device(w_codes, dev) ||
+        !on_device(w_scales, dev) || !on_device(w_row_scale, dev) || !on_device(expert_offsets, dev) ||
+        !on_device(out_bf16, dev) || !on_device(dev_status, dev))
+        return EP_ERR_DEVICE;
+    DeviceGuard g(dev);
+    if (!g.ok)
+        return EP_ERR_DEVICE;
+    LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
+    epq::Nvfp4GemmArgs a = {};
+    a.x = x_codes;
+    a.x_scales = x_scales;
+    a.x_row = x_row_scale;
+    a.ld_x = ld_x;
+    a.w = w_codes;
+    a.w_scales = w_scales;
+    a.w_row = w_row_scale;
+    a.ld_w = ld_w;
+    a.offsets = expert_offsets;
+    a.out = out_bf16;
+    a.R_cap = (int)R_cap;
+    a.E = E;
+    a.K = (int)K;
+    a.N = (int)N;
+    a.status = dev_status;
+    return cuda_status(R_cap > 0 ? epq::launch_nvfp4_gemm(c, a) : cudaSuccess);
+}
+
+size_t ep_nvfp4_wgrad_workspace_bytes(int E) { return (size_t)epq::nvfp4_wgrad_workspace(E < 1 ? 1 : E); }
+
+ep_status ep_nvfp4_grouped_wgrad(const uint8_t *dy_codes, const uint8_t *dy_scales, const float *dy_scale_enc,
+                                 const uint8_t *x_codes, const uint8_t *x_scales, const float *x_scale_enc,
+                                 int64_t R_cap, int64_t N, int64_t K, const int32_t *expert_offsets, int E,
+                                 void *workspace, size_t ws_bytes, void *d_w, int dtype, int accumulate,
+                                 uint32_t *dev_status, void *stream)
+{
+    if (!dy_scale_enc || !x_scale_enc || !workspace ||
+        (R_cap > 0 && (!dy_codes || !dy_scales || !x_codes || !x_scales)))
+        return EP_ERR_NULL;
+    const ep_status st = wgrad_checks(R_cap, N, K, E, 128, expert_offsets, d_w, dtype, accumulate, dev_status);
+    if (st != EP_OK)
+        return st;
+    if (!expert_offsets && R_cap % 128 != 0)
+        return EP_ERR_SHAPE;
+    if (ws_bytes < (size_t)epq::nvfp4_wgrad_workspace(E))
+        return EP_ERR_CAPACITY;
+    if (!aligned16(dy_codes) || !aligned16(dy_scales) || !aligned_to(dy_scale_enc, 4) || !aligned16(x_codes) ||
+        !aligned16(x_scales) || !aligned_to(x_scale_enc, 4) || !aligned_to(workspace, 128))
+        return EP_ERR_ALIGN;
+    const int dev = device_of(d_w);
+    if (dev < 0 || !on_device(dy_codes, dev) || !on_device(dy_scales, dev) || !on_device(dy_scale_enc, dev) ||
+        !on_device(x_codes, dev) || !on_device(x_scales, dev) || !on_device(x_scale_enc, dev) ||
+        !on_device(expert_offsets, dev) || !on_device(workspace, dev) || !on_device(dev_status, dev))
+        return EP_ERR_DEVICE;
+    DeviceGuard g(dev);
+    if (!g.ok)
+        return EP_ERR_DEVICE;
+    LaunchCtx c{(cudaStream_t)stream, dev, sm_count(dev)};
+    epq::Nvfp4WgradArgs a = {};
+    a.dy = dy_codes;
+    a.dy_scales = dy_scales;
+    a.dy_enc = dy_scale_enc;
+    a.x = x_codes;
+    a.x_scales = x_scales;
+    a.x_enc = x_scale_enc;
+    a.offsets = expert_offsets;
+    a.workspace = workspace;
+    a.d_w = d_w;
+    a.R_cap = (int)R_cap;
+    a.E = E;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.f32 = dtype == EP_DTYPE_F32;
+    a.add = accumulate != 0;
+    a.status = dev_status;
+    return cuda_status(epq::launch_nvfp4_wgrad(c, a));
 }
 
 ep_status ep_nvfp4_matvec(const void *x_bf16, int64_t T, int64_t K, int64_t ld_x, int x_per_slot,

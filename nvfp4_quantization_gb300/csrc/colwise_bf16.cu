@@ -162,7 +162,7 @@ colwise_rht_bf16_kernel(const __grid_constant__ CUtensorMap tm_x, int H, int R_c
                         uint8_t *__restrict__ cw_codes, uint8_t *__restrict__ cw_scales, float *__restrict__ amax_row,
                         float *__restrict__ amax_col, float *__restrict__ scale_enc,
                         const __grid_constant__ PhiloxKey key, uint32_t sign_mask, uint32_t *__restrict__ status,
-                        const __grid_constant__ CbRcp rcp, int codes_v8)
+                        const __grid_constant__ CbRcp rcp, int codes_v8, int tiled)
 {
     extern __shared__ uint8_t cb_smem_raw[];
     CbSmem &sm = *reinterpret_cast<CbSmem *>((reinterpret_cast<uintptr_t>(cb_smem_raw) + 127) & ~(uintptr_t)127);
@@ -267,9 +267,12 @@ colwise_rht_bf16_kernel(const __grid_constant__ CUtensorMap tm_x, int H, int R_c
         uint8_t *d0 = cw_codes + (int64_t)off * (H / 2) + (int64_t)h0 * (n / 2) + rl / 2;
         st_global_32B(d0, c0[0], c0[1], c0[2], c0[3], codes_v8 != 0);
         st_global_32B(d0 + n / 2, c1[0], c1[1], c1[2], c1[3], codes_v8 != 0);
-        uint8_t *cs = cw_scales + (int64_t)off * (H / 16) + (int64_t)h0 * (n / 16) + rl / 16;
+        // four scales of a column: 64 rows, or a column's piece of a 128 x 4 tile
+        uint8_t *cs = cw_scales + (int64_t)off * (H / 16) +
+                      (tiled ? ((int64_t)(h0 >> 7) * (n / 64) + rl / 64) * 512 + (h0 & 31) * 16 + ((h0 & 127) >> 5) * 4
+                             : (int64_t)h0 * (n / 16) + rl / 16);
         *reinterpret_cast<uint32_t *>(cs) = pack4(s2[0] & 0xffu, s2[1] & 0xffu, s2[2] & 0xffu, s2[3] & 0xffu);
-        *reinterpret_cast<uint32_t *>(cs + n / 16) =
+        *reinterpret_cast<uint32_t *>(cs + (tiled ? 16 : n / 16)) =
             pack4((s2[0] >> 8) & 0xffu, (s2[1] >> 8) & 0xffu, (s2[2] >> 8) & 0xffu, (s2[3] >> 8) & 0xffu);
     }
     // never leave with a load of this warp's ring still in flight (after a
@@ -473,7 +476,7 @@ static CbRcp make_cb_rcp()
 cudaError_t launch_colwise_rht_bf16(const LaunchCtx &c, const uint16_t *x, int R_cap, int H, const int32_t *offsets,
                                     int E, const float *amax_in, uint8_t *cw_codes, uint8_t *cw_scales,
                                     float *amax_row, float *amax_col, float *scale_enc, int rounding, uint64_t seed,
-                                    uint32_t sign_mask, uint32_t *status)
+                                    uint32_t sign_mask, uint32_t *status, bool tiled)
 {
     static const CbRcp rcp = make_cb_rcp();
     // the input as a byte tensor [R_cap][2H]; a box is one unit, 64 rows x 128
@@ -498,7 +501,7 @@ cudaError_t launch_colwise_rht_bf16(const LaunchCtx &c, const uint16_t *x, int R
     const int v8 = (reinterpret_cast<uintptr_t>(cw_codes) & 31u) == 0;
     return launch_pdl(kern, dim3((unsigned)grid), dim3(kCbWarps * 32), smem, c.stream, tm_x, H, R_cap, offsets, E,
                       amax_in, cw_codes, cw_scales, amax_row, amax_col, scale_enc, philox_key(seed), sign_mask,
-                      status, rcp, v8);
+                      status, rcp, v8, (int)tiled);
 }
 
 } // namespace epq

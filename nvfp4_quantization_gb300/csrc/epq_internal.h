@@ -101,10 +101,12 @@ struct GroupedOut {
     float *scale_enc;
 };
 
+// tiled: the scales in the layout of block-scaled GEMM operands (H % 128 == 0,
+// checked by the caller).
 cudaError_t launch_colwise_rht_bf16(const LaunchCtx &c, const uint16_t *x, int R_cap, int H, const int32_t *offsets,
                                     int E, const float *amax_in, uint8_t *cw_codes, uint8_t *cw_scales,
                                     float *amax_row, float *amax_col, float *scale_enc, int rounding, uint64_t seed,
-                                    uint32_t sign_mask, uint32_t *status);
+                                    uint32_t sign_mask, uint32_t *status, bool tiled = false);
 
 cudaError_t launch_mxfp8_colwise(const LaunchCtx &c, const uint16_t *x, int R_cap, int H, const int32_t *offsets,
                                  int E, uint8_t *buf, uint32_t *status);
@@ -187,6 +189,83 @@ cudaError_t launch_matvec(const LaunchCtx &c, const MatvecArgs &a);
 // box_inner count 16-bit units instead.
 bool make_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t pitch,
               uint32_t box_inner, uint32_t box_outer, int elem = 1);
+
+// Tensor map of a 3-D tensor (dims[0] contiguous, pitches of the other two in
+// bytes), with a swizzle of 0, 64 or 128 bytes.
+enum class MapType { U8, Bf16, F32, I64 };
+bool make_map_3d(CUtensorMap *m, MapType type, const void *base, const uint64_t (&dims)[3],
+                 const uint64_t (&pitches)[2], const uint32_t (&box)[3], int swizzle);
+
+// y[r] = W_e x[r] for the rows of expert e; `transposed`: w is [E, K, N].
+struct GroupedGemmArgs {
+    const void *x;           // BF16 [R_cap, K], row pitch ld_x elements
+    int64_t ld_x;
+    const void *w;           // BF16 [E, N, K] or [E, K, N]
+    bool transposed;
+    const int32_t *offsets;  // [E + 1] or NULL: all R_cap rows, one expert
+    void *out;               // BF16 [R_cap, N]
+    int R_cap, E, K, N;
+    uint32_t *status;
+};
+
+cudaError_t launch_grouped_gemm(const LaunchCtx &c, const GroupedGemmArgs &a);
+
+// d_w[e] = sum over e's rows of dy[r] x[r]^T.
+struct GroupedWgradArgs {
+    const void *dy, *x;      // BF16 [R_cap, N] and [R_cap, K], row pitches ld_dy and ld_x elements
+    int64_t ld_dy, ld_x;
+    const int32_t *offsets;  // [E + 1] or NULL
+    const int32_t *counts;   // [E] or NULL: all rows of a slot
+    void *d_w;               // [E, N, K], FP32 or BF16
+    int R_cap, E, N, K;
+    bool f32, add;
+    uint32_t *status;
+};
+
+cudaError_t launch_grouped_wgrad(const LaunchCtx &c, const GroupedWgradArgs &a);
+
+// Packed rows -> tiled block scales and row scales.
+struct OperandArgs {
+    const uint8_t *rows;     // [groups * per_group, S]
+    int64_t S;
+    int64_t groups, per_group;
+    const int32_t *offsets;  // with one group: [E + 1] or NULL
+    int E, K;
+    uint8_t *scales;         // [groups][ceil(per_group / 128)][ceil(K / 64)][512]
+    float *row_scale;        // [groups * per_group]
+    uint32_t *status;
+};
+
+cudaError_t launch_operand(const LaunchCtx &c, const OperandArgs &a);
+
+struct Nvfp4GemmArgs {
+    const uint8_t *x, *x_scales;   // codes, row pitch ld_x bytes; tiled scales
+    const float *x_row;            // [R_cap]
+    int64_t ld_x;
+    const uint8_t *w, *w_scales;   // codes [E][N], row pitch ld_w bytes; tiled scales
+    const float *w_row;            // [E * N]
+    int64_t ld_w;
+    const int32_t *offsets;
+    void *out;                     // BF16 [R_cap, N]
+    int R_cap, E, K, N;
+    uint32_t *status;
+};
+
+cudaError_t launch_nvfp4_gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a);
+
+struct Nvfp4WgradArgs {
+    const uint8_t *dy, *dy_scales, *x, *x_scales;   // columnwise operands, tiled scales
+    const float *dy_enc, *x_enc;                    // [E]
+    const int32_t *offsets;                         // or NULL
+    void *workspace;                                // nvfp4_wgrad_workspace(E) bytes, 128-byte aligned
+    void *d_w;                                      // [E, N, K]
+    int R_cap, E, N, K;
+    bool f32, add;
+    uint32_t *status;
+};
+
+inline int64_t nvfp4_wgrad_workspace(int E) { return (int64_t)E * 4 * sizeof(CUtensorMap); }
+cudaError_t launch_nvfp4_wgrad(const LaunchCtx &c, const Nvfp4WgradArgs &a);
 
 // Bytes of a packed NVFP4 row: roundup16(9H/16 + 16).
 inline int64_t row_bytes(int64_t H) { return (9 * H / 16 + 16 + 15) / 16 * 16; }

@@ -1,0 +1,593 @@
+// Matrix products grouped by expert, on the tensor cores: the kernel behind
+// ep_grouped_gemm, ep_grouped_wgrad and their NVFP4 forms.
+//
+// Rows lie in expert order, expert e's in [off_e, off_e + n_e).  Two shapes:
+//   rows as N (kWgrad false):  y[r][m] = sum_k w_e[m][k] x[r][k].  The weights
+//     are the M side of the matrix instruction and the rows its N side, whose
+//     size may change from tile to tile: a slot of 128 rows costs 128, not 256.
+//   rows as K (kWgrad true):   d_w[e][m][n] = sum_r dy[r][m] x[r][n].
+//
+// A persistent kernel: one CTA a SM, tiles of 128 x kCtas by up to 256 dealt
+// out in turn.  Warp 0 feeds a ring of shared-memory stages by TMA (128 bytes
+// along K a row and stage: 64 BF16 or 256 E2M1), one thread of warp 1 issues
+// the matrix products into tensor memory, warps 4-7 take finished sums from
+// there to global memory while the next tile is computed in the other half of
+// tensor memory.
+#pragma once
+
+#include "epq_internal.h"
+#include "umma.cuh"
+
+namespace epq {
+
+constexpr int kGThreads = 256;
+constexpr int kTileN = 256;
+constexpr int kGroupTiles = 8;       // tiles of the N side that share the M side's tiles in L2
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+enum { kMapA = 0, kMapB = 1, kMapSa = 2, kMapSb = 3 };
+
+struct GroupedParams {
+    CUtensorMap map[4];              // A, B, block scales of A and B (NVFP4 weight gradient: in `maps`)
+    CUtensorMap out;
+    const CUtensorMap *maps;         // NVFP4 weight gradient: [E][4], written by the kernel before
+    const int32_t *offsets;          // [E + 1], or NULL: one expert with all R_cap rows
+    const int32_t *counts;           // BF16 weight gradient: [E] or NULL
+    const float *m_scale;            // NVFP4: rows as N: [E * M] of the weights' rows; rows as K: [E] of dy
+    const float *n_scale;            //        [R_cap] of the rows;                     [E] of x
+    uint32_t *status;
+    int R_cap, E;
+    int M, N, K;                     // rows as N: M features, K; rows as K: M x N
+    int add;                         // rows as K, FP32: add to d_w
+};
+
+template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_> struct GroupedCfg {
+    static constexpr bool kFp4 = kFp4_, kWgrad = kWgrad_, kF32 = kF32_;
+    static constexpr int kCtas = kCtas_;
+    static constexpr bool kAmn = kAmn_;                       // A with its M side contiguous (BF16)
+    static constexpr bool kBmn = kWgrad && !kFp4;
+    static constexpr int kBlockK = kFp4 ? 256 : 64;           // elements of K a stage
+    static constexpr int kStepK = kFp4 ? 64 : 16;             // elements of K a matrix instruction
+    static constexpr uint32_t kABytes = 128 * 128;
+    static constexpr uint32_t kBBytes = kTileN / kCtas * 128;
+    static constexpr uint32_t kSaBytes = kFp4 ? 2048 : 0;
+    static constexpr uint32_t kSbBytes = kFp4 ? 4096 : 0;
+    static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
+    static constexpr uint32_t kOutBytes = kWgrad ? 4096 : 2048;   // a warp's piece of a tile, twice
+    static constexpr uint32_t kOutAll = 4 * 2 * kOutBytes;
+    static constexpr uint32_t kBudget = 232448 - 1024 - 8192 - 4096;  // alignment, plan and barriers, row scales
+    static constexpr int kStages = (int)((kBudget - kOutAll) / kStageBytes);
+    // tensor memory: two accumulators of 256 columns; with block scales the two
+    // overlap in 64 columns, which are emptied first
+    static constexpr uint32_t kAcc1 = kFp4 ? 192 : 256;
+    static constexpr uint32_t kSaCol = 448, kSbCol = 464;
+    static constexpr int kChunk = kWgrad && !kF32 ? 64 : 32;      // columns that the epilogue takes at a time
+};
+
+struct __align__(8) GroupedBars {
+    uint64_t full[8], empty[8], tail[8];
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem, pad;
+};
+
+template <class C> constexpr uint32_t grouped_smem_bytes()
+{
+    return 1024 + C::kStages * C::kStageBytes + C::kOutAll + 4096 + 8192;
+}
+
+// A tile: its expert, the expert's rows, where it lies and its steps.
+struct GroupedTile {
+    int e, row0, rows;    // the expert's first row and number of rows (rows as N: of this tile)
+    int m0, n0;           // first row of the M side (of the pair), first of the N side
+    int n;                // columns of the N side
+    int kb;               // blocks of K
+};
+
+template <class C>
+__device__ __forceinline__ int expert_rows(const GroupedParams &p, int e, int &off, uint32_t &err)
+{
+    if (!p.offsets) {
+        off = 0;
+        return p.R_cap;
+    }
+    off = __ldg(p.offsets + e);
+    const int end = __ldg(p.offsets + e + 1);
+    if (off < 0 || end < off || ((off | end) & 127)) {
+        err |= kDevErrBadExpert;
+        return 0;
+    }
+    if (end > p.R_cap) {
+        err |= kDevErrCapacity;      // the columnwise layout of a cut slot is not known: none of it
+        return C::kFp4 && C::kWgrad ? 0 : max(0, p.R_cap - off);
+    }
+    return end - off;
+}
+
+template <class C> __device__ __forceinline__ int m_tiles(const GroupedParams &p)
+{
+    return (p.M + 128 * C::kCtas - 1) / (128 * C::kCtas);
+}
+
+template <class C>
+__device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams &p, const int *start, int t)
+{
+    GroupedTile o;
+    int lo = 0, hi = p.E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    o.e = lo;
+    uint32_t err = 0;
+    const int rows = expert_rows<C>(p, lo, o.row0, err);
+    const int mt = m_tiles<C>(p), nt = ((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN;
+    // groups of kGroupTiles tiles of the N side; in a group they change fastest
+    const int j = t - start[lo], g = j / (kGroupTiles * mt), in = j - g * kGroupTiles * mt;
+    const int gn = min(kGroupTiles, nt - g * kGroupTiles);
+    const int mi = in / gn, ni = g * kGroupTiles + in - mi * gn;
+    o.m0 = mi * 128 * C::kCtas;
+    o.n0 = ni * kTileN;
+    if (C::kWgrad) {
+        o.rows = rows;
+        if (p.counts)
+            o.rows = max(0, min(rows, __ldg(p.counts + lo)));
+        o.n = min(kTileN, p.N - o.n0);
+        o.kb = (o.rows + C::kBlockK - 1) / C::kBlockK;
+    } else {
+        o.rows = o.n = min(kTileN, rows - o.n0);
+        o.kb = (p.K + C::kBlockK - 1) / C::kBlockK;
+    }
+    return o;
+}
+
+// Tiles of every expert summed up, in shared memory; what is wrong with the
+// offsets goes to the status word.
+template <class C>
+__device__ __forceinline__ void grouped_plan(const GroupedParams &p, int *start, int *partial)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.E + kGThreads - 1) / kGThreads, e0 = tid * per;
+    const int mt = m_tiles<C>(p);
+    uint32_t err = 0;
+    int mine = 0, off;
+    for (int e = e0; e < min(e0 + per, p.E); ++e) {
+        const int rows = expert_rows<C>(p, e, off, err);
+        mine += mt * (((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN);
+    }
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d)
+            sum += v;
+    }
+    if (lane == 31)
+        partial[warp] = sum;
+    __syncthreads();
+    int at = sum - mine;
+    for (int w = 0; w < warp; ++w)
+        at += partial[w];
+    uint32_t ignore = 0;
+    for (int e = e0; e < min(e0 + per, p.E); ++e) {
+        start[e] = at;
+        const int rows = expert_rows<C>(p, e, off, ignore);
+        at += mt * (((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN);
+    }
+    if (tid == kGThreads - 1)
+        start[p.E] = at;       // the last threads have no expert or the last ones
+    if (err && blockIdx.x == 0)
+        raise_status(p.status, err);
+}
+
+template <class C>
+__global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_constant__ GroupedParams p)
+{
+    constexpr int kCtas = C::kCtas, kStages = C::kStages;
+    extern __shared__ uint8_t g_smem_raw[];
+    const uint32_t raw = smem_u32(g_smem_raw);
+    uint8_t *const base = g_smem_raw + ((1024 - (raw & 1023)) & 1023);
+    const uint32_t ring = smem_u32(base);
+    uint8_t *const out_s = base + kStages * C::kStageBytes;
+    float *const row_scale_s = reinterpret_cast<float *>(out_s + C::kOutAll);    // [4][256]
+    GroupedBars &bar = *reinterpret_cast<GroupedBars *>(out_s + C::kOutAll + 4096);
+    int *const start = reinterpret_cast<int *>(&bar + 1);                        // [E + 1]
+    int *const partial = start + p.E + 1;                                        // [8]
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
+    const int unit = (int)blockIdx.x / kCtas, units = (int)gridDim.x / kCtas;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bar.full[s], kCtas);
+            mbar_init(&bar.empty[s], 1);
+            mbar_init(&bar.tail[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bar.acc_full[b], 1);
+            mbar_init(&bar.acc_empty[b], 4 * kCtas);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 2)
+        tmem_alloc<kCtas>(smem_u32(&bar.tmem), 512);
+    pdl_launch_dependents();
+    pdl_wait();
+    grouped_plan<C>(p, start, partial);
+    tmem_fence_before();
+    if constexpr (kCtas == 2)
+        cluster_sync();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = bar.tmem;
+    const int tiles = start[p.E];
+    // barriers that the leader's matrix products wait on
+    const uint32_t full0 = kCtas == 2 ? at_rank(smem_u32(&bar.full[0]), 0) : smem_u32(&bar.full[0]);
+    bool ok = true;
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------------ copies
+        uint32_t it = 0, cut_it = 0;
+        int last_e = -1;
+        const CUtensorMap *maps = p.map;
+        for (int t = unit; t < tiles && ok; t += units) {
+            const GroupedTile o = grouped_tile<C>(p, start, t);
+            const int half = ((o.n + 63) / 64 * 64) / kCtas;              // of the N side: this CTA's
+            const uint32_t bytes = C::kABytes + C::kSaBytes + C::kSbBytes + (half + 63) / 64 * 8192;
+            if (C::kFp4 && C::kWgrad && o.e != last_e && o.kb > 0) {
+                maps = p.maps + 4 * o.e;
+                for (int i = 0; i < 4; ++i)
+                    tensormap_acquire(maps + i);
+                last_e = o.e;
+            }
+            const int tail_rows = C::kWgrad && !C::kFp4 && p.counts ? o.rows % C::kBlockK : 0;
+            for (int kb = 0; kb < o.kb; ++kb, ++it) {
+                const int s = (int)(it % kStages);
+                if (it >= kStages && !mbar_wait_for(&bar.empty[s], ((it / kStages) - 1) & 1, kWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                // a last block of rows that has to be cut is counted on a barrier
+                // of this CTA's own first
+                const bool cut = tail_rows && kb == o.kb - 1;
+                uint64_t *const tail = &bar.tail[cut_it % kStages];
+                const uint32_t f = cut ? smem_u32(tail) : full0 + 8 * s;
+                if (cut) {
+                    mbar_arrive_expect_tx(tail, bytes);
+                    ++cut_it;
+                } else {
+                    mbar_arrive_expect_tx_at(f, bytes);
+                }
+                const uint32_t a = ring + s * C::kStageBytes, b = a + C::kABytes;
+                const int k0 = kb * C::kBlockK;
+                const int m = o.m0 + 128 * (int)rank, n = o.n0 + half * (int)rank;
+                if constexpr (C::kFp4) {
+                    const int x = k0 / 2, xs = k0 / 64 * 64;              // bytes; scales of 64 in units of 8 bytes
+                    const uint32_t sa = b + C::kBBytes, sb = sa + C::kSaBytes;
+                    const int z = C::kWgrad ? 0 : o.e;
+                    const int nrow = C::kWgrad ? n : o.row0 + n;
+                    tma_load_3d<kCtas>(a, maps + kMapA, x, m, z, f);
+                    for (int i = 0; i < half; i += 64)
+                        tma_load_3d<kCtas>(b + i * 128, maps + kMapB, x, nrow + i, 0, f);
+                    tma_load_3d<kCtas>(sa, maps + kMapSa, xs, m / 128, z, f);
+                    tma_load_3d<kCtas>(sb, maps + kMapSb, xs, (C::kWgrad ? o.n0 : o.row0 + o.n0) / 128, 0, f);
+                } else if constexpr (C::kWgrad) {
+                    for (int i = 0; i < 128; i += 64)
+                        tma_load_3d<kCtas>(a + i * 128, maps + kMapA, m + i, o.row0 + k0, 0, f);
+                    for (int i = 0; i < half; i += 64)
+                        tma_load_3d<kCtas>(b + i * 128, maps + kMapB, n + i, o.row0 + k0, 0, f);
+                } else {
+                    if constexpr (C::kAmn) {
+                        for (int i = 0; i < 128; i += 64)
+                            tma_load_3d<kCtas>(a + i * 128, maps + kMapA, m + i, k0, o.e, f);
+                    } else {
+                        tma_load_3d<kCtas>(a, maps + kMapA, k0, m, o.e, f);
+                    }
+                    for (int i = 0; i < half; i += 64)
+                        tma_load_3d<kCtas>(b + i * 128, maps + kMapB, k0, o.row0 + n + i, 0, f);
+                }
+            }
+        }
+        // never leave with copies in flight: in each stage the last one's
+        // consumption, or at least its arrival
+        for (uint32_t i = it > (uint32_t)kStages ? it - kStages : 0; i < it; ++i)
+            if (!mbar_wait_for(&bar.empty[i % kStages], (i / kStages) & 1, kWaitNs)) {
+                ok = false;
+                if (rank == 0)
+                    (void)mbar_wait_for(&bar.full[i % kStages], (i / kStages) & 1, kWaitNs);
+            }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ------------------------------------------------------------ products
+        uint32_t it = 0, acc_it = 0;
+        for (int t = unit; t < tiles && ok; t += units) {
+            const GroupedTile o = grouped_tile<C>(p, start, t);
+            if (o.kb == 0)
+                continue;
+            const uint32_t b = acc_it & 1;
+            if constexpr (C::kFp4) {
+                if (acc_it > 0 && !mbar_wait_for(&bar.acc_empty[0], (acc_it - 1) & 1, kWaitNs))
+                    ok = false;
+            } else {
+                if (acc_it > 1 && !mbar_wait_for(&bar.acc_empty[b], ((acc_it >> 1) - 1) & 1, kWaitNs))
+                    ok = false;
+            }
+            if (!ok)
+                break;
+            tmem_fence_after();
+            const uint32_t d = tmem + b * C::kAcc1;
+            const uint32_t un = (uint32_t)(o.n + 63) / 64 * 64;
+            uint32_t idesc = (1u << 7) | (1u << 10) | ((un >> 3) << 17) | ((uint32_t)(8 * kCtas) << 24);
+            if (!C::kFp4)
+                idesc |= (1u << 4) | ((uint32_t)C::kAmn << 15) | ((uint32_t)C::kBmn << 16);
+            const int k_all = C::kWgrad ? o.rows : p.K;
+            for (int kb = 0; kb < o.kb; ++kb, ++it) {
+                const int s = (int)(it % kStages);
+                if (!mbar_wait_for(&bar.full[s], (it / kStages) & 1, kWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                const uint32_t a = ring + s * C::kStageBytes, bb = a + C::kABytes;
+                const int steps = min(4, (k_all - kb * C::kBlockK + C::kStepK - 1) / C::kStepK);
+                if constexpr (C::kFp4) {
+                    const uint32_t sa = bb + C::kBBytes, sb = sa + C::kSaBytes;
+                    for (int j = 0; j < steps; ++j) {
+                        tmem_cp_scales<kCtas>(tmem + C::kSaCol + 4 * j, desc_scales(sa + 512 * j));
+                        tmem_cp_scales<kCtas>(tmem + C::kSbCol + 8 * j, desc_scales(sb + 512 * j));
+                        if (un > 128)
+                            tmem_cp_scales<kCtas>(tmem + C::kSbCol + 8 * j + 4, desc_scales(sb + 2048 + 512 * j));
+                    }
+                    for (int j = 0; j < steps; ++j)
+                        mma_nvfp4<kCtas>(d, desc_k_major(a + 32 * j), desc_k_major(bb + 32 * j), idesc,
+                                         tmem + C::kSaCol + 4 * j, tmem + C::kSbCol + 8 * j, kb > 0 || j > 0);
+                } else {
+                    for (int j = 0; j < steps; ++j)
+                        mma_bf16<kCtas>(d, C::kAmn ? desc_mn_major(a + 2048 * j) : desc_k_major(a + 32 * j),
+                                        C::kBmn ? desc_mn_major(bb + 2048 * j) : desc_k_major(bb + 32 * j), idesc,
+                                        kb > 0 || j > 0);
+                }
+                mma_commit<kCtas>(smem_u32(&bar.empty[s]));
+            }
+            if (!ok)
+                break;
+            mma_commit<kCtas>(smem_u32(&bar.acc_full[b]));
+            ++acc_it;
+        }
+    } else if (C::kWgrad && !C::kFp4 && warp == 3 && p.counts) {
+        // ------------------------------------------------------------ cut blocks
+        // rows of a slot behind the expert's tokens count as zero, whatever they hold
+        uint32_t it = 0, cut_it = 0;
+        for (int t = unit; t < tiles && ok; t += units) {
+            const GroupedTile o = grouped_tile<C>(p, start, t);
+            const int rem = o.rows % C::kBlockK;
+            it += o.kb;
+            if (!rem)
+                continue;
+            const int s = (int)((it - 1) % kStages);
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait_for(&bar.tail[cut_it % kStages], (cut_it / kStages) & 1, kWaitNs));
+            if (!ok)
+                break;
+            ++cut_it;
+            const int boxes = 2 + (((o.n + 63) / 64 * 64) / kCtas + 63) / 64;
+            uint8_t *const a = base + s * C::kStageBytes;       // A's boxes, then B's
+            for (int x = 0; x < boxes; ++x)
+                for (int i = rem * 8 + lane; i < 512; i += 32)
+                    reinterpret_cast<uint4 *>(a + 8192 * x)[i] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_at(full0 + 8 * s);
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ sums
+        const int w = warp - 4;
+        uint8_t *const mine = out_s + w * 2 * C::kOutBytes;
+        const uint32_t acc_empty0 = kCtas == 2 ? at_rank(smem_u32(&bar.acc_empty[0]), 0) : smem_u32(&bar.acc_empty[0]);
+        uint32_t acc_it = 0, piece = 0;
+        for (int t = unit; t < tiles; t += units) {
+            const GroupedTile o = grouped_tile<C>(p, start, t);
+            if (o.kb == 0 && p.add)
+                continue;
+            const int m = o.m0 + 128 * (int)rank + 32 * w;      // first of this warp's 32 rows of the M side
+            const uint32_t b = acc_it & 1;
+            const uint32_t acc = tmem + ((uint32_t)(32 * w) << 16) + b * C::kAcc1;
+            float ms[4], scale0 = 1.f, scale1 = 1.f;
+            if constexpr (C::kFp4 && !C::kWgrad) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int f = m + 8 * h + lane / 4;
+                    ms[h] = f < p.M ? __ldg(p.m_scale + (int64_t)o.e * p.M + f) : 0.f;
+                }
+#pragma unroll
+                for (int c = 0; c < kTileN / 32; ++c)
+                    row_scale_s[kTileN * w + 32 * c + lane] =
+                        32 * c + lane < o.n ? __ldg(p.n_scale + o.row0 + o.n0 + 32 * c + lane) : 0.f;
+                __syncwarp();
+            } else if constexpr (C::kFp4) {
+                scale0 = __fdiv_rn(1.f, __ldg(p.m_scale + o.e));
+                scale1 = __fdiv_rn(1.f, __ldg(p.n_scale + o.e));
+            }
+            if (o.kb > 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait_for(&bar.acc_full[b], (acc_it >> 1) & 1,
+                                                           kWaitNs + 4096ull * (uint64_t)o.kb))) {
+                    ok = false;
+                    break;
+                }
+                ++acc_it;
+                tmem_fence_after();
+            }
+            const int nch = (o.n + C::kChunk - 1) / C::kChunk;
+            // with overlapping accumulators the shared columns first: at the end of
+            // the one, at the beginning of the other
+            const int last_shared = C::kFp4 ? min(nch - 1, 64 / C::kChunk - 1) : nch - 1;
+            for (int cc = 0; cc < nch; ++cc) {
+                const int c = C::kFp4 && b == 0 ? nch - 1 - cc : cc;
+                uint32_t r[C::kChunk];
+                if (o.kb > 0) {
+                    if constexpr (!C::kWgrad) {
+                        tmem_ld_16x32(acc + 32 * c, r);
+                        tmem_ld_16x32(acc + (16u << 16) + 32 * c, r + 16);
+                    } else {
+                        tmem_ld_32x32(acc + C::kChunk * c, r);
+                        if constexpr (C::kChunk == 64)
+                            tmem_ld_32x32(acc + C::kChunk * c + 32, r + 32);
+                    }
+                    tmem_wait_ld(r);
+                    if constexpr (C::kChunk == 64)
+                        tmem_wait_ld(r + 32);
+                    if (cc == last_shared) {
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_at(acc_empty0 + (C::kFp4 ? 0 : 8 * b));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C::kChunk; ++i)
+                        r[i] = 0u;
+                }
+                if (m >= p.M)
+                    continue;
+                uint8_t *const dst = mine + (piece & 1) * C::kOutBytes;
+                ++piece;
+                if (lane == 0)
+                    tma_store_wait_read<1>();
+                __syncwarp();
+                const uint32_t d = smem_u32(dst);
+                if constexpr (!C::kWgrad) {
+                    // 32 tokens x 32 features, a token's 64 bytes in a row (64-byte swizzle)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float2 ts = make_float2(1.f, 1.f);
+                        if constexpr (C::kFp4)
+                            ts = *reinterpret_cast<const float2 *>(row_scale_s + kTileN * w + 32 * c + 8 * i +
+                                                                   2 * (lane & 3));
+                        uint32_t q[4];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            float v0 = u2f(r[16 * (h / 2) + 4 * i + 2 * (h & 1)]);
+                            float v1 = u2f(r[16 * (h / 2) + 4 * i + 2 * (h & 1) + 1]);
+                            if constexpr (C::kFp4) {
+                                v0 = v0 * ms[h] * ts.x;
+                                v1 = v1 * ms[h] * ts.y;
+                            }
+                            q[h] = cvt_bf16x2(v0, v1);
+                        }
+                        const int row = 8 * i + (lane & 7), chunk = lane >> 3;
+                        st_matrix_trans(d + 64 * row + ((chunk ^ ((row >> 1) & 3)) << 4), q[0], q[1], q[2], q[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d<false>(&p.out, m, o.row0 + o.n0 + 32 * c, 0, d);
+                        tma_store_commit();
+                    }
+                } else {
+                    // 32 rows of 128 bytes (128-byte swizzle)
+                    if constexpr (C::kFp4) {
+#pragma unroll
+                        for (int i = 0; i < C::kChunk; ++i)
+                            r[i] = f2u(u2f(r[i]) * scale0 * scale1);
+                    }
+                    if constexpr (!C::kF32) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            r[i] = cvt_bf16x2(u2f(r[2 * i]), u2f(r[2 * i + 1]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(dst + 128 * lane + ((i ^ (lane & 7)) << 4)) =
+                            make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (C::kF32 && p.add)
+                            tma_store_3d<true>(&p.out, o.n0 + C::kChunk * c, m, o.e, d);
+                        else
+                            tma_store_3d<false>(&p.out, o.n0 + C::kChunk * c, m, o.e, d);
+                        tma_store_commit();
+                    }
+                }
+            }
+        }
+        if (lane == 0)
+            tma_store_wait0();
+    }
+
+    if (!ok && lane == 0)
+        raise_status(p.status, kDevErrTimeout);
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if constexpr (kCtas == 2)
+        cluster_sync();
+    if (warp == 2)
+        tmem_dealloc<kCtas>(tmem, 512);
+}
+
+// ---------------------------------------------------------------- launch
+// Clusters of this kernel that are resident at once.
+template <class C> cudaError_t grouped_units(const LaunchCtx &c, int &units)
+{
+    static std::atomic<int> known[64];
+    static std::atomic<uint32_t> limit_set[2];
+    const uint32_t smem = grouped_smem_bytes<C>();
+    cudaError_t e = ensure_smem_limit(grouped_kernel<C>, c.device, (int)smem, limit_set);
+    if (e != cudaSuccess)
+        return e;
+    if (C::kCtas == 1) {
+        units = c.num_sms;
+        return cudaSuccess;
+    }
+    if (c.device < 64 && (units = known[c.device].load(std::memory_order_relaxed)) > 0)
+        return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C::kCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(c.num_sms / C::kCtas * C::kCtas));
+    cfg.blockDim = dim3(kGThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&units, grouped_kernel<C>, &cfg);
+    if (e != cudaSuccess)
+        return e;
+    if (units < 1)
+        units = 1;
+    if (c.device < 64)
+        known[c.device].store(units, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+// `most_tiles`: a bound on the call's tiles that the host knows.
+template <class C> cudaError_t launch_grouped(const LaunchCtx &c, const GroupedParams &p, int64_t most_tiles)
+{
+    int units = 0;
+    cudaError_t e = grouped_units<C>(c, units);
+    if (e != cudaSuccess)
+        return e;
+    if (most_tiles < units)
+        units = (int)(most_tiles < 1 ? 1 : most_tiles);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C::kCtas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(units * C::kCtas));
+    cfg.blockDim = dim3(kGThreads);
+    cfg.dynamicSmemBytes = grouped_smem_bytes<C>();
+    cfg.stream = c.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = C::kCtas == 2 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, grouped_kernel<C>, p);
+}
+
+} // namespace epq
