@@ -325,7 +325,9 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             const int k_all = C::kWgrad ? o.rows : p.K;
             for (int kb = 0; kb < o.kb; ++kb, ++it) {
                 const int s = (int)(it % kStages);
-                if (!mbar_wait_for(&bar.full[s], (it / kStages) & 1, kWaitNs)) {
+                const bool cut = C::kBmn && p.counts && kb == o.kb - 1;
+                if (cut ? !mbar_wait_for<true>(&bar.full[s], (it / kStages) & 1, kWaitNs)
+                        : !mbar_wait_for(&bar.full[s], (it / kStages) & 1, kWaitNs)) {
                     ok = false;
                     break;
                 }
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_at(full0 + 8 * s);
+                mbar_arrive_release_at(full0 + 8 * s);
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ sums

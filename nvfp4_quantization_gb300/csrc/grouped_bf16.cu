@@ -63,12 +63,12 @@ cudaError_t launch_grouped_gemm(const LaunchCtx &c, const GroupedGemmArgs &a)
 {
     if (a.R_cap == 0)
         return cudaSuccess;
-    return a.transposed ? gemm<true, 1>(c, a) : gemm<false, 1>(c, a);
+    return a.transposed ? gemm<true, 2>(c, a) : gemm<false, 2>(c, a);
 }
 
 cudaError_t launch_grouped_wgrad(const LaunchCtx &c, const GroupedWgradArgs &a)
 {
-    return a.f32 ? wgrad<true, 1>(c, a) : wgrad<false, 1>(c, a);
+    return a.f32 ? wgrad<true, 2>(c, a) : wgrad<false, 2>(c, a);
 }
 
 } // namespace epq

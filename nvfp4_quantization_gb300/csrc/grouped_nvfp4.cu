@@ -213,12 +213,12 @@ cudaError_t launch_operand(const LaunchCtx &c, const OperandArgs &a)
 
 cudaError_t launch_nvfp4_gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a)
 {
-    return gemm<1>(c, a);
+    return gemm<2>(c, a);
 }
 
 cudaError_t launch_nvfp4_wgrad(const LaunchCtx &c, const Nvfp4WgradArgs &a)
 {
-    return a.f32 ? wgrad<true, 1>(c, a) : wgrad<false, 1>(c, a);
+    return a.f32 ? wgrad<true, 2>(c, a) : wgrad<false, 2>(c, a);
 }
 
 } // namespace epq

@@ -15,7 +15,8 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
-// A try at a phase that threads of either CTA of a pair complete.
+// A try at a phase that a thread of the pair's other CTA completes after writes
+// to its own shared memory.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity)
 {
     uint32_t ok;
@@ -27,14 +28,15 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t pa
 }
 
 // Wait on a phase of an mbarrier, for limit_ns at most; false if it gave up.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
 {
     for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait_cluster(bar, parity))
+        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))
             return true;
     const uint64_t t0 = now_ns();
     while (now_ns() - t0 < limit_ns)
-        if (mbar_try_wait_cluster(bar, parity))
+        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))
             return true;
     return false;
 }
@@ -55,15 +57,23 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank)
     return r;
 }
 
-// Arrivals on a barrier of any CTA of the cluster.
-__device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
+// Arrivals on a barrier of any CTA of the cluster.  The first orders this
+// thread's writes to shared memory before it.  The others order none (a release
+// at cluster scope waits for the thread's earlier copies to be on their way:
+// with one a stage the products below ran at 0.4 of their rate).
+__device__ __forceinline__ void mbar_arrive_release_at(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_expect_tx_at(uint32_t bar, uint32_t bytes)
 {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
 
