@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
     const uint32_t full0 = kCtas == 2 ? at_rank(smem_u32(&bar.full[0]), 0) : smem_u32(&bar.full[0]);
     bool ok = true;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ------------------------------------------------------------ copies
         uint32_t it = 0, cut_it = 0;
         int last_e = -1;
@@ -239,56 +239,56 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             const uint32_t bytes = C::kABytes + C::kSaBytes + C::kSbBytes + (half + 63) / 64 * 8192;
             if (C::kFp4 && C::kWgrad && o.e != last_e && o.kb > 0) {
                 maps = p.maps + 4 * o.e;
-                for (int i = 0; i < 4; ++i)
-                    tensormap_acquire(maps + i);
+                if (lane < 4)
+                    tensormap_acquire(maps + lane);
+                __syncwarp();
                 last_e = o.e;
             }
             const int tail_rows = C::kWgrad && !C::kFp4 && p.counts ? o.rows % C::kBlockK : 0;
+            const int m = o.m0 + 128 * (int)rank, n = o.n0 + half * (int)rank;
             for (int kb = 0; kb < o.kb; ++kb, ++it) {
                 const int s = (int)(it % kStages);
-                if (it >= kStages && !mbar_wait_for(&bar.empty[s], ((it / kStages) - 1) & 1, kWaitNs)) {
+                if (it >= kStages &&
+                    !__all_sync(0xffffffffu, mbar_wait_for(&bar.empty[s], ((it / kStages) - 1) & 1, kWaitNs))) {
                     ok = false;
                     break;
                 }
                 // a last block of rows that has to be cut is counted on a barrier
                 // of this CTA's own first
                 const bool cut = tail_rows && kb == o.kb - 1;
-                uint64_t *const tail = &bar.tail[cut_it % kStages];
-                const uint32_t f = cut ? smem_u32(tail) : full0 + 8 * s;
-                if (cut) {
-                    mbar_arrive_expect_tx(tail, bytes);
-                    ++cut_it;
-                } else {
-                    mbar_arrive_expect_tx_at(f, bytes);
-                }
+                const uint32_t f = cut ? smem_u32(&bar.tail[cut_it % kStages]) : full0 + 8 * s;
+                cut_it += cut;
                 const uint32_t a = ring + s * C::kStageBytes, b = a + C::kABytes;
                 const int k0 = kb * C::kBlockK;
-                const int m = o.m0 + 128 * (int)rank, n = o.n0 + half * (int)rank;
-                if constexpr (C::kFp4) {
-                    const int x = k0 / 2, xs = k0 / 64 * 64;              // bytes; scales of 64 in units of 8 bytes
-                    const uint32_t sa = b + C::kBBytes, sb = sa + C::kSaBytes;
-                    const int z = C::kWgrad ? 0 : o.e;
-                    const int nrow = C::kWgrad ? n : o.row0 + n;
-                    tma_load_3d<kCtas>(a, maps + kMapA, x, m, z, f);
-                    for (int i = 0; i < half; i += 64)
-                        tma_load_3d<kCtas>(b + i * 128, maps + kMapB, x, nrow + i, 0, f);
-                    tma_load_3d<kCtas>(sa, maps + kMapSa, xs, m / 128, z, f);
-                    tma_load_3d<kCtas>(sb, maps + kMapSb, xs, (C::kWgrad ? o.n0 : o.row0 + o.n0) / 128, 0, f);
-                } else if constexpr (C::kWgrad) {
-                    for (int i = 0; i < 128; i += 64)
-                        tma_load_3d<kCtas>(a + i * 128, maps + kMapA, m + i, o.row0 + k0, 0, f);
-                    for (int i = 0; i < half; i += 64)
-                        tma_load_3d<kCtas>(b + i * 128, maps + kMapB, n + i, o.row0 + k0, 0, f);
-                } else {
-                    if constexpr (C::kAmn) {
+                if (elect_one()) {
+                    mbar_arrive_expect_tx_at(f, bytes);
+                    if constexpr (C::kFp4) {
+                        const int x = k0 / 2, xs = k0 / 64 * 64;          // bytes; scales of 64 in units of 8 bytes
+                        const uint32_t sa = b + C::kBBytes, sb = sa + C::kSaBytes;
+                        const int z = C::kWgrad ? 0 : o.e;
+                        const int nrow = C::kWgrad ? n : o.row0 + n;
+                        tma_load_3d<kCtas>(a, maps + kMapA, x, m, z, f);
+                        for (int i = 0; i < half; i += 64)
+                            tma_load_3d<kCtas>(b + i * 128, maps + kMapB, x, nrow + i, 0, f);
+                        tma_load_3d<kCtas>(sa, maps + kMapSa, xs, m / 128, z, f);
+                        tma_load_3d<kCtas>(sb, maps + kMapSb, xs, (C::kWgrad ? o.n0 : o.row0 + o.n0) / 128, 0, f);
+                    } else if constexpr (C::kWgrad) {
                         for (int i = 0; i < 128; i += 64)
-                            tma_load_3d<kCtas>(a + i * 128, maps + kMapA, m + i, k0, o.e, f);
+                            tma_load_3d<kCtas>(a + i * 128, maps + kMapA, m + i, o.row0 + k0, 0, f);
+                        for (int i = 0; i < half; i += 64)
+                            tma_load_3d<kCtas>(b + i * 128, maps + kMapB, n + i, o.row0 + k0, 0, f);
                     } else {
-                        tma_load_3d<kCtas>(a, maps + kMapA, k0, m, o.e, f);
+                        if constexpr (C::kAmn) {
+                            for (int i = 0; i < 128; i += 64)
+                                tma_load_3d<kCtas>(a + i * 128, maps + kMapA, m + i, k0, o.e, f);
+                        } else {
+                            tma_load_3d<kCtas>(a, maps + kMapA, k0, m, o.e, f);
+                        }
+                        for (int i = 0; i < half; i += 64)
+                            tma_load_3d<kCtas>(b + i * 128, maps + kMapB, k0, o.row0 + n + i, 0, f);
                     }
-                    for (int i = 0; i < half; i += 64)
-                        tma_load_3d<kCtas>(b + i * 128, maps + kMapB, k0, o.row0 + n + i, 0, f);
                 }
+                __syncwarp();
             }
         }
         // never leave with copies in flight: in each stage the last one's
@@ -299,7 +299,8 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                 if (rank == 0)
                     (void)mbar_wait_for(&bar.full[i % kStages], (i / kStages) & 1, kWaitNs);
             }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+        ok = __all_sync(0xffffffffu, ok);
+    } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ products
         uint32_t it = 0, acc_it = 0;
         for (int t = unit; t < tiles && ok; t += units) {
@@ -307,13 +308,11 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             if (o.kb == 0)
                 continue;
             const uint32_t b = acc_it & 1;
-            if constexpr (C::kFp4) {
-                if (acc_it > 0 && !mbar_wait_for(&bar.acc_empty[0], (acc_it - 1) & 1, kWaitNs))
-                    ok = false;
-            } else {
-                if (acc_it > 1 && !mbar_wait_for(&bar.acc_empty[b], ((acc_it >> 1) - 1) & 1, kWaitNs))
-                    ok = false;
-            }
+            if constexpr (C::kFp4)
+                ok = acc_it == 0 || mbar_wait_for(&bar.acc_empty[0], (acc_it - 1) & 1, kWaitNs);
+            else
+                ok = acc_it < 2 || mbar_wait_for(&bar.acc_empty[b], ((acc_it >> 1) - 1) & 1, kWaitNs);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
             tmem_fence_after();
@@ -326,36 +325,46 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             for (int kb = 0; kb < o.kb; ++kb, ++it) {
                 const int s = (int)(it % kStages);
                 const bool cut = C::kBmn && p.counts && kb == o.kb - 1;
-                if (cut ? !mbar_wait_for<true>(&bar.full[s], (it / kStages) & 1, kWaitNs)
-                        : !mbar_wait_for(&bar.full[s], (it / kStages) & 1, kWaitNs)) {
-                    ok = false;
+                ok = cut ? mbar_wait_for<true>(&bar.full[s], (it / kStages) & 1, kWaitNs)
+                         : mbar_wait_for(&bar.full[s], (it / kStages) & 1, kWaitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
                     break;
-                }
                 tmem_fence_after();
                 const uint32_t a = ring + s * C::kStageBytes, bb = a + C::kABytes;
-                const int steps = min(4, (k_all - kb * C::kBlockK + C::kStepK - 1) / C::kStepK);
-                if constexpr (C::kFp4) {
-                    const uint32_t sa = bb + C::kBBytes, sb = sa + C::kSaBytes;
-                    for (int j = 0; j < steps; ++j) {
-                        tmem_cp_scales<kCtas>(tmem + C::kSaCol + 4 * j, desc_scales(sa + 512 * j));
-                        tmem_cp_scales<kCtas>(tmem + C::kSbCol + 8 * j, desc_scales(sb + 512 * j));
-                        if (un > 128)
-                            tmem_cp_scales<kCtas>(tmem + C::kSbCol + 8 * j + 4, desc_scales(sb + 2048 + 512 * j));
+                const int steps = (k_all - kb * C::kBlockK + C::kStepK - 1) / C::kStepK;
+                if (elect_one()) {
+                    if constexpr (C::kFp4) {
+                        const uint32_t sa = bb + C::kBBytes, sb = sa + C::kSaBytes;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j < steps) {
+                                tmem_cp_scales<kCtas>(tmem + C::kSaCol + 4 * j, desc_scales(sa + 512 * j));
+                                tmem_cp_scales<kCtas>(tmem + C::kSbCol + 8 * j, desc_scales(sb + 512 * j));
+                                if (un > 128)
+                                    tmem_cp_scales<kCtas>(tmem + C::kSbCol + 8 * j + 4,
+                                                          desc_scales(sb + 2048 + 512 * j));
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < steps)
+                                mma_nvfp4<kCtas>(d, desc_k_major(a + 32 * j), desc_k_major(bb + 32 * j), idesc,
+                                                 tmem + C::kSaCol + 4 * j, tmem + C::kSbCol + 8 * j, kb > 0 || j > 0);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < steps)
+                                mma_bf16<kCtas>(d, C::kAmn ? desc_mn_major(a + 2048 * j) : desc_k_major(a + 32 * j),
+                                                C::kBmn ? desc_mn_major(bb + 2048 * j) : desc_k_major(bb + 32 * j),
+                                                idesc, kb > 0 || j > 0);
                     }
-                    for (int j = 0; j < steps; ++j)
-                        mma_nvfp4<kCtas>(d, desc_k_major(a + 32 * j), desc_k_major(bb + 32 * j), idesc,
-                                         tmem + C::kSaCol + 4 * j, tmem + C::kSbCol + 8 * j, kb > 0 || j > 0);
-                } else {
-                    for (int j = 0; j < steps; ++j)
-                        mma_bf16<kCtas>(d, C::kAmn ? desc_mn_major(a + 2048 * j) : desc_k_major(a + 32 * j),
-                                        C::kBmn ? desc_mn_major(bb + 2048 * j) : desc_k_major(bb + 32 * j), idesc,
-                                        kb > 0 || j > 0);
+                    mma_commit<kCtas>(smem_u32(&bar.empty[s]));
+                    if (kb == o.kb - 1)
+                        mma_commit<kCtas>(smem_u32(&bar.acc_full[b]));
                 }
-                mma_commit<kCtas>(smem_u32(&bar.empty[s]));
+                __syncwarp();
             }
-            if (!ok)
-                break;
-            mma_commit<kCtas>(smem_u32(&bar.acc_full[b]));
             ++acc_it;
         }
     } else if (C::kWgrad && !C::kFp4 && warp == 3 && p.counts) {
