@@ -192,7 +192,7 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, 
 
 // Tensor map of a 3-D tensor (dims[0] contiguous, pitches of the other two in
 // bytes), with a swizzle of 0, 64 or 128 bytes.
-enum class MapType { U8, Bf16, F32, I64 };
+enum class MapType { U8, Bf16, F32 };
 bool make_map_3d(CUtensorMap *m, MapType type, const void *base, const uint64_t (&dims)[3],
                  const uint64_t (&pitches)[2], const uint32_t (&box)[3], int swizzle);
 

@@ -53,10 +53,13 @@ template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_> struct G
     static constexpr uint32_t kSaBytes = kFp4 ? 2048 : 0;
     static constexpr uint32_t kSbBytes = kFp4 ? 4096 : 0;
     static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
-    static constexpr uint32_t kOutBytes = kWgrad ? 4096 : 2048;   // a warp's piece of a tile, twice
-    static constexpr uint32_t kOutAll = 4 * 2 * kOutBytes;
-    static constexpr uint32_t kBudget = 232448 - 1024 - 8192 - 4096;  // alignment, plan and barriers, row scales
-    static constexpr int kStages = (int)((kBudget - kOutAll) / kStageBytes);
+    static constexpr uint32_t kOutBytes = kWgrad ? 4096 : 2048;   // a warp's piece of a tile
+    static constexpr int kPieces = 3;                             // of them on their way out
+    static constexpr uint32_t kOutAll = 4 * kPieces * kOutBytes;
+    static constexpr uint32_t kRowScales = kFp4 && !kWgrad ? 4 * kTileN * 4 : 0;
+    static constexpr uint32_t kPlan = 4608;                       // barriers and tile counts of 1024 experts
+    static constexpr uint32_t kRest = 1024 + kOutAll + kRowScales + kPlan;    // 1024: the ring's alignment
+    static constexpr int kStages = (int)((232448 - kRest) / kStageBytes);
     // tensor memory: two accumulators of 256 columns; with block scales the two
     // overlap in 64 columns, which are emptied first
     static constexpr uint32_t kAcc1 = kFp4 ? 192 : 256;
@@ -64,7 +67,7 @@ template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_> struct G
     static constexpr int kChunk = kWgrad && !kF32 ? 64 : 32;      // columns that the epilogue takes at a time
 };
 
-struct __align__(8) GroupedBars {
+struct __align__(8) GroupedBars {      // up to 8 stages
     uint64_t full[8], empty[8], tail[8];
     uint64_t acc_full[2], acc_empty[2];
     uint32_t tmem, pad;
@@ -72,7 +75,7 @@ struct __align__(8) GroupedBars {
 
 template <class C> constexpr uint32_t grouped_smem_bytes()
 {
-    return 1024 + C::kStages * C::kStageBytes + C::kOutAll + 4096 + 8192;
+    return C::kRest + C::kStages * C::kStageBytes;
 }
 
 // A tile: its expert, the expert's rows, where it lies and its steps.
@@ -111,7 +114,9 @@ template <class C> __device__ __forceinline__ int m_tiles(const GroupedParams &p
 template <class C>
 __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams &p, const int *start, int t)
 {
-    GroupedTile o;
+    GroupedTile o = {};
+    if (t >= start[p.E])
+        return o;
     int lo = 0, hi = p.E - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -142,6 +147,40 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams &p, cons
     }
     return o;
 }
+
+// The tiles of one CTA (pair) in order, for a whole warp: each lane works out
+// one of the next 32, so that a change of tiles costs a few shuffles (worked
+// out one by one the products paused for about 0.5 us a tile).
+template <class C> struct GroupedWalk {
+    const GroupedParams &p;
+    const int *start;
+    int next, step, i;
+    GroupedTile mine;
+
+    __device__ __forceinline__ GroupedWalk(const GroupedParams &p_, const int *start_, int first, int step_)
+        : p(p_), start(start_), next(first), step(step_), i(32)
+    {
+    }
+
+    __device__ __forceinline__ GroupedTile tile()
+    {
+        if (i == 32) {
+            mine = grouped_tile<C>(p, start, next + step * (int)(threadIdx.x & 31));
+            next += 32 * step;
+            i = 0;
+        }
+        GroupedTile o;
+        o.e = __shfl_sync(0xffffffffu, mine.e, i);
+        o.row0 = __shfl_sync(0xffffffffu, mine.row0, i);
+        o.rows = __shfl_sync(0xffffffffu, mine.rows, i);
+        o.m0 = __shfl_sync(0xffffffffu, mine.m0, i);
+        o.n0 = __shfl_sync(0xffffffffu, mine.n0, i);
+        o.n = __shfl_sync(0xffffffffu, mine.n, i);
+        o.kb = __shfl_sync(0xffffffffu, mine.kb, i);
+        ++i;
+        return o;
+    }
+};
 
 // Tiles of every expert summed up, in shared memory; what is wrong with the
 // offsets goes to the status word.
@@ -192,7 +231,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
     const uint32_t ring = smem_u32(base);
     uint8_t *const out_s = base + kStages * C::kStageBytes;
     float *const row_scale_s = reinterpret_cast<float *>(out_s + C::kOutAll);    // [4][256]
-    GroupedBars &bar = *reinterpret_cast<GroupedBars *>(out_s + C::kOutAll + 4096);
+    GroupedBars &bar = *reinterpret_cast<GroupedBars *>(out_s + C::kOutAll + C::kRowScales);
     int *const start = reinterpret_cast<int *>(&bar + 1);                        // [E + 1]
     int *const partial = start + p.E + 1;                                        // [8]
 
@@ -227,6 +266,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
     // barriers that the leader's matrix products wait on
     const uint32_t full0 = kCtas == 2 ? at_rank(smem_u32(&bar.full[0]), 0) : smem_u32(&bar.full[0]);
     bool ok = true;
+    GroupedWalk<C> walk(p, start, unit, units);
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies
@@ -234,7 +274,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
         int last_e = -1;
         const CUtensorMap *maps = p.map;
         for (int t = unit; t < tiles && ok; t += units) {
-            const GroupedTile o = grouped_tile<C>(p, start, t);
+            const GroupedTile o = walk.tile();
             const int half = ((o.n + 63) / 64 * 64) / kCtas;              // of the N side: this CTA's
             const uint32_t bytes = C::kABytes + C::kSaBytes + C::kSbBytes + (half + 63) / 64 * 8192;
             if (C::kFp4 && C::kWgrad && o.e != last_e && o.kb > 0) {
@@ -263,15 +303,15 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                 if (elect_one()) {
                     mbar_arrive_expect_tx_at(f, bytes);
                     if constexpr (C::kFp4) {
-                        const int x = k0 / 2, xs = k0 / 64 * 64;          // bytes; scales of 64 in units of 8 bytes
+                        const int x = k0 / 2, ys = k0 / 16;               // bytes; pieces of 128 bytes of scales
                         const uint32_t sa = b + C::kBBytes, sb = sa + C::kSaBytes;
-                        const int z = C::kWgrad ? 0 : o.e;
+                        const int z = C::kWgrad ? 0 : o.e, zs = z * ((p.M + 127) / 128);
                         const int nrow = C::kWgrad ? n : o.row0 + n;
                         tma_load_3d<kCtas>(a, maps + kMapA, x, m, z, f);
                         for (int i = 0; i < half; i += 64)
                             tma_load_3d<kCtas>(b + i * 128, maps + kMapB, x, nrow + i, 0, f);
-                        tma_load_3d<kCtas>(sa, maps + kMapSa, xs, m / 128, z, f);
-                        tma_load_3d<kCtas>(sb, maps + kMapSb, xs, (C::kWgrad ? o.n0 : o.row0 + o.n0) / 128, 0, f);
+                        tma_load_3d<kCtas>(sa, maps + kMapSa, 0, ys, zs + m / 128, f);
+                        tma_load_3d<kCtas>(sb, maps + kMapSb, 0, ys, (C::kWgrad ? o.n0 : o.row0 + o.n0) / 128, f);
                     } else if constexpr (C::kWgrad) {
                         for (int i = 0; i < 128; i += 64)
                             tma_load_3d<kCtas>(a + i * 128, maps + kMapA, m + i, o.row0 + k0, 0, f);
@@ -304,7 +344,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
         // ------------------------------------------------------------ products
         uint32_t it = 0, acc_it = 0;
         for (int t = unit; t < tiles && ok; t += units) {
-            const GroupedTile o = grouped_tile<C>(p, start, t);
+            const GroupedTile o = walk.tile();
             if (o.kb == 0)
                 continue;
             const uint32_t b = acc_it & 1;
@@ -372,7 +412,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
         // rows of a slot behind the expert's tokens count as zero, whatever they hold
         uint32_t it = 0, cut_it = 0;
         for (int t = unit; t < tiles && ok; t += units) {
-            const GroupedTile o = grouped_tile<C>(p, start, t);
+            const GroupedTile o = walk.tile();
             const int rem = o.rows % C::kBlockK;
             it += o.kb;
             if (!rem)
@@ -396,11 +436,13 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
     } else if (warp >= 4) {
         // ------------------------------------------------------------ sums
         const int w = warp - 4;
-        uint8_t *const mine = out_s + w * 2 * C::kOutBytes;
+        uint8_t *const mine = out_s + w * C::kPieces * C::kOutBytes;
+        float *const ts_w = row_scale_s + kTileN * w;
         const uint32_t acc_empty0 = kCtas == 2 ? at_rank(smem_u32(&bar.acc_empty[0]), 0) : smem_u32(&bar.acc_empty[0]);
-        uint32_t acc_it = 0, piece = 0;
+        uint32_t acc_it = 0;
+        int piece = 0;
         for (int t = unit; t < tiles; t += units) {
-            const GroupedTile o = grouped_tile<C>(p, start, t);
+            const GroupedTile o = walk.tile();
             if (o.kb == 0 && p.add)
                 continue;
             const int m = o.m0 + 128 * (int)rank + 32 * w;      // first of this warp's 32 rows of the M side
@@ -413,60 +455,50 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                     const int f = m + 8 * h + lane / 4;
                     ms[h] = f < p.M ? __ldg(p.m_scale + (int64_t)o.e * p.M + f) : 0.f;
                 }
+                __syncwarp();
 #pragma unroll
                 for (int c = 0; c < kTileN / 32; ++c)
-                    row_scale_s[kTileN * w + 32 * c + lane] =
-                        32 * c + lane < o.n ? __ldg(p.n_scale + o.row0 + o.n0 + 32 * c + lane) : 0.f;
+                    ts_w[32 * c + lane] = 32 * c + lane < o.n ? __ldg(p.n_scale + o.row0 + o.n0 + 32 * c + lane) : 0.f;
                 __syncwarp();
             } else if constexpr (C::kFp4) {
                 scale0 = __fdiv_rn(1.f, __ldg(p.m_scale + o.e));
                 scale1 = __fdiv_rn(1.f, __ldg(p.n_scale + o.e));
             }
-            if (o.kb > 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait_for(&bar.acc_full[b], (acc_it >> 1) & 1,
-                                                           kWaitNs + 4096ull * (uint64_t)o.kb))) {
-                    ok = false;
-                    break;
-                }
-                ++acc_it;
-                tmem_fence_after();
-            }
             const int nch = (o.n + C::kChunk - 1) / C::kChunk;
-            // with overlapping accumulators the shared columns first: at the end of
-            // the one, at the beginning of the other
+            // with overlapping accumulators the shared columns come first: the end
+            // of the one, the beginning of the other
             const int last_shared = C::kFp4 ? min(nch - 1, 64 / C::kChunk - 1) : nch - 1;
-            for (int cc = 0; cc < nch; ++cc) {
-                const int c = C::kFp4 && b == 0 ? nch - 1 - cc : cc;
-                uint32_t r[C::kChunk];
-                if (o.kb > 0) {
-                    if constexpr (!C::kWgrad) {
-                        tmem_ld_16x32(acc + 32 * c, r);
-                        tmem_ld_16x32(acc + (16u << 16) + 32 * c, r + 16);
-                    } else {
-                        tmem_ld_32x32(acc + C::kChunk * c, r);
-                        if constexpr (C::kChunk == 64)
-                            tmem_ld_32x32(acc + C::kChunk * c + 32, r + 32);
-                    }
-                    tmem_wait_ld(r);
-                    if constexpr (C::kChunk == 64)
-                        tmem_wait_ld(r + 32);
-                    if (cc == last_shared) {
-                        tmem_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_at(acc_empty0 + (C::kFp4 ? 0 : 8 * b));
-                    }
+            const bool back = C::kFp4 && b == 0;
+            auto load = [&](int cc, uint32_t *r) {
+                const uint32_t at0 = acc + C::kChunk * (back ? nch - 1 - cc : cc);
+                if constexpr (!C::kWgrad) {
+                    tmem_ld_16x32(at0, r);
+                    tmem_ld_16x32(at0 + (16u << 16), r + 16);
                 } else {
-#pragma unroll
-                    for (int i = 0; i < C::kChunk; ++i)
-                        r[i] = 0u;
+                    tmem_ld_32x32(at0, r);
+                    if constexpr (C::kChunk == 64)
+                        tmem_ld_32x32(at0 + 32, r + 32);
                 }
+            };
+            auto arrived = [&](int cc, uint32_t *r) {
+                tmem_wait_ld(r);
+                if constexpr (C::kChunk == 64)
+                    tmem_wait_ld(r + 32);
+                if (cc == last_shared) {
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_at(acc_empty0 + (C::kFp4 ? 0 : 8 * b));
+                }
+            };
+            auto emit = [&](int cc, uint32_t *r) {
                 if (m >= p.M)
-                    continue;
-                uint8_t *const dst = mine + (piece & 1) * C::kOutBytes;
-                ++piece;
+                    return;
+                const int c = back ? nch - 1 - cc : cc;
+                uint8_t *const dst = mine + piece * C::kOutBytes;
+                piece = piece == C::kPieces - 1 ? 0 : piece + 1;
                 if (lane == 0)
-                    tma_store_wait_read<1>();
+                    tma_store_wait_read<C::kPieces - 1>();
                 __syncwarp();
                 const uint32_t d = smem_u32(dst);
                 if constexpr (!C::kWgrad) {
@@ -475,8 +507,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                     for (int i = 0; i < 4; ++i) {
                         float2 ts = make_float2(1.f, 1.f);
                         if constexpr (C::kFp4)
-                            ts = *reinterpret_cast<const float2 *>(row_scale_s + kTileN * w + 32 * c + 8 * i +
-                                                                   2 * (lane & 3));
+                            ts = *reinterpret_cast<const float2 *>(ts_w + 32 * c + 8 * i + 2 * (lane & 3));
                         uint32_t q[4];
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
@@ -522,6 +553,37 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                             tma_store_3d<false>(&p.out, o.n0 + C::kChunk * c, m, o.e, d);
                         tma_store_commit();
                     }
+                }
+            };
+            uint32_t ra[C::kChunk], rb[C::kChunk];
+            if (C::kWgrad && o.kb == 0) {          // no rows: zeros
+                for (int cc = 0; cc < nch; ++cc) {
+#pragma unroll
+                    for (int i = 0; i < C::kChunk; ++i)
+                        ra[i] = 0u;
+                    emit(cc, ra);
+                }
+                continue;
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait_for(&bar.acc_full[b], (acc_it >> 1) & 1,
+                                                       kWaitNs + 4096ull * (uint64_t)o.kb))) {
+                ok = false;
+                break;
+            }
+            ++acc_it;
+            tmem_fence_after();
+            // the next columns are on their way while these are written
+            load(0, ra);
+            for (int cc = 0; cc < nch; cc += 2) {
+                arrived(cc, ra);
+                if (cc + 1 < nch)
+                    load(cc + 1, rb);
+                emit(cc, ra);
+                if (cc + 1 < nch) {
+                    arrived(cc + 1, rb);
+                    if (cc + 2 < nch)
+                        load(cc + 2, ra);
+                    emit(cc + 1, rb);
                 }
             }
         }

@@ -85,6 +85,12 @@ template <int kDim> __device__ __forceinline__ void map_set_dim(uint32_t m, uint
                  : "memory");
 }
 
+template <int kDim> __device__ __forceinline__ void map_set_pitch(uint32_t m, uint64_t v)
+{
+    asm volatile("tensormap.replace.tile.global_stride.shared::cta.b1024.b64 [%0], %1, %2;" ::"r"(m), "n"(kDim), "l"(v)
+                 : "memory");
+}
+
 __global__ void __launch_bounds__(128) wgrad_maps_kernel(const __grid_constant__ MapArgs a, const int32_t *offsets,
                                                          int R_cap, CUtensorMap *out)
 {
@@ -99,16 +105,17 @@ __global__ void __launch_bounds__(128) wgrad_maps_kernel(const __grid_constant__
         return;                                   // no rows: not used
     if (lane == 0) {
         const uint32_t at = smem_u32(&m[i]);
-        const int64_t n = end - off, H = a.H[i];
-        // codes: [H][n / 2] bytes; scales: [H / 128] rows of n units of 8 bytes
+        const int64_t n = end - off, H = a.H[i];      // dimension 0 of the codes and 1 of the scales, and their pitches
         const uint64_t base = (uint64_t)(a.base[i] + off * H / (i < 2 ? 2 : 16));
-        const uint64_t pitch = i < 2 ? n / 2 : n * 8;
         asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(at), "l"(base)
                      : "memory");
-        map_set_dim<0>(at, (uint32_t)(i < 2 ? n / 2 : n));
-        map_set_dim<1>(at, (uint32_t)(i < 2 ? H : H / 128));
-        asm volatile("tensormap.replace.tile.global_stride.shared::cta.b1024.b64 [%0], 0, %1;" ::"r"(at), "l"(pitch)
-                     : "memory");
+        if (i < 2) {                              // codes: [H][n / 2] bytes
+            map_set_dim<0>(at, (uint32_t)(n / 2));
+            map_set_pitch<0>(at, n / 2);
+        } else {                                  // scales: [H / 128][n / 16][128] bytes
+            map_set_dim<1>(at, (uint32_t)(n / 16));
+            map_set_pitch<1>(at, n * 8);
+        }
     }
     __syncwarp();
     asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned"
@@ -122,11 +129,12 @@ bool code_map(CUtensorMap *m, const void *p, int64_t inner, int64_t outer, int64
                        {(uint64_t)pitch, (uint64_t)(pitch * outer)}, {128, (uint32_t)rows, 1}, 128);
 }
 
-// Tiled scales: rows of `tiles` tiles of 512 bytes, copied four tiles x `rows`.
-bool scale_map(CUtensorMap *m, const void *p, int64_t tiles, int64_t outer, int64_t experts, int rows)
+// Tiled scales: blocks of 128 rows, each of `tiles` tiles of 512 bytes; copied
+// four tiles at a time of `blocks` blocks, as pieces of 128 bytes.
+bool scale_map(CUtensorMap *m, const void *p, int64_t tiles, int64_t count, int blocks)
 {
-    return make_map_3d(m, MapType::I64, p, {(uint64_t)tiles * 64, (uint64_t)outer, (uint64_t)experts},
-                       {(uint64_t)tiles * 512, (uint64_t)(tiles * outer) * 512}, {256, (uint32_t)rows, 1}, 0);
+    return make_map_3d(m, MapType::U8, p, {128, (uint64_t)tiles * 4, (uint64_t)count}, {128, (uint64_t)tiles * 512},
+                       {128, 16, (uint32_t)blocks}, 0);
 }
 
 template <int kCtas> cudaError_t gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a)
@@ -140,8 +148,8 @@ template <int kCtas> cudaError_t gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a
         return cudaSuccess;
     const bool ok = code_map(&p.map[kMapA], a.w, a.K / 2, a.N, a.ld_w, a.E, 128) &&
                     code_map(&p.map[kMapB], a.x, a.K / 2, a.R_cap, a.ld_x, 1, 64) &&
-                    scale_map(&p.map[kMapSa], a.w_scales, kt, ceil_div(a.N, 128), a.E, 1) &&
-                    scale_map(&p.map[kMapSb], a.x_scales, kt, blocks, 1, 2) &&
+                    scale_map(&p.map[kMapSa], a.w_scales, kt, ceil_div(a.N, 128) * a.E, 1) &&
+                    scale_map(&p.map[kMapSb], a.x_scales, kt, blocks, 2) &&
                     make_map_3d(&p.out, MapType::Bf16, a.out, {(uint64_t)a.N, (uint64_t)a.R_cap, 1},
                                 {(uint64_t)a.N * 2, (uint64_t)a.N * 2 * a.R_cap}, {32, 32, 1}, 64);
     if (!ok)
@@ -171,8 +179,8 @@ template <bool kF32, int kCtas> cudaError_t wgrad(const LaunchCtx &c, const Nvfp
         const int64_t n = (a.R_cap + 127) / 128 * 128;
         const bool ok = code_map(&m.like[kMapA], a.dy, n / 2, a.N, n / 2, 1, 128) &&
                         code_map(&m.like[kMapB], a.x, n / 2, a.K, n / 2, 1, 64) &&
-                        scale_map(&m.like[kMapSa], a.dy_scales, n / 64, a.N / 128, 1, 1) &&
-                        scale_map(&m.like[kMapSb], a.x_scales, n / 64, a.K / 128, 1, 2);
+                        scale_map(&m.like[kMapSa], a.dy_scales, n / 64, a.N / 128, 1) &&
+                        scale_map(&m.like[kMapSb], a.x_scales, n / 64, a.K / 128, 2);
         if (!ok)
             return cudaErrorInvalidValue;
         m.base[kMapA] = a.dy;

@@ -43,7 +43,7 @@ bool make_map_3d(CUtensorMap *m, MapType type, const void *base, const uint64_t 
     if (!enc)
         return false;
     constexpr CUtensorMapDataType types[] = {CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                             CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_DATA_TYPE_INT64};
+                                             CU_TENSOR_MAP_DATA_TYPE_FLOAT32};
     cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
     cuuint64_t s[2] = {pitches[0], pitches[1]};
     cuuint32_t b[3] = {box[0], box[1], box[2]};
