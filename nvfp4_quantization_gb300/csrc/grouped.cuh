@@ -20,9 +20,10 @@
 
 namespace epq {
 
-constexpr int kGThreads = 256;
+constexpr int kGThreads = 384;
 constexpr int kTileN = 256;
 constexpr int kGroupTiles = 8;       // tiles of the N side that share the M side's tiles in L2
+constexpr int kOutWarps = 8;         // of them two to a quarter of the accumulator's lanes
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 enum { kMapA = 0, kMapB = 1, kMapSa = 2, kMapSb = 3 };
@@ -54,11 +55,9 @@ template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_> struct G
     static constexpr uint32_t kSbBytes = kFp4 ? 4096 : 0;
     static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
     static constexpr uint32_t kOutBytes = kWgrad ? 4096 : 2048;   // a warp's piece of a tile
-    static constexpr int kPieces = 3;                             // of them on their way out
-    static constexpr uint32_t kOutAll = 4 * kPieces * kOutBytes;
-    static constexpr uint32_t kRowScales = kFp4 && !kWgrad ? 4 * kTileN * 4 : 0;
-    static constexpr uint32_t kPlan = 4608;                       // barriers and tile counts of 1024 experts
-    static constexpr uint32_t kRest = 1024 + kOutAll + kRowScales + kPlan;    // 1024: the ring's alignment
+    static constexpr uint32_t kOutAll = kOutWarps * kOutBytes;
+    static constexpr uint32_t kPlan = 2560;                       // barriers and tile counts of 1024 experts
+    static constexpr uint32_t kRest = kOutAll + kPlan;
     static constexpr int kStages = (int)((232448 - kRest) / kStageBytes);
     // tensor memory: two accumulators of 256 columns; with block scales the two
     // overlap in 64 columns, which are emptied first
@@ -69,7 +68,7 @@ template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_> struct G
 
 struct __align__(8) GroupedBars {      // up to 8 stages
     uint64_t full[8], empty[8], tail[8];
-    uint64_t acc_full[2], acc_empty[2];
+    uint64_t acc_full[2], acc_empty[2], acc_shared;
     uint32_t tmem, pad;
 };
 
@@ -115,9 +114,9 @@ template <class C>
 __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams &p, const int *start, int t)
 {
     GroupedTile o = {};
-    if (t >= start[p.E])
+    if (t >= start[(p.E + 1) >> 1])
         return o;
-    int lo = 0, hi = p.E - 1;
+    int lo = 0, hi = (p.E - 1) >> 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (start[mid] <= t)
@@ -125,12 +124,19 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams &p, cons
         else
             hi = mid - 1;
     }
-    o.e = lo;
     uint32_t err = 0;
-    const int rows = expert_rows<C>(p, lo, o.row0, err);
-    const int mt = m_tiles<C>(p), nt = ((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN;
+    const int mt = m_tiles<C>(p);
+    int j = t - start[lo];
+    o.e = 2 * lo;
+    int rows = expert_rows<C>(p, o.e, o.row0, err);
+    int nt = ((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN;
+    if (j >= mt * nt) {
+        j -= mt * nt;
+        rows = expert_rows<C>(p, ++o.e, o.row0, err);
+        nt = ((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN;
+    }
     // groups of kGroupTiles tiles of the N side; in a group they change fastest
-    const int j = t - start[lo], g = j / (kGroupTiles * mt), in = j - g * kGroupTiles * mt;
+    const int g = j / (kGroupTiles * mt), in = j - g * kGroupTiles * mt;
     const int gn = min(kGroupTiles, nt - g * kGroupTiles);
     const int mi = in / gn, ni = g * kGroupTiles + in - mi * gn;
     o.m0 = mi * 128 * C::kCtas;
@@ -138,7 +144,7 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams &p, cons
     if (C::kWgrad) {
         o.rows = rows;
         if (p.counts)
-            o.rows = max(0, min(rows, __ldg(p.counts + lo)));
+            o.rows = max(0, min(rows, __ldg(p.counts + o.e)));
         o.n = min(kTileN, p.N - o.n0);
         o.kb = (o.rows + C::kBlockK - 1) / C::kBlockK;
     } else {
@@ -182,19 +188,21 @@ template <class C> struct GroupedWalk {
     }
 };
 
-// Tiles of every expert summed up, in shared memory; what is wrong with the
-// offsets goes to the status word.
+// Tiles before every second expert, and all of them, in shared memory; what is
+// wrong with the offsets goes to the status word.
 template <class C>
 __device__ __forceinline__ void grouped_plan(const GroupedParams &p, int *start, int *partial)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.E + kGThreads - 1) / kGThreads, e0 = tid * per;
-    const int mt = m_tiles<C>(p);
+    constexpr int kPer = 4;                       // experts of a thread: 1024 and more in all
+    const int e0 = tid * kPer, mt = m_tiles<C>(p);
     uint32_t err = 0;
-    int mine = 0, off;
-    for (int e = e0; e < min(e0 + per, p.E); ++e) {
-        const int rows = expert_rows<C>(p, e, off, err);
-        mine += mt * (((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN);
+    int n[kPer], mine = 0, off;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int rows = e0 + i < p.E ? expert_rows<C>(p, e0 + i, off, err) : 0;
+        n[i] = e0 + i < p.E ? mt * (((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN) : 0;
+        mine += n[i];
     }
     int sum = mine;
 #pragma unroll
@@ -209,31 +217,51 @@ __device__ __forceinline__ void grouped_plan(const GroupedParams &p, int *start,
     int at = sum - mine;
     for (int w = 0; w < warp; ++w)
         at += partial[w];
-    uint32_t ignore = 0;
-    for (int e = e0; e < min(e0 + per, p.E); ++e) {
-        start[e] = at;
-        const int rows = expert_rows<C>(p, e, off, ignore);
-        at += mt * (((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if ((i & 1) == 0 && e0 + i < p.E)
+            start[(e0 + i) >> 1] = at;
+        at += n[i];
     }
     if (tid == kGThreads - 1)
-        start[p.E] = at;       // the last threads have no expert or the last ones
+        start[(p.E + 1) >> 1] = at;               // the last thread has no expert
     if (err && blockIdx.x == 0)
         raise_status(p.status, err);
 }
+
+// A place in the ring of stages.
+template <int kStages> struct GroupedRing {
+    uint32_t s = 0, phase = 0;
+    __device__ __forceinline__ void step()
+    {
+        if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    __device__ __forceinline__ GroupedRing before(uint32_t n) const      // n <= kStages
+    {
+        GroupedRing r = *this;
+        if (r.s < n) {
+            r.s += kStages;
+            r.phase ^= 1;
+        }
+        r.s -= n;
+        return r;
+    }
+};
 
 template <class C>
 __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_constant__ GroupedParams p)
 {
     constexpr int kCtas = C::kCtas, kStages = C::kStages;
-    extern __shared__ uint8_t g_smem_raw[];
-    const uint32_t raw = smem_u32(g_smem_raw);
-    uint8_t *const base = g_smem_raw + ((1024 - (raw & 1023)) & 1023);
+    extern __shared__ __align__(1024) uint8_t g_smem[];          // stages, pieces of output, barriers, plan
+    uint8_t *const base = g_smem;
     const uint32_t ring = smem_u32(base);
     uint8_t *const out_s = base + kStages * C::kStageBytes;
-    float *const row_scale_s = reinterpret_cast<float *>(out_s + C::kOutAll);    // [4][256]
-    GroupedBars &bar = *reinterpret_cast<GroupedBars *>(out_s + C::kOutAll + C::kRowScales);
-    int *const start = reinterpret_cast<int *>(&bar + 1);                        // [E + 1]
-    int *const partial = start + p.E + 1;                                        // [8]
+    GroupedBars &bar = *reinterpret_cast<GroupedBars *>(out_s + C::kOutAll);
+    int *const partial = reinterpret_cast<int *>(&bar + 1);      // [kGThreads / 32]
+    int *const start = partial + kGThreads / 32;                 // [(E + 1) / 2 + 1]
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
@@ -247,8 +275,9 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bar.acc_full[b], 1);
-            mbar_init(&bar.acc_empty[b], 4 * kCtas);
+            mbar_init(&bar.acc_empty[b], kOutWarps * kCtas);
         }
+        mbar_init(&bar.acc_shared, kOutWarps * kCtas);
         fence_mbar_init();
     }
     if (warp == 2)
@@ -262,15 +291,17 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = bar.tmem;
-    const int tiles = start[p.E];
-    // barriers that the leader's matrix products wait on
-    const uint32_t full0 = kCtas == 2 ? at_rank(smem_u32(&bar.full[0]), 0) : smem_u32(&bar.full[0]);
+    const int tiles = start[(p.E + 1) >> 1];
+    // barriers that the products wait on: the leader's
+    auto at_leader = [&](uint64_t *b) { return kCtas == 2 ? at_rank(smem_u32(b), 0) : smem_u32(b); };
+    const uint32_t full0 = at_leader(&bar.full[0]);
     bool ok = true;
     GroupedWalk<C> walk(p, start, unit, units);
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies
-        uint32_t it = 0, cut_it = 0;
+        GroupedRing<kStages> at;
+        uint32_t used = 0, cut_it = 0;
         int last_e = -1;
         const CUtensorMap *maps = p.map;
         for (int t = unit; t < tiles && ok; t += units) {
@@ -284,23 +315,21 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                 __syncwarp();
                 last_e = o.e;
             }
-            const int tail_rows = C::kWgrad && !C::kFp4 && p.counts ? o.rows % C::kBlockK : 0;
+            const bool has_cut = C::kBmn && p.counts && o.rows % C::kBlockK;
             const int m = o.m0 + 128 * (int)rank, n = o.n0 + half * (int)rank;
-            for (int kb = 0; kb < o.kb; ++kb, ++it) {
-                const int s = (int)(it % kStages);
-                if (it >= kStages &&
-                    !__all_sync(0xffffffffu, mbar_wait_for(&bar.empty[s], ((it / kStages) - 1) & 1, kWaitNs))) {
+            for (int kb = 0; kb < o.kb; ++kb) {
+                if (used >= kStages &&
+                    !__all_sync(0xffffffffu, mbar_wait_for(&bar.empty[at.s], at.phase ^ 1, kWaitNs))) {
                     ok = false;
                     break;
                 }
-                // a last block of rows that has to be cut is counted on a barrier
-                // of this CTA's own first
-                const bool cut = tail_rows && kb == o.kb - 1;
-                const uint32_t f = cut ? smem_u32(&bar.tail[cut_it % kStages]) : full0 + 8 * s;
-                cut_it += cut;
-                const uint32_t a = ring + s * C::kStageBytes, b = a + C::kABytes;
-                const int k0 = kb * C::kBlockK;
                 if (elect_one()) {
+                    // a last block of rows that has to be cut is counted on a barrier
+                    // of this CTA's own first
+                    const uint32_t f = has_cut && kb == o.kb - 1 ? smem_u32(&bar.tail[cut_it % kStages])
+                                                                 : full0 + 8 * at.s;
+                    const uint32_t a = ring + at.s * C::kStageBytes, b = a + C::kABytes;
+                    const int k0 = kb * C::kBlockK;
                     mbar_arrive_expect_tx_at(f, bytes);
                     if constexpr (C::kFp4) {
                         const int x = k0 / 2, ys = k0 / 16;               // bytes; pieces of 128 bytes of scales
@@ -329,82 +358,87 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                     }
                 }
                 __syncwarp();
+                at.step();
+                ++used;
             }
+            cut_it += has_cut;
         }
         // never leave with copies in flight: in each stage the last one's
         // consumption, or at least its arrival
-        for (uint32_t i = it > (uint32_t)kStages ? it - kStages : 0; i < it; ++i)
-            if (!mbar_wait_for(&bar.empty[i % kStages], (i / kStages) & 1, kWaitNs)) {
-                ok = false;
-                if (rank == 0)
-                    (void)mbar_wait_for(&bar.full[i % kStages], (i / kStages) & 1, kWaitNs);
+        if (elect_one()) {
+            for (uint32_t i = min(used, (uint32_t)kStages); i > 0; --i) {
+                const GroupedRing<kStages> back = at.before(i);
+                if (!mbar_wait_for(&bar.empty[back.s], back.phase, kWaitNs)) {
+                    ok = false;
+                    if (rank == 0)
+                        (void)mbar_wait_for(&bar.full[back.s], back.phase, kWaitNs);
+                }
             }
+        }
         ok = __all_sync(0xffffffffu, ok);
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ products
-        uint32_t it = 0, acc_it = 0;
+        GroupedRing<kStages> at;
+        uint32_t acc_it = 0, last_un = 0;
         for (int t = unit; t < tiles && ok; t += units) {
             const GroupedTile o = walk.tile();
             if (o.kb == 0)
                 continue;
             const uint32_t b = acc_it & 1;
-            if constexpr (C::kFp4)
-                ok = acc_it == 0 || mbar_wait_for(&bar.acc_empty[0], (acc_it - 1) & 1, kWaitNs);
-            else
-                ok = acc_it < 2 || mbar_wait_for(&bar.acc_empty[b], ((acc_it >> 1) - 1) & 1, kWaitNs);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok)
-                break;
-            tmem_fence_after();
             const uint32_t d = tmem + b * C::kAcc1;
             const uint32_t un = (uint32_t)(o.n + 63) / 64 * 64;
             uint32_t idesc = (1u << 7) | (1u << 10) | ((un >> 3) << 17) | ((uint32_t)(8 * kCtas) << 24);
             if (!C::kFp4)
                 idesc |= (1u << 4) | ((uint32_t)C::kAmn << 15) | ((uint32_t)C::kBmn << 16);
             const int k_all = C::kWgrad ? o.rows : p.K;
-            for (int kb = 0; kb < o.kb; ++kb, ++it) {
-                const int s = (int)(it % kStages);
-                const bool cut = C::kBmn && p.counts && kb == o.kb - 1;
-                ok = cut ? mbar_wait_for<true>(&bar.full[s], (it / kStages) & 1, kWaitNs)
-                         : mbar_wait_for(&bar.full[s], (it / kStages) & 1, kWaitNs);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    break;
+            if (elect_one()) {
+                ok = acc_it < 2 || mbar_wait_for(&bar.acc_empty[b], ((acc_it >> 1) - 1) & 1, kWaitNs);
+                // the columns that the accumulators share, where both tiles use them
+                if (C::kFp4 && acc_it > 0 && (b ? last_un : un) > C::kAcc1)
+                    ok = ok && mbar_wait_for(&bar.acc_shared, (acc_it - 1) & 1, kWaitNs);
                 tmem_fence_after();
-                const uint32_t a = ring + s * C::kStageBytes, bb = a + C::kABytes;
-                const int steps = (k_all - kb * C::kBlockK + C::kStepK - 1) / C::kStepK;
-                if (elect_one()) {
+                for (int kb = 0; kb < o.kb && ok; ++kb) {
+                    const bool cut = C::kBmn && p.counts && kb == o.kb - 1;
+                    ok = cut ? mbar_wait_for<true>(&bar.full[at.s], at.phase, kWaitNs)
+                             : mbar_wait_for(&bar.full[at.s], at.phase, kWaitNs);
+                    if (!ok)
+                        break;
+                    tmem_fence_after();
+                    const uint32_t a = ring + at.s * C::kStageBytes, bb = a + C::kABytes;
+                    const uint64_t da = C::kAmn ? desc_mn_major(a) : desc_k_major(a);
+                    const uint64_t db = C::kBmn ? desc_mn_major(bb) : desc_k_major(bb);
+                    constexpr uint64_t ja = (C::kAmn ? 2048 : 32) >> 4, jb = (C::kBmn ? 2048 : 32) >> 4;   // a step
+                    const int steps = (k_all - kb * C::kBlockK + C::kStepK - 1) / C::kStepK;
                     if constexpr (C::kFp4) {
-                        const uint32_t sa = bb + C::kBBytes, sb = sa + C::kSaBytes;
+                        const uint64_t dsa = desc_scales(bb + C::kBBytes), dsb = dsa + (C::kSaBytes >> 4);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if (j < steps) {
-                                tmem_cp_scales<kCtas>(tmem + C::kSaCol + 4 * j, desc_scales(sa + 512 * j));
-                                tmem_cp_scales<kCtas>(tmem + C::kSbCol + 8 * j, desc_scales(sb + 512 * j));
+                                tmem_cp_scales<kCtas>(tmem + C::kSaCol + 4 * j, dsa + 32 * j);
+                                tmem_cp_scales<kCtas>(tmem + C::kSbCol + 8 * j, dsb + 32 * j);
                                 if (un > 128)
-                                    tmem_cp_scales<kCtas>(tmem + C::kSbCol + 8 * j + 4,
-                                                          desc_scales(sb + 2048 + 512 * j));
+                                    tmem_cp_scales<kCtas>(tmem + C::kSbCol + 8 * j + 4, dsb + 128 + 32 * j);
                             }
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if (j < steps)
-                                mma_nvfp4<kCtas>(d, desc_k_major(a + 32 * j), desc_k_major(bb + 32 * j), idesc,
-                                                 tmem + C::kSaCol + 4 * j, tmem + C::kSbCol + 8 * j, kb > 0 || j > 0);
+                                mma_nvfp4<kCtas>(d, da + ja * j, db + jb * j, idesc, tmem + C::kSaCol + 4 * j,
+                                                 tmem + C::kSbCol + 8 * j, kb > 0 || j > 0);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if (j < steps)
-                                mma_bf16<kCtas>(d, C::kAmn ? desc_mn_major(a + 2048 * j) : desc_k_major(a + 32 * j),
-                                                C::kBmn ? desc_mn_major(bb + 2048 * j) : desc_k_major(bb + 32 * j),
-                                                idesc, kb > 0 || j > 0);
+                                mma_bf16<kCtas>(d, da + ja * j, db + jb * j, idesc, kb > 0 || j > 0);
                     }
-                    mma_commit<kCtas>(smem_u32(&bar.empty[s]));
-                    if (kb == o.kb - 1)
-                        mma_commit<kCtas>(smem_u32(&bar.acc_full[b]));
+                    mma_commit<kCtas>(smem_u32(&bar.empty[at.s]));
+                    at.step();
                 }
-                __syncwarp();
+                if (ok)
+                    mma_commit<kCtas>(smem_u32(&bar.acc_full[b]));
             }
+            ok = __all_sync(0xffffffffu, ok);
+            last_un = un;
             ++acc_it;
         }
     } else if (C::kWgrad && !C::kFp4 && warp == 3 && p.counts) {
@@ -435,12 +469,11 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ sums
-        const int w = warp - 4;
-        uint8_t *const mine = out_s + w * C::kPieces * C::kOutBytes;
-        float *const ts_w = row_scale_s + kTileN * w;
-        const uint32_t acc_empty0 = kCtas == 2 ? at_rank(smem_u32(&bar.acc_empty[0]), 0) : smem_u32(&bar.acc_empty[0]);
+        const int w = warp & 3, side = (warp - 4) >> 2;         // its lanes; which of every two pieces
+        uint8_t *const dst = out_s + (warp - 4) * C::kOutBytes;
+        const uint32_t d = smem_u32(dst);
+        const uint32_t acc_empty0 = at_leader(&bar.acc_empty[0]), acc_shared = at_leader(&bar.acc_shared);
         uint32_t acc_it = 0;
-        int piece = 0;
         for (int t = unit; t < tiles; t += units) {
             const GroupedTile o = walk.tile();
             if (o.kb == 0 && p.add)
@@ -448,6 +481,10 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             const int m = o.m0 + 128 * (int)rank + 32 * w;      // first of this warp's 32 rows of the M side
             const uint32_t b = acc_it & 1;
             const uint32_t acc = tmem + ((uint32_t)(32 * w) << 16) + b * C::kAcc1;
+            const int nch = (o.n + C::kChunk - 1) / C::kChunk;
+            // with overlapping accumulators the shared columns come first: the end
+            // of the one, the beginning of the other
+            const bool back = C::kFp4 && b == 0;
             float ms[4], scale0 = 1.f, scale1 = 1.f;
             if constexpr (C::kFp4 && !C::kWgrad) {
 #pragma unroll
@@ -455,59 +492,32 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                     const int f = m + 8 * h + lane / 4;
                     ms[h] = f < p.M ? __ldg(p.m_scale + (int64_t)o.e * p.M + f) : 0.f;
                 }
-                __syncwarp();
-#pragma unroll
-                for (int c = 0; c < kTileN / 32; ++c)
-                    ts_w[32 * c + lane] = 32 * c + lane < o.n ? __ldg(p.n_scale + o.row0 + o.n0 + 32 * c + lane) : 0.f;
-                __syncwarp();
             } else if constexpr (C::kFp4) {
                 scale0 = __fdiv_rn(1.f, __ldg(p.m_scale + o.e));
                 scale1 = __fdiv_rn(1.f, __ldg(p.n_scale + o.e));
             }
-            const int nch = (o.n + C::kChunk - 1) / C::kChunk;
-            // with overlapping accumulators the shared columns come first: the end
-            // of the one, the beginning of the other
-            const int last_shared = C::kFp4 ? min(nch - 1, 64 / C::kChunk - 1) : nch - 1;
-            const bool back = C::kFp4 && b == 0;
-            auto load = [&](int cc, uint32_t *r) {
-                const uint32_t at0 = acc + C::kChunk * (back ? nch - 1 - cc : cc);
-                if constexpr (!C::kWgrad) {
-                    tmem_ld_16x32(at0, r);
-                    tmem_ld_16x32(at0 + (16u << 16), r + 16);
-                } else {
-                    tmem_ld_32x32(at0, r);
-                    if constexpr (C::kChunk == 64)
-                        tmem_ld_32x32(at0 + 32, r + 32);
-                }
+            // the row scale of token `lane` of a piece
+            auto row_scale = [&](int cc) {
+                const int i = 32 * (back ? nch - 1 - cc : cc) + lane;
+                return C::kFp4 && !C::kWgrad && cc < nch && i < o.n ? __ldg(p.n_scale + o.row0 + o.n0 + i) : 0.f;
             };
-            auto arrived = [&](int cc, uint32_t *r) {
-                tmem_wait_ld(r);
-                if constexpr (C::kChunk == 64)
-                    tmem_wait_ld(r + 32);
-                if (cc == last_shared) {
-                    tmem_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_at(acc_empty0 + (C::kFp4 ? 0 : 8 * b));
-                }
-            };
+            float ts_next = row_scale(side), ts_lane = 0.f;
             auto emit = [&](int cc, uint32_t *r) {
                 if (m >= p.M)
                     return;
                 const int c = back ? nch - 1 - cc : cc;
-                uint8_t *const dst = mine + piece * C::kOutBytes;
-                piece = piece == C::kPieces - 1 ? 0 : piece + 1;
-                if (lane == 0)
-                    tma_store_wait_read<C::kPieces - 1>();
+                if (elect_one())
+                    tma_store_wait_read0();
                 __syncwarp();
-                const uint32_t d = smem_u32(dst);
                 if constexpr (!C::kWgrad) {
                     // 32 tokens x 32 features, a token's 64 bytes in a row (64-byte swizzle)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float2 ts = make_float2(1.f, 1.f);
-                        if constexpr (C::kFp4)
-                            ts = *reinterpret_cast<const float2 *>(ts_w + 32 * c + 8 * i + 2 * (lane & 3));
+                        if constexpr (C::kFp4) {
+                            ts.x = __shfl_sync(0xffffffffu, ts_lane, 8 * i + 2 * (lane & 3));
+                            ts.y = __shfl_sync(0xffffffffu, ts_lane, 8 * i + 2 * (lane & 3) + 1);
+                        }
                         uint32_t q[4];
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
@@ -524,7 +534,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         tma_store_3d<false>(&p.out, m, o.row0 + o.n0 + 32 * c, 0, d);
                         tma_store_commit();
                     }
@@ -546,7 +556,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                             make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         if (C::kF32 && p.add)
                             tma_store_3d<true>(&p.out, o.n0 + C::kChunk * c, m, o.e, d);
                         else
@@ -555,13 +565,13 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                     }
                 }
             };
-            uint32_t ra[C::kChunk], rb[C::kChunk];
+            uint32_t r[C::kChunk];
             if (C::kWgrad && o.kb == 0) {          // no rows: zeros
-                for (int cc = 0; cc < nch; ++cc) {
+                for (int cc = side; cc < nch; cc += 2) {
 #pragma unroll
                     for (int i = 0; i < C::kChunk; ++i)
-                        ra[i] = 0u;
-                    emit(cc, ra);
+                        r[i] = 0u;
+                    emit(cc, r);
                 }
                 continue;
             }
@@ -572,22 +582,42 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             }
             ++acc_it;
             tmem_fence_after();
-            // the next columns are on their way while these are written
-            load(0, ra);
-            for (int cc = 0; cc < nch; cc += 2) {
-                arrived(cc, ra);
-                if (cc + 1 < nch)
-                    load(cc + 1, rb);
-                emit(cc, ra);
-                if (cc + 1 < nch) {
-                    arrived(cc + 1, rb);
-                    if (cc + 2 < nch)
-                        load(cc + 2, ra);
-                    emit(cc + 1, rb);
+            int cc = side;
+            do {
+                if (cc < nch) {
+                    const uint32_t at0 = acc + C::kChunk * (back ? nch - 1 - cc : cc);
+                    if constexpr (!C::kWgrad) {
+                        tmem_ld_16x32(at0, r);
+                        tmem_ld_16x32(at0 + (16u << 16), r + 16);
+                    } else {
+                        tmem_ld_32x32(at0, r);
+                        if constexpr (C::kChunk == 64)
+                            tmem_ld_32x32(at0 + 32, r + 32);
+                    }
+                    ts_lane = ts_next;
+                    ts_next = row_scale(cc + 2);
+                    tmem_wait_ld(r);
+                    if constexpr (C::kChunk == 64)
+                        tmem_wait_ld(r + 32);
                 }
-            }
+                // what the next products wait for
+                const bool first = C::kFp4 && cc == side, last = cc + 2 >= nch;
+                if (first || last) {
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (first)
+                            mbar_arrive_at(acc_shared);
+                        if (last)
+                            mbar_arrive_at(acc_empty0 + 8 * b);
+                    }
+                }
+                if (cc < nch)
+                    emit(cc, r);
+                cc += 2;
+            } while (cc < nch);
         }
-        if (lane == 0)
+        if (elect_one())
             tma_store_wait0();
     }
 

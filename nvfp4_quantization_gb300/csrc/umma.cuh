@@ -116,13 +116,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int x, int y,
                          (uint64_t)m), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
 }
 
-// All but the newest n stores of this thread have read their shared memory.
-template <int n>
-__device__ __forceinline__ void tma_store_wait_read()
-{
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
-}
-
 // A tensor map that another kernel wrote: its bytes before any use through the
 // tensor-map proxy.
 __device__ __forceinline__ void tensormap_acquire(const CUtensorMap *m)
