@@ -713,31 +713,34 @@ def ep_nvfp4_operand(rows: torch.Tensor, H: int, offsets: torch.Tensor | None = 
     ep_nvfp4_pack_weights makes them (no ``offsets``)."""
     if not rows.is_cuda:
         raise ValueError("rows must be a CUDA tensor")
-    S = (9 * H // 16 + 31) // 16 * 16                          # row_bytes(H)
-    if rows.dim() not in (2, 3):
+    shape, S = rows.shape, (9 * H // 16 + 31) // 16 * 16       # S = row_bytes(H)
+    if len(shape) == 2:
+        (n, width), groups = shape, 1
+        _need_offsets(offsets, E)
+    elif len(shape) == 3:
+        groups, n, width = shape
+        if offsets is not None or E != 1:
+            raise ValueError("weights take no offsets")
+    else:
         raise ValueError("rows must have two or three dimensions")
-    _need_dense(rows, "rows", tuple(rows.shape[:-1]) + (S,), torch.uint8)
-    groups, n = (1, rows.shape[0]) if rows.dim() == 2 else (rows.shape[0], rows.shape[1])
-    if rows.dim() == 3 and (offsets is not None or E != 1):
-        raise ValueError("weights take no offsets")
-    _need_offsets(offsets, E)
-    dev = rows.device
-    nbytes = groups * nvfp4_scale_bytes(n, H)
+    if width != S or rows.dtype != torch.uint8 or not rows.is_contiguous():
+        raise ValueError(f"rows must be contiguous uint8 rows of {S} bytes, got {rows.dtype} {tuple(shape)}")
+    dev, nbytes = rows.device, groups * nvfp4_scale_bytes(n, H)
     if scales is None:
         scales = _empty((nbytes,), torch.uint8, dev, stream)
     else:
         _need_dense(scales, "scales", (nbytes,), torch.uint8)
-    shape = tuple(rows.shape[:-1])
     if row_scale is None:
-        row_scale = _empty(shape, torch.float32, dev, stream)
+        row_scale = _empty(shape[:-1], torch.float32, dev, stream)
     else:
-        _need_dense(row_scale, "row_scale", shape, torch.float32)
+        _need_dense(row_scale, "row_scale", shape[:-1], torch.float32)
     status = _status_or_new(status, dev, stream)
     st = _lib.lib().ep_nvfp4_operand(rows.data_ptr(), groups, n, H, _at(offsets), E, scales.data_ptr(),
                                      row_scale.data_ptr(), status.data_ptr(), _stream_of(stream, dev))
     if st:
         check("ep_nvfp4_operand", st)
-    return {"rw_codes": rows[..., : H // 2], "rw_scales": scales, "rw_row_scale": row_scale}
+    codes = rows.as_strided((n, H // 2), (S, 1)) if groups == 1 and len(shape) == 2 else rows[..., : H // 2]
+    return {"rw_codes": codes, "rw_scales": scales, "rw_row_scale": row_scale}
 
 
 def _need_bytes(t: torch.Tensor, name: str, n: int):

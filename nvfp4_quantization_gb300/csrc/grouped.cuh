@@ -668,6 +668,21 @@ template <class C> cudaError_t grouped_units(const LaunchCtx &c, int &units)
     return cudaSuccess;
 }
 
+// Whether single CTAs (128 x 256 a tile) rather than pairs (256 x 256) take a call
+// whose M side has M rows and whose N sides make n_tiles tiles.  A pair reads half
+// the bytes of the N side a CTA; single CTAs have the finer tiles.  Measured on
+// GB300, single against pair: where all tiles run at once 8.5 us against 9.2 (one
+// token, 2 of 8 experts of 1024 x 1024, BF16); where rounds of tiles decide 14.5
+// against 18.0 (16 experts of 1152 x 1024, NVFP4 weight gradient: 4 rounds against
+// 5); with many rounds 1.06 (BF16 products), 1.14 to 1.23 (weight gradients) and
+// 1.36 (NVFP4 products) times the pair's time.
+template <class C> bool single_ctas(const LaunchCtx &c, int64_t M, int64_t n_tiles)
+{
+    const int64_t one = (M + 127) / 128 * n_tiles, pair = (M + 255) / 256 * n_tiles;
+    const int64_t rounds1 = (one + c.num_sms - 1) / c.num_sms, rounds2 = (pair + c.num_sms / 2 - 1) / (c.num_sms / 2);
+    return one <= c.num_sms || rounds1 * (C::kWgrad ? 12 : C::kFp4 ? 14 : 11) < rounds2 * 10;
+}
+
 // `most_tiles`: a bound on the call's tiles that the host knows.
 template <class C> cudaError_t launch_grouped(const LaunchCtx &c, const GroupedParams &p, int64_t most_tiles)
 {

@@ -63,11 +63,16 @@ cudaError_t launch_grouped_gemm(const LaunchCtx &c, const GroupedGemmArgs &a)
 {
     if (a.R_cap == 0)
         return cudaSuccess;
+    // tiles of the rows: about half a tile an expert is lost in its slot
+    if (single_ctas<GroupedCfg<false, false, false, 1, false>>(c, a.N, ceil_div(a.R_cap, kTileN) + a.E / 2))
+        return a.transposed ? gemm<true, 1>(c, a) : gemm<false, 1>(c, a);
     return a.transposed ? gemm<true, 2>(c, a) : gemm<false, 2>(c, a);
 }
 
 cudaError_t launch_grouped_wgrad(const LaunchCtx &c, const GroupedWgradArgs &a)
 {
+    if (single_ctas<GroupedCfg<false, true, true, 1, false>>(c, a.N, a.E * ceil_div(a.K, kTileN)))
+        return a.f32 ? wgrad<true, 1>(c, a) : wgrad<false, 1>(c, a);
     return a.f32 ? wgrad<true, 2>(c, a) : wgrad<false, 2>(c, a);
 }
 

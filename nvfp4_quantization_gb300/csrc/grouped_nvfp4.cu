@@ -221,11 +221,15 @@ cudaError_t launch_operand(const LaunchCtx &c, const OperandArgs &a)
 
 cudaError_t launch_nvfp4_gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a)
 {
+    if (single_ctas<GroupedCfg<true, false, false, 1, false>>(c, a.N, ceil_div(a.R_cap, kTileN) + a.E / 2))
+        return gemm<1>(c, a);
     return gemm<2>(c, a);
 }
 
 cudaError_t launch_nvfp4_wgrad(const LaunchCtx &c, const Nvfp4WgradArgs &a)
 {
+    if (single_ctas<GroupedCfg<true, true, false, 1, false>>(c, a.N, a.E * ceil_div(a.K, kTileN)))
+        return a.f32 ? wgrad<true, 1>(c, a) : wgrad<false, 1>(c, a);
     return a.f32 ? wgrad<true, 2>(c, a) : wgrad<false, 2>(c, a);
 }
 
