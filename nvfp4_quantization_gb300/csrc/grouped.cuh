@@ -8,11 +8,11 @@
 //   rows as K (kWgrad true):   d_w[e][m][n] = sum_r dy[r][m] x[r][n].
 //
 // A persistent kernel: one CTA a SM, tiles of 128 x kCtas by up to 256 dealt
-// out in turn.  Warp 0 feeds a ring of shared-memory stages by TMA (128 bytes
-// along K a row and stage: 64 BF16 or 256 E2M1), one thread of warp 1 issues
-// the matrix products into tensor memory, warps 4-7 take finished sums from
-// there to global memory while the next tile is computed in the other half of
-// tensor memory.
+// out in turn.  Warps 0-7 take finished sums from tensor memory to global memory
+// while the next tile is computed in the other half of tensor memory; warp 8
+// feeds a ring of shared-memory stages by TMA (128 bytes along K a row and
+// stage: 64 BF16 or 256 E2M1), one thread of warp 9 issues the matrix products
+// into tensor memory, warp 10 cuts ragged blocks.
 #pragma once
 
 #include "epq_internal.h"
@@ -20,10 +20,11 @@
 
 namespace epq {
 
-constexpr int kGThreads = 384;
+constexpr int kGThreads = 352;       // 11 warps: up to 184 registers a thread
 constexpr int kTileN = 256;
 constexpr int kGroupTiles = 8;       // tiles of the N side that share the M side's tiles in L2
-constexpr int kOutWarps = 8;         // of them two to a quarter of the accumulator's lanes
+constexpr int kOutWarps = 8;         // two to a quarter of the accumulator's lanes
+constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpCut = 10;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 enum { kMapA = 0, kMapB = 1, kMapSa = 2, kMapSb = 3 };
@@ -64,6 +65,15 @@ template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_> struct G
     static constexpr uint32_t kAcc1 = kFp4 ? 192 : 256;
     static constexpr uint32_t kSaCol = 448, kSbCol = 464;
     static constexpr int kChunk = kWgrad && !kF32 ? 64 : 32;      // columns that the epilogue takes at a time
+    // FP32 outputs: a sum is taken out of tensor memory after this many blocks of K
+    // and its parts added up in FP32.  The matrix unit truncates as it adds, so its
+    // error grows with its additions: over 2048 rows of BF16 (128 additions) 2.1e-6
+    // of the result, over 65536 7.6e-5; in parts of 768 rows 6.8e-7 and 7.5e-7.
+    // NVFP4 loses less (16384 rows 2.0e-6, in parts of 8192 8.2e-7).  BF16 keeps
+    // its parts in registers (4 % of a step with 2048 rows an expert), NVFP4, where
+    // there is seldom more than one, adds them in global memory.
+    static constexpr bool kParts = kWgrad && kF32, kKeep = kParts && !kFp4;
+    static constexpr int kPartBlocks = kFp4 ? 32 : 12;
 };
 
 struct __align__(8) GroupedBars {      // up to 8 stages
@@ -280,7 +290,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
         mbar_init(&bar.acc_shared, kOutWarps * kCtas);
         fence_mbar_init();
     }
-    if (warp == 2)
+    if (warp == kWarpCut)
         tmem_alloc<kCtas>(smem_u32(&bar.tmem), 512);
     pdl_launch_dependents();
     pdl_wait();
@@ -298,7 +308,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
     bool ok = true;
     GroupedWalk<C> walk(p, start, unit, units);
 
-    if (warp == 0) {
+    if (warp == kWarpCopy) {
         // ------------------------------------------------------------ copies
         GroupedRing<kStages> at;
         uint32_t used = 0, cut_it = 0;
@@ -376,7 +386,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             }
         }
         ok = __all_sync(0xffffffffu, ok);
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == kWarpMma && rank == 0) {
         // ------------------------------------------------------------ products
         GroupedRing<kStages> at;
         uint32_t acc_it = 0, last_un = 0;
@@ -384,20 +394,29 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             const GroupedTile o = walk.tile();
             if (o.kb == 0)
                 continue;
-            const uint32_t b = acc_it & 1;
-            const uint32_t d = tmem + b * C::kAcc1;
             const uint32_t un = (uint32_t)(o.n + 63) / 64 * 64;
             uint32_t idesc = (1u << 7) | (1u << 10) | ((un >> 3) << 17) | ((uint32_t)(8 * kCtas) << 24);
             if (!C::kFp4)
                 idesc |= (1u << 4) | ((uint32_t)C::kAmn << 15) | ((uint32_t)C::kBmn << 16);
             const int k_all = C::kWgrad ? o.rows : p.K;
             if (elect_one()) {
-                ok = acc_it < 2 || mbar_wait_for(&bar.acc_empty[b], ((acc_it >> 1) - 1) & 1, kWaitNs);
-                // the columns that the accumulators share, where both tiles use them
-                if (C::kFp4 && acc_it > 0 && (b ? last_un : un) > C::kAcc1)
-                    ok = ok && mbar_wait_for(&bar.acc_shared, (acc_it - 1) & 1, kWaitNs);
-                tmem_fence_after();
-                for (int kb = 0; kb < o.kb && ok; ++kb) {
+                uint32_t b = 0, d = 0;
+                bool add = true;
+                for (int kb = 0; kb < o.kb; ++kb) {
+                    if (kb == 0 || (C::kParts && kb % C::kPartBlocks == 0)) {
+                        b = acc_it & 1;
+                        d = tmem + b * C::kAcc1;
+                        add = false;
+                        ok = acc_it < 2 || mbar_wait_for(&bar.acc_empty[b], ((acc_it >> 1) - 1) & 1, kWaitNs);
+                        // the columns that the accumulators share, where both sums use them
+                        if (C::kFp4 && acc_it > 0 && (b ? last_un : un) > C::kAcc1)
+                            ok = ok && mbar_wait_for(&bar.acc_shared, (acc_it - 1) & 1, kWaitNs);
+                        if (!ok)
+                            break;
+                        last_un = un;
+                        ++acc_it;
+                        tmem_fence_after();
+                    }
                     const bool cut = C::kBmn && p.counts && kb == o.kb - 1;
                     ok = cut ? mbar_wait_for<true>(&bar.full[at.s], at.phase, kWaitNs)
                              : mbar_wait_for(&bar.full[at.s], at.phase, kWaitNs);
@@ -424,24 +443,23 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                         for (int j = 0; j < 4; ++j)
                             if (j < steps)
                                 mma_nvfp4<kCtas>(d, da + ja * j, db + jb * j, idesc, tmem + C::kSaCol + 4 * j,
-                                                 tmem + C::kSbCol + 8 * j, kb > 0 || j > 0);
+                                                 tmem + C::kSbCol + 8 * j, add || j > 0);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if (j < steps)
-                                mma_bf16<kCtas>(d, da + ja * j, db + jb * j, idesc, kb > 0 || j > 0);
+                                mma_bf16<kCtas>(d, da + ja * j, db + jb * j, idesc, add || j > 0);
                     }
+                    add = true;
                     mma_commit<kCtas>(smem_u32(&bar.empty[at.s]));
                     at.step();
+                    if (kb == o.kb - 1 || (C::kParts && (kb + 1) % C::kPartBlocks == 0))
+                        mma_commit<kCtas>(smem_u32(&bar.acc_full[b]));
                 }
-                if (ok)
-                    mma_commit<kCtas>(smem_u32(&bar.acc_full[b]));
             }
             ok = __all_sync(0xffffffffu, ok);
-            last_un = un;
-            ++acc_it;
         }
-    } else if (C::kWgrad && !C::kFp4 && warp == 3 && p.counts) {
+    } else if (C::kWgrad && !C::kFp4 && warp == kWarpCut && p.counts) {
         // ------------------------------------------------------------ cut blocks
         // rows of a slot behind the expert's tokens count as zero, whatever they hold
         uint32_t it = 0, cut_it = 0;
@@ -467,10 +485,10 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             if (lane == 0)
                 mbar_arrive_release_at(full0 + 8 * s);
         }
-    } else if (warp >= 4) {
+    } else if (warp < kOutWarps) {
         // ------------------------------------------------------------ sums
-        const int w = warp & 3, side = (warp - 4) >> 2;         // its lanes; which of every two pieces
-        uint8_t *const dst = out_s + (warp - 4) * C::kOutBytes;
+        const int w = warp & 3, side = warp >> 2;               // its lanes; which of every two pieces
+        uint8_t *const dst = out_s + warp * C::kOutBytes;
         const uint32_t d = smem_u32(dst);
         const uint32_t acc_empty0 = at_leader(&bar.acc_empty[0]), acc_shared = at_leader(&bar.acc_shared);
         uint32_t acc_it = 0;
@@ -479,12 +497,12 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             if (o.kb == 0 && p.add)
                 continue;
             const int m = o.m0 + 128 * (int)rank + 32 * w;      // first of this warp's 32 rows of the M side
-            const uint32_t b = acc_it & 1;
-            const uint32_t acc = tmem + ((uint32_t)(32 * w) << 16) + b * C::kAcc1;
             const int nch = (o.n + C::kChunk - 1) / C::kChunk;
+            const int parts = C::kParts ? (o.kb + C::kPartBlocks - 1) / C::kPartBlocks : 1;
             // with overlapping accumulators the shared columns come first: the end
-            // of the one, the beginning of the other
-            const bool back = C::kFp4 && b == 0;
+            // of the one, the beginning of the other (not of a sum in
+            // parts: a warp's columns stay the same)
+            const bool back = C::kFp4 && (acc_it & 1) == 0 && parts == 1;
             float ms[4], scale0 = 1.f, scale1 = 1.f;
             if constexpr (C::kFp4 && !C::kWgrad) {
 #pragma unroll
@@ -502,7 +520,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                 return C::kFp4 && !C::kWgrad && cc < nch && i < o.n ? __ldg(p.n_scale + o.row0 + o.n0 + i) : 0.f;
             };
             float ts_next = row_scale(side), ts_lane = 0.f;
-            auto emit = [&](int cc, uint32_t *r) {
+            auto emit = [&](int cc, uint32_t *r, bool add) {
                 if (m >= p.M)
                     return;
                 const int c = back ? nch - 1 - cc : cc;
@@ -557,7 +575,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (elect_one()) {
-                        if (C::kF32 && p.add)
+                        if (C::kF32 && add)
                             tma_store_3d<true>(&p.out, o.n0 + C::kChunk * c, m, o.e, d);
                         else
                             tma_store_3d<false>(&p.out, o.n0 + C::kChunk * c, m, o.e, d);
@@ -571,51 +589,77 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
 #pragma unroll
                     for (int i = 0; i < C::kChunk; ++i)
                         r[i] = 0u;
-                    emit(cc, r);
+                    emit(cc, r, false);
                 }
                 continue;
             }
-            if (!__all_sync(0xffffffffu, mbar_wait_for(&bar.acc_full[b], (acc_it >> 1) & 1,
-                                                       kWaitNs + 4096ull * (uint64_t)o.kb))) {
-                ok = false;
-                break;
-            }
-            ++acc_it;
-            tmem_fence_after();
-            int cc = side;
-            do {
-                if (cc < nch) {
-                    const uint32_t at0 = acc + C::kChunk * (back ? nch - 1 - cc : cc);
-                    if constexpr (!C::kWgrad) {
-                        tmem_ld_16x32(at0, r);
-                        tmem_ld_16x32(at0 + (16u << 16), r + 16);
-                    } else {
-                        tmem_ld_32x32(at0, r);
+            float keep[C::kKeep ? 4 : 1][32];
+            for (int part = 0; part < parts; ++part) {
+                if (C::kParts && !C::kKeep && part > 0 && elect_one())
+                    tma_store_wait0();             // what is added to has been written
+                const uint32_t b = acc_it & 1;
+                const uint32_t acc = tmem + ((uint32_t)(32 * w) << 16) + b * C::kAcc1;
+                if (!__all_sync(0xffffffffu, mbar_wait_for(&bar.acc_full[b], (acc_it >> 1) & 1,
+                                                           kWaitNs + 4096ull * (uint64_t)o.kb))) {
+                    ok = false;
+                    break;
+                }
+                ++acc_it;
+                tmem_fence_after();
+                const bool shared_first = C::kFp4 && (back || b == 1);
+#pragma unroll
+                for (int q = 0; q < kTileN / 2 / C::kChunk; ++q) {
+                    const int cc = side + 2 * q;
+                    if (q > 0 && cc >= nch)
+                        break;
+                    if (cc < nch) {
+                        const uint32_t at0 = acc + C::kChunk * (back ? nch - 1 - cc : cc);
+                        if constexpr (!C::kWgrad) {
+                            tmem_ld_16x32(at0, r);
+                            tmem_ld_16x32(at0 + (16u << 16), r + 16);
+                        } else {
+                            tmem_ld_32x32(at0, r);
+                            if constexpr (C::kChunk == 64)
+                                tmem_ld_32x32(at0 + 32, r + 32);
+                        }
+                        ts_lane = ts_next;
+                        ts_next = row_scale(cc + 2);
+                        tmem_wait_ld(r);
                         if constexpr (C::kChunk == 64)
-                            tmem_ld_32x32(at0 + 32, r + 32);
+                            tmem_wait_ld(r + 32);
                     }
-                    ts_lane = ts_next;
-                    ts_next = row_scale(cc + 2);
-                    tmem_wait_ld(r);
-                    if constexpr (C::kChunk == 64)
-                        tmem_wait_ld(r + 32);
-                }
-                // what the next products wait for
-                const bool first = C::kFp4 && cc == side, last = cc + 2 >= nch;
-                if (first || last) {
-                    tmem_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (first)
-                            mbar_arrive_at(acc_shared);
-                        if (last)
-                            mbar_arrive_at(acc_empty0 + 8 * b);
+                    // what the next products wait for
+                    const bool last = cc + 2 >= nch, shared = C::kFp4 && (shared_first ? q == 0 : last);
+                    if (shared || last) {
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (shared)
+                                mbar_arrive_at(acc_shared);
+                            if (last)
+                                mbar_arrive_at(acc_empty0 + 8 * b);
+                        }
                     }
+                    if (cc >= nch)
+                        break;
+                    if constexpr (C::kKeep) {
+                        if (part > 0) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                r[i] = f2u(u2f(r[i]) + keep[q][i]);
+                        }
+                        if (part < parts - 1) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                keep[q][i] = u2f(r[i]);
+                            continue;
+                        }
+                    }
+                    emit(cc, r, p.add || (!C::kKeep && part > 0));
                 }
-                if (cc < nch)
-                    emit(cc, r);
-                cc += 2;
-            } while (cc < nch);
+            }
+            if (!ok)
+                break;
         }
         if (elect_one())
             tma_store_wait0();
@@ -628,7 +672,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
     __syncthreads();
     if constexpr (kCtas == 2)
         cluster_sync();
-    if (warp == 2)
+    if (warp == kWarpCut)
         tmem_dealloc<kCtas>(tmem, 512);
 }
 
