@@ -81,7 +81,7 @@ class Nvfp4Layer:
 
     def __init__(self, w1, w2):
         self.E, self.I = w2.shape[0], w2.shape[2]
-        operand = lambda w: nq.ep_nvfp4_operand(nq.ep_nvfp4_pack_weights(w), w.shape[2])   # noqa: E731
+        operand = lambda w: nq.ep_nvfp4_operand(nq.ep_nvfp4_pack_weights(w), w.shape[2], copy_codes=True)   # noqa: E731
         self.w1, self.w2 = operand(w1), operand(w2)
         self.w1_t, self.w2_t = (operand(w.transpose(1, 2).contiguous()) for w in (w1, w2))
 

@@ -625,9 +625,9 @@ size_t ep_nvfp4_scale_bytes(int64_t rows, int64_t H);
 /*
  * ep_nvfp4_operand -- packed rows as an operand of ep_nvfp4_grouped_gemm
  * without the columnwise half of a direct receive: the block scales in 128 x 4
- * tiles and the row scales; the codes are read from the rows themselves (codes
- * pointer = rows, pitch = ep_nvfp4_row_bytes(H)).  For weights, and for rows
- * whose weight gradient is not wanted.
+ * tiles and the row scales; the codes can be read from the rows themselves
+ * (codes pointer = rows, pitch = ep_nvfp4_row_bytes(H)).  For weights, and for
+ * rows whose weight gradient is not wanted.
  *   rows            device u8 [groups * rows_per_group, S] (ep_nvfp4_pack
  *                   layout).
  *   groups          1 for rows; E for weights [E, N, S], each expert's rows
@@ -639,12 +639,20 @@ size_t ep_nvfp4_scale_bytes(int64_t rows, int64_t H);
  *                   ep_nvfp4_direct_receive_swizzled; what overhangs in a
  *                   tile, along the rows or along H, is zero.
  *   row_scale       device f32 [groups * rows_per_group].
+ *   codes           device u8 [groups * rows_per_group, H/2] or NULL.  With it
+ *                   the codes are copied there, row after row.  Packed rows
+ *                   start anywhere on 16 bytes, which costs the products' copies
+ *                   a fifth of their rate: large batches gain from rows of their
+ *                   own (98304 rows, 64 experts of 4096 x 4096 on GB300: 630 us
+ *                   from packed rows and weights, 525 from copies; 128 tokens 8
+ *                   of 64 experts 121 and 112).
  */
 ep_status ep_nvfp4_operand(const uint8_t *rows, int64_t groups,
                            int64_t rows_per_group, int64_t H,
                            const int32_t *expert_offsets, int E,
                            uint8_t *scales, float *row_scale,
-                           uint32_t *dev_status, void *stream);
+                           uint8_t *codes, uint32_t *dev_status,
+                           void *stream);
 
 /*
  * ep_nvfp4_grouped_gemm -- the expert products of NVFP4 rows with NVFP4

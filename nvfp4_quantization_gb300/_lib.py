@@ -100,7 +100,7 @@ def _declare(L):
     L.ep_grouped_wgrad.argtypes = [_P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _I32, _P, _I32, _I32, _P, _P]
     L.ep_grouped_wgrad.restype = _I32
     L.ep_nvfp4_scale_bytes.argtypes = [_I64, _I64]; L.ep_nvfp4_scale_bytes.restype = ctypes.c_size_t
-    L.ep_nvfp4_operand.argtypes = [_P, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _P]
+    L.ep_nvfp4_operand.argtypes = [_P, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _P, _P]
     L.ep_nvfp4_operand.restype = _I32
     L.ep_nvfp4_grouped_gemm.argtypes = [_P, _I64, _P, _P, _I64, _I64, _P, _I64, _P, _P, _I32, _I64, _P, _P, _P, _P]
     L.ep_nvfp4_grouped_gemm.restype = _I32

@@ -704,9 +704,13 @@ def nvfp4_scale_bytes(rows: int, H: int) -> int:
 
 def ep_nvfp4_operand(rows: torch.Tensor, H: int, offsets: torch.Tensor | None = None, E: int = 1,
                      scales: torch.Tensor | None = None, row_scale: torch.Tensor | None = None,
-                     status: torch.Tensor | None = None, stream=None) -> dict:
-    """Packed NVFP4 rows as an operand of ep_nvfp4_grouped_gemm: keys rw_codes (a
-    view of the rows), rw_scales (tiled) and rw_row_scale.
+                     status: torch.Tensor | None = None, stream=None, copy_codes: bool = False,
+                     codes: torch.Tensor | None = None) -> dict:
+    """Packed NVFP4 rows as an operand of ep_nvfp4_grouped_gemm: keys rw_codes,
+    rw_scales (tiled) and rw_row_scale.
+
+    rw_codes is a view of the rows; with ``copy_codes`` (or ``codes``, uint8 [...,
+    H/2]) a copy, from which large products run up to a fifth faster.
 
     ``rows`` uint8 [R_cap, row_bytes(H)], of which [0, offsets[E]) are taken
     (all without ``offsets``), or weights [E, N, row_bytes(H)] as
@@ -734,12 +738,17 @@ def ep_nvfp4_operand(rows: torch.Tensor, H: int, offsets: torch.Tensor | None = 
         row_scale = _empty(shape[:-1], torch.float32, dev, stream)
     else:
         _need_dense(row_scale, "row_scale", shape[:-1], torch.float32)
+    if codes is not None:
+        _need_dense(codes, "codes", shape[:-1] + (H // 2,), torch.uint8)
+    elif copy_codes:
+        codes = _empty(shape[:-1] + (H // 2,), torch.uint8, dev, stream)
     status = _status_or_new(status, dev, stream)
     st = _lib.lib().ep_nvfp4_operand(rows.data_ptr(), groups, n, H, _at(offsets), E, scales.data_ptr(),
-                                     row_scale.data_ptr(), status.data_ptr(), _stream_of(stream, dev))
+                                     row_scale.data_ptr(), _at(codes), status.data_ptr(), _stream_of(stream, dev))
     if st:
         check("ep_nvfp4_operand", st)
-    codes = rows.as_strided((n, H // 2), (S, 1)) if groups == 1 and len(shape) == 2 else rows[..., : H // 2]
+    if codes is None:
+        codes = rows.as_strided((n, H // 2), (S, 1)) if len(shape) == 2 else rows[..., : H // 2]
     return {"rw_codes": codes, "rw_scales": scales, "rw_row_scale": row_scale}
 
 

@@ -699,7 +699,7 @@ size_t ep_nvfp4_scale_bytes(int64_t rows, int64_t H)
 }
 
 ep_status ep_nvfp4_operand(const uint8_t *rows, int64_t groups, int64_t rows_per_group, int64_t H,
-                           const int32_t *expert_offsets, int E, uint8_t *scales, float *row_scale,
+                           const int32_t *expert_offsets, int E, uint8_t *scales, float *row_scale, uint8_t *codes,
                            uint32_t *dev_status, void *stream)
 {
     const bool any = groups > 0 && rows_per_group > 0;
@@ -711,11 +711,11 @@ ep_status ep_nvfp4_operand(const uint8_t *rows, int64_t groups, int64_t rows_per
         (groups > 0 && rows_per_group > (int64_t)INT32_MAX / groups) ||
         groups * ((rows_per_group + 127) / 128) > (int64_t)INT32_MAX)
         return EP_ERR_CAPACITY;
-    if (!aligned16(rows) || !aligned16(scales) || !aligned_to(row_scale, 4))
+    if (!aligned16(rows) || !aligned16(scales) || !aligned_to(row_scale, 4) || !aligned16(codes))
         return EP_ERR_ALIGN;
     const int dev = device_of(any ? (const void *)rows : (const void *)dev_status);
     if (dev < 0 || !on_device(expert_offsets, dev) || !on_device(scales, dev) || !on_device(row_scale, dev) ||
-        !on_device(dev_status, dev))
+        !on_device(codes, dev) || !on_device(dev_status, dev))
         return EP_ERR_DEVICE;
     DeviceGuard g(dev);
     if (!g.ok)
@@ -731,6 +731,7 @@ ep_status ep_nvfp4_operand(const uint8_t *rows, int64_t groups, int64_t rows_per
     a.K = (int)H;
     a.scales = scales;
     a.row_scale = row_scale;
+    a.codes = codes;
     a.status = dev_status;
     return cuda_status(epq::launch_operand(c, a));
 }

@@ -233,6 +233,7 @@ struct OperandArgs {
     int E, K;
     uint8_t *scales;         // [groups][ceil(per_group / 128)][ceil(K / 64)][512]
     float *row_scale;        // [groups * per_group]
+    uint8_t *codes;          // [groups * per_group, K / 2] or NULL
     uint32_t *status;
 };
 

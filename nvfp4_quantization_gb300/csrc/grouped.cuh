@@ -320,8 +320,10 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
             const uint32_t bytes = C::kABytes + C::kSaBytes + C::kSbBytes + (half + 63) / 64 * 8192;
             if (C::kFp4 && C::kWgrad && o.e != last_e && o.kb > 0) {
                 maps = p.maps + 4 * o.e;
-                if (lane < 4)
-                    tensormap_acquire(maps + lane);
+                // by every thread, that is also by the one that uses the maps: their
+                // place may have held other maps before
+                for (int i = 0; i < 4; ++i)
+                    tensormap_acquire(maps + i);
                 __syncwarp();
                 last_e = o.e;
             }

@@ -57,6 +57,15 @@ __global__ void __launch_bounds__(kOpThreads) operand_kernel(const __grid_consta
     }
     if (blockIdx.y == 0 && tid < 128 && m0 + tid < limit)
         a.row_scale[g * a.per_group + m0 + tid] = *reinterpret_cast<const float *>(rows + tid * a.S + a.S - 16);
+    if (a.codes) {                                // the same tiles' codes: 32 bytes a tile and row
+        const int c0 = 32 * t0, units = (min(a.K / 2, c0 + 32 * nt) - c0) / 16, n = (int)min((int64_t)128, limit - m0);
+        uint8_t *to = a.codes + (g * a.per_group + m0) * (a.K / 2) + c0;
+        for (int i = tid; i < n * units; i += kOpThreads) {
+            const int m = i / units, q = i - m * units;
+            *reinterpret_cast<uint4 *>(to + (int64_t)m * (a.K / 2) + 16 * q) =
+                *reinterpret_cast<const uint4 *>(rows + m * a.S + c0 + 16 * q);
+        }
+    }
     __syncthreads();
     uint8_t *out = a.scales + ((g * mt + m0 / 128) * kt + t0) * 512;
     for (int i = tid; i < 32 * nt; i += kOpThreads) {

@@ -201,7 +201,8 @@ def randn(g, *shape, spread=1.0):
 def test_operand(R, K):
     g = gen(5)
     rows = pack_rows(randn(g, R, K))
-    op = nq.ep_nvfp4_operand(rows, K)
+    op, copied = nq.ep_nvfp4_operand(rows, K), nq.ep_nvfp4_operand(rows, K, copy_codes=True)
+    assert all(torch.equal(copied[name], op[name]) for name in op) and copied["rw_codes"].is_contiguous()
     M, kt = -(-R // 128) * 128, -(-K // 64)
     want = torch.zeros(M, kt * 4, dtype=torch.uint8, device="cuda")
     want[:R, : K // 16] = rows[:, K // 2: 9 * K // 16]
@@ -224,8 +225,13 @@ def test_operand_of_slots_and_of_weights():
     want[:, :10] = rows[: off[-1], K // 2: 9 * K // 16]
     assert torch.equal(untile(op["rw_scales"], off[-1], 12), want)
     assert (scales[off[-1] * 12:] == 0xAB).all() and (row_scale[off[-1]:] == 7.0).all()
+    codes = torch.full((R_cap, K // 2), 0xCD, dtype=torch.uint8, device="cuda")
+    copied = nq.ep_nvfp4_operand(rows, K, offsets, 3, codes=codes)
+    assert copied["rw_codes"] is codes and torch.equal(codes[: off[-1]], rows[: off[-1], : K // 2])
+    assert (codes[off[-1]:] == 0xCD).all()
     w = nq.ep_nvfp4_pack_weights(randn(g, 3, 150, K).to(torch.bfloat16))
     op = nq.ep_nvfp4_operand(w, K)
+    assert torch.equal(nq.ep_nvfp4_operand(w, K, copy_codes=True)["rw_codes"], op["rw_codes"])
     for e in range(3):
         one = nq.ep_nvfp4_operand(w[e], K)
         assert torch.equal(op["rw_scales"].view(3, -1)[e], one["rw_scales"])

@@ -84,6 +84,32 @@ def test_graph_replay_with_other_values_and_offsets():
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
+def test_one_workspace_for_many_calls():
+    """Calls of other sizes and operands in turn with one workspace, nothing between
+    them: each uses its own tensor maps, not those that lay there before."""
+    g = gen(32)
+    ws = torch.empty(512 * 7, dtype=torch.uint8, device="cuda")
+    sets = []
+    for counts, n, k in (([130, 0, 300, 7, 128], 256, 384), ([1500], 128, 128), ([5, 700, 1, 128, 0, 64, 900], 512, 256),
+                         ([128] * 7, 256, 384)):
+        offsets, off, R_cap, live = slots(counts)
+        ops = [tg.columnwise((randn(g, R_cap, h) * live.unsqueeze(1)).to(torch.bfloat16), offsets, len(counts))
+               for h in (n, k)]
+        want = nq.ep_nvfp4_grouped_wgrad(ops[0], ops[1], n, k, offsets, len(counts))
+        for e in range(len(counts)):
+            if off[e + 1] > off[e]:
+                a, b = (tg.columnwise_values(op, h, off, e) for op, h in zip(ops, (n, k)))
+                within(want[e], a @ b.t(), sum_bound(off[e + 1] - off[e], a.abs() @ b.abs().t(), a @ b.t(),
+                                                     torch.float32, more=4))
+        sets.append((ops, n, k, offsets, len(counts), want, torch.empty_like(want), nq.new_status("cuda")))
+    for _ in range(30):
+        for ops, n, k, offsets, E, want, out, status in sets:
+            out.fill_(NAN)
+        for ops, n, k, offsets, E, want, out, status in sets:
+            nq.ep_nvfp4_grouped_wgrad(ops[0], ops[1], n, k, offsets, E, d_w=out, workspace=ws, status=status)
+        assert all(torch.equal(out, want) and int(status) == 0 for *_, want, out, status in sets)
+
+
 def test_slots_that_are_not_whole_tiles():
     g = gen(23)
     offsets, off, R_cap, live = slots([128, 128, 256])

@@ -48,16 +48,17 @@ def test_wgrad_refusals(kw, status):
 
 
 def _operand(**kw):
-    a = dict(rows=FAKE, g=1, n=600, H=64, off=FAKE, E=4, sc=FAKE, rs=FAKE, st=FAKE)
+    a = dict(rows=FAKE, g=1, n=600, H=64, off=FAKE, E=4, sc=FAKE, rs=FAKE, co=None, st=FAKE)
     a.update(kw)
-    return nq.lib().ep_nvfp4_operand(a["rows"], a["g"], a["n"], a["H"], a["off"], a["E"], a["sc"], a["rs"], a["st"], None)
+    return nq.lib().ep_nvfp4_operand(a["rows"], a["g"], a["n"], a["H"], a["off"], a["E"], a["sc"], a["rs"], a["co"],
+                                     a["st"], None)
 
 
 @pytest.mark.parametrize("kw, status", [
     (dict(rows=None), -1), (dict(sc=None), -1), (dict(rs=None), -1), (dict(st=None), -1), (dict(H=48), -2),
     (dict(H=0), -2), (dict(E=0), -2), (dict(E=1025), -2), (dict(off=None), -2), (dict(g=2), -2),
     (dict(n=-1), -4), (dict(n=1 << 31), -4), (dict(g=4, n=1 << 30, off=None, E=1), -4), (dict(rows=HALF), -3),
-    (dict(sc=HALF), -3), (dict(rs=ODD), -3)])
+    (dict(sc=HALF), -3), (dict(rs=ODD), -3), (dict(co=HALF), -3)])
 def test_operand_refusals(kw, status):
     assert _operand(**kw) == status
 
