@@ -682,9 +682,6 @@ ep_status ep_nvfp4_grouped_gemm(const uint8_t *x_codes, int64_t ld_x,
                                 const int32_t *expert_offsets, void *out_bf16,
                                 uint32_t *dev_status, void *stream);
 
-/* Device workspace of ep_nvfp4_grouped_wgrad: 512 bytes an expert. */
-size_t ep_nvfp4_wgrad_workspace_bytes(int E);
-
 /*
  * ep_nvfp4_grouped_wgrad -- the weight gradient from the columnwise operands:
  *   d_w[e][n][k] = sum over e's rows of dy[n][r] * x[k][r] / (Sdy[e] * Sx[e]),
@@ -696,9 +693,6 @@ size_t ep_nvfp4_wgrad_workspace_bytes(int E);
  *                   ep_nvfp4_colwise_rht_bf16_swizzled for H = N;
  *   x_codes, x_scales, x_scale_enc: the same for H = K.
  *                   Without expert_offsets R_cap is a multiple of 128.
- *   workspace       device, 128-byte aligned, ws_bytes >=
- *                   ep_nvfp4_wgrad_workspace_bytes(E); needs no filling.  Calls
- *                   that may overlap need one each.
  *   d_w, dtype, accumulate: as in ep_grouped_wgrad.  An expert whose rows go
  *                   past R_cap counts as empty as a whole.
  * N % 128 == 0, K % 128 == 0.
@@ -711,8 +705,7 @@ ep_status ep_nvfp4_grouped_wgrad(const uint8_t *dy_codes,
                                  const float *x_scale_enc, int64_t R_cap,
                                  int64_t N, int64_t K,
                                  const int32_t *expert_offsets, int E,
-                                 void *workspace, size_t ws_bytes, void *d_w,
-                                 int dtype, int accumulate,
+                                 void *d_w, int dtype, int accumulate,
                                  uint32_t *dev_status, void *stream);
 
 /* Human-readable name of a status code. */

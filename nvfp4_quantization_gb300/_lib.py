@@ -33,8 +33,8 @@ SYMBOLS = ("ep_nvfp4_row_bytes", "ep_rows_capacity", "ep_route_workspace_bytes",
            "ep_nvfp4_direct_receive_swizzled", "ep_nvfp4_colwise_rht_bf16", "ep_mxfp8_pack",
            "ep_mxfp8_colwise", "ep_pack", "ep_combine", "ep_combine_backward", "ep_swiglu", "ep_swiglu_backward",
            "ep_nvfp4_matvec", "ep_nvfp4_colwise_rht_bf16_swizzled", "ep_grouped_gemm", "ep_grouped_wgrad",
-           "ep_nvfp4_scale_bytes", "ep_nvfp4_operand", "ep_nvfp4_grouped_gemm", "ep_nvfp4_wgrad_workspace_bytes",
-           "ep_nvfp4_grouped_wgrad", "ep_status_string")
+           "ep_nvfp4_scale_bytes", "ep_nvfp4_operand", "ep_nvfp4_grouped_gemm", "ep_nvfp4_grouped_wgrad",
+           "ep_status_string")
 
 
 class EpGrouped(ctypes.Structure):
@@ -104,9 +104,7 @@ def _declare(L):
     L.ep_nvfp4_operand.restype = _I32
     L.ep_nvfp4_grouped_gemm.argtypes = [_P, _I64, _P, _P, _I64, _I64, _P, _I64, _P, _P, _I32, _I64, _P, _P, _P, _P]
     L.ep_nvfp4_grouped_gemm.restype = _I32
-    L.ep_nvfp4_wgrad_workspace_bytes.argtypes = [_I32]; L.ep_nvfp4_wgrad_workspace_bytes.restype = ctypes.c_size_t
-    L.ep_nvfp4_grouped_wgrad.argtypes = [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I32, _P, ctypes.c_size_t, _P,
-                                         _I32, _I32, _P, _P]
+    L.ep_nvfp4_grouped_wgrad.argtypes = [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I32, _P, _I32, _I32, _P, _P]
     L.ep_nvfp4_grouped_wgrad.restype = _I32
     L.ep_status_string.argtypes = [_I32]; L.ep_status_string.restype = ctypes.c_char_p
 

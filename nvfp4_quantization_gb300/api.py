@@ -804,17 +804,15 @@ def ep_nvfp4_grouped_gemm(x: dict, w: dict, offsets: torch.Tensor | None = None,
 
 def ep_nvfp4_grouped_wgrad(dy: dict, x: dict, N: int, K: int, offsets: torch.Tensor | None = None, E: int = 1,
                            d_w: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
-                           accumulate: bool = False, workspace: torch.Tensor | None = None,
-                           status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                           accumulate: bool = False, status: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
     """Gradient of the expert weights, [E, N, K], from the columnwise NVFP4
     operands of dy (N columns) and x (K columns): keys cw_codes, cw_scales in
     tiles, cw_scale_enc, as ep_nvfp4_direct_receive and
     ep_nvfp4_colwise_rht_bf16 make them with ``swizzled=True`` and one sign
     mask.
 
-    ``d_w``, ``dtype``, ``accumulate`` as in ep_grouped_wgrad.  ``workspace``
-    (uint8, 512 bytes an expert): calls that may overlap need one each; made
-    here without it."""
+    ``d_w``, ``dtype``, ``accumulate`` as in ep_grouped_wgrad."""
     codes = dy["cw_codes"]
     if not codes.is_cuda:
         raise ValueError('dy["cw_codes"] must be a CUDA tensor')
@@ -827,16 +825,12 @@ def ep_nvfp4_grouped_wgrad(dy: dict, x: dict, N: int, K: int, offsets: torch.Ten
         _need_f32(op["cw_scale_enc"], f'{name}["cw_scale_enc"]', E)
     _need_offsets(offsets, E)
     d_w = _weight_gradient(d_w, (E, N, K), dtype, accumulate, dev, stream)
-    if workspace is None:
-        workspace = _empty((512 * E,), torch.uint8, dev, stream)
-    else:
-        _need_bytes(workspace, "workspace", 512 * E)
     status = _status_or_new(status, dev, stream)
     st = _lib.lib().ep_nvfp4_grouped_wgrad(codes.data_ptr(), dy["cw_scales"].data_ptr(), dy["cw_scale_enc"].data_ptr(),
                                            x["cw_codes"].data_ptr(), x["cw_scales"].data_ptr(),
-                                           x["cw_scale_enc"].data_ptr(), R_cap, N, K, _at(offsets), E,
-                                           workspace.data_ptr(), workspace.numel(), d_w.data_ptr(), _DTYPE[d_w.dtype],
-                                           int(accumulate), status.data_ptr(), _stream_of(stream, dev))
+                                           x["cw_scale_enc"].data_ptr(), R_cap, N, K, _at(offsets), E, d_w.data_ptr(),
+                                           _DTYPE[d_w.dtype], int(accumulate), status.data_ptr(),
+                                           _stream_of(stream, dev))
     if st:
         check("ep_nvfp4_grouped_wgrad", st)
     return d_w

@@ -781,15 +781,12 @@ ep_status ep_nvfp4_grouped_gemm(const uint8_t *x_codes, int64_t ld_x, const uint
     return cuda_status(R_cap > 0 ? epq::launch_nvfp4_gemm(c, a) : cudaSuccess);
 }
 
-size_t ep_nvfp4_wgrad_workspace_bytes(int E) { return (size_t)epq::nvfp4_wgrad_workspace(E < 1 ? 1 : E); }
-
 ep_status ep_nvfp4_grouped_wgrad(const uint8_t *dy_codes, const uint8_t *dy_scales, const float *dy_scale_enc,
                                  const uint8_t *x_codes, const uint8_t *x_scales, const float *x_scale_enc,
                                  int64_t R_cap, int64_t N, int64_t K, const int32_t *expert_offsets, int E,
-                                 void *workspace, size_t ws_bytes, void *d_w, int dtype, int accumulate,
-                                 uint32_t *dev_status, void *stream)
+                                 void *d_w, int dtype, int accumulate, uint32_t *dev_status, void *stream)
 {
-    if (!dy_scale_enc || !x_scale_enc || !workspace ||
+    if (!dy_scale_enc || !x_scale_enc ||
         (R_cap > 0 && (!dy_codes || !dy_scales || !x_codes || !x_scales)))
         return EP_ERR_NULL;
     const ep_status st = wgrad_checks(R_cap, N, K, E, 128, expert_offsets, d_w, dtype, accumulate, dev_status);
@@ -797,15 +794,13 @@ ep_status ep_nvfp4_grouped_wgrad(const uint8_t *dy_codes, const uint8_t *dy_scal
         return st;
     if (!expert_offsets && R_cap % 128 != 0)
         return EP_ERR_SHAPE;
-    if (ws_bytes < (size_t)epq::nvfp4_wgrad_workspace(E))
-        return EP_ERR_CAPACITY;
     if (!aligned16(dy_codes) || !aligned16(dy_scales) || !aligned_to(dy_scale_enc, 4) || !aligned16(x_codes) ||
-        !aligned16(x_scales) || !aligned_to(x_scale_enc, 4) || !aligned_to(workspace, 128))
+        !aligned16(x_scales) || !aligned_to(x_scale_enc, 4))
         return EP_ERR_ALIGN;
     const int dev = device_of(d_w);
     if (dev < 0 || !on_device(dy_codes, dev) || !on_device(dy_scales, dev) || !on_device(dy_scale_enc, dev) ||
         !on_device(x_codes, dev) || !on_device(x_scales, dev) || !on_device(x_scale_enc, dev) ||
-        !on_device(expert_offsets, dev) || !on_device(workspace, dev) || !on_device(dev_status, dev))
+        !on_device(expert_offsets, dev) || !on_device(dev_status, dev))
         return EP_ERR_DEVICE;
     DeviceGuard g(dev);
     if (!g.ok)
@@ -819,7 +814,6 @@ ep_status ep_nvfp4_grouped_wgrad(const uint8_t *dy_codes, const uint8_t *dy_scal
     a.x_scales = x_scales;
     a.x_enc = x_scale_enc;
     a.offsets = expert_offsets;
-    a.workspace = workspace;
     a.d_w = d_w;
     a.R_cap = (int)R_cap;
     a.E = E;

@@ -258,14 +258,12 @@ struct Nvfp4WgradArgs {
     const uint8_t *dy, *dy_scales, *x, *x_scales;   // columnwise operands, tiled scales
     const float *dy_enc, *x_enc;                    // [E]
     const int32_t *offsets;                         // or NULL
-    void *workspace;                                // nvfp4_wgrad_workspace(E) bytes, 128-byte aligned
     void *d_w;                                      // [E, N, K]
     int R_cap, E, N, K;
     bool f32, add;
     uint32_t *status;
 };
 
-inline int64_t nvfp4_wgrad_workspace(int E) { return (int64_t)E * 4 * sizeof(CUtensorMap); }
 cudaError_t launch_nvfp4_wgrad(const LaunchCtx &c, const Nvfp4WgradArgs &a);
 
 // Bytes of a packed NVFP4 row: roundup16(9H/16 + 16).

@@ -13,6 +13,11 @@
 // feeds a ring of shared-memory stages by TMA (128 bytes along K a row and
 // stage: 64 BF16 or 256 E2M1), one thread of warp 9 issues the matrix products
 // into tensor memory, warp 10 cuts ragged blocks.
+//
+// The columnwise NVFP4 operands are a matrix of its own for every expert, whose
+// pitch only the device knows, so no tensor map of the host's fits them.  There
+// warps 12-15 copy the rows in 16-byte pieces, and warp 8 passes the arrival of
+// a stage on to the matrix products.
 #pragma once
 
 #include "epq_internal.h"
@@ -20,19 +25,18 @@
 
 namespace epq {
 
-constexpr int kGThreads = 352;       // 11 warps: up to 184 registers a thread
 constexpr int kTileN = 256;
 constexpr int kGroupTiles = 8;       // tiles of the N side that share the M side's tiles in L2
 constexpr int kOutWarps = 8;         // two to a quarter of the accumulator's lanes
-constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpCut = 10;
+constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpCut = 10, kWarpRows = 12, kRowWarps = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 enum { kMapA = 0, kMapB = 1, kMapSa = 2, kMapSb = 3 };
 
 struct GroupedParams {
-    CUtensorMap map[4];              // A, B, block scales of A and B (NVFP4 weight gradient: in `maps`)
+    CUtensorMap map[4];              // A, B, block scales of A and B
     CUtensorMap out;
-    const CUtensorMap *maps;         // NVFP4 weight gradient: [E][4], written by the kernel before
+    const uint8_t *col[4];           // NVFP4 weight gradient: the same, as the columnwise operands
     const int32_t *offsets;          // [E + 1], or NULL: one expert with all R_cap rows
     const int32_t *counts;           // BF16 weight gradient: [E] or NULL
     const float *m_scale;            // NVFP4: rows as N: [E * M] of the weights' rows; rows as K: [E] of dy
@@ -47,6 +51,8 @@ template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_> struct G
     static constexpr bool kFp4 = kFp4_, kWgrad = kWgrad_, kF32 = kF32_;
     static constexpr int kCtas = kCtas_;
     static constexpr bool kAmn = kAmn_;                       // A with its M side contiguous (BF16)
+    static constexpr bool kRows = kFp4 && kWgrad;             // copied in pieces, not by TMA
+    static constexpr int kThreads = kRows ? 32 * (kWarpRows + kRowWarps) : 352;
     static constexpr bool kBmn = kWgrad && !kFp4;
     static constexpr int kBlockK = kFp4 ? 256 : 64;           // elements of K a stage
     static constexpr int kStepK = kFp4 ? 64 : 16;             // elements of K a matrix instruction
@@ -77,7 +83,7 @@ template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_> struct G
 };
 
 struct __align__(8) GroupedBars {      // up to 8 stages
-    uint64_t full[8], empty[8], tail[8];
+    uint64_t full[8], empty[8], tail[8];        // tail: what landed here, before it is passed on
     uint64_t acc_full[2], acc_empty[2], acc_shared;
     uint32_t tmem, pad;
 };
@@ -102,15 +108,15 @@ __device__ __forceinline__ int expert_rows(const GroupedParams &p, int e, int &o
         off = 0;
         return p.R_cap;
     }
-    off = __ldg(p.offsets + e);
-    const int end = __ldg(p.offsets + e + 1);
+    off = ld_word(p.offsets + e);
+    const int end = ld_word(p.offsets + e + 1);
     if (off < 0 || end < off || ((off | end) & 127)) {
         err |= kDevErrBadExpert;
         return 0;
     }
     if (end > p.R_cap) {
         err |= kDevErrCapacity;      // the columnwise layout of a cut slot is not known: none of it
-        return C::kFp4 && C::kWgrad ? 0 : max(0, p.R_cap - off);
+        return C::kRows ? 0 : max(0, p.R_cap - off);
     }
     return end - off;
 }
@@ -154,7 +160,7 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams &p, cons
     if (C::kWgrad) {
         o.rows = rows;
         if (p.counts)
-            o.rows = max(0, min(rows, __ldg(p.counts + o.e)));
+            o.rows = max(0, min(rows, ld_word(p.counts + o.e)));
         o.n = min(kTileN, p.N - o.n0);
         o.kb = (o.rows + C::kBlockK - 1) / C::kBlockK;
     } else {
@@ -233,7 +239,7 @@ __device__ __forceinline__ void grouped_plan(const GroupedParams &p, int *start,
             start[(e0 + i) >> 1] = at;
         at += n[i];
     }
-    if (tid == kGThreads - 1)
+    if (tid == C::kThreads - 1)
         start[(p.E + 1) >> 1] = at;               // the last thread has no expert
     if (err && blockIdx.x == 0)
         raise_status(p.status, err);
@@ -262,7 +268,7 @@ template <int kStages> struct GroupedRing {
 };
 
 template <class C>
-__global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_constant__ GroupedParams p)
+__global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_constant__ GroupedParams p)
 {
     constexpr int kCtas = C::kCtas, kStages = C::kStages;
     extern __shared__ __align__(1024) uint8_t g_smem[];          // stages, pieces of output, barriers, plan
@@ -270,8 +276,8 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
     const uint32_t ring = smem_u32(base);
     uint8_t *const out_s = base + kStages * C::kStageBytes;
     GroupedBars &bar = *reinterpret_cast<GroupedBars *>(out_s + C::kOutAll);
-    int *const partial = reinterpret_cast<int *>(&bar + 1);      // [kGThreads / 32]
-    int *const start = partial + kGThreads / 32;                 // [(E + 1) / 2 + 1]
+    int *const partial = reinterpret_cast<int *>(&bar + 1);      // [C::kThreads / 32]
+    int *const start = partial + C::kThreads / 32;               // [(E + 1) / 2 + 1]
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bar.full[s], kCtas);
             mbar_init(&bar.empty[s], 1);
-            mbar_init(&bar.tail[s], 1);
+            mbar_init(&bar.tail[s], C::kRows ? 32 * kRowWarps : 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bar.acc_full[b], 1);
@@ -308,25 +314,85 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
     bool ok = true;
     GroupedWalk<C> walk(p, start, unit, units);
 
-    if (warp == kWarpCopy) {
+    if (C::kRows && warp == kWarpCopy) {
+        // ------------------------------------------------------------ arrivals
+        // what the other threads copied, ordered before the matrix unit's reads
+        GroupedRing<kStages> at;
+        for (int t = unit; t < tiles && ok; t += units) {
+            const GroupedTile o = walk.tile();
+            for (int kb = 0; kb < o.kb; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait_for(&bar.tail[at.s], at.phase, kWaitNs));
+                if (!ok)
+                    break;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_release_at(full0 + 8 * at.s);
+                at.step();
+            }
+        }
+    } else if (C::kRows && warp >= kWarpRows) {
+        // ------------------------------------------------------------ rows
+        const int id = tid - 32 * kWarpRows, c = id & 7, r0 = id >> 3;   // piece of a row; first of every 16 rows
+        GroupedRing<kStages> at;
+        uint32_t used = 0;
+        for (int t = unit; t < tiles && ok; t += units) {
+            const GroupedTile o = walk.tile();
+            const int half = ((o.n + 63) / 64 * 64) / kCtas, m = o.m0 + 128 * (int)rank, n = o.n0 + half * (int)rank;
+            const int64_t pitch = o.rows / 2, blocks = (int64_t)o.rows * 8;    // bytes of a row, of 128 rows' scales
+            const uint8_t *ca = p.col[kMapA] + (int64_t)o.row0 * p.M / 2 + (m + r0) * pitch + 16 * c;
+            const uint8_t *cb = p.col[kMapB] + (int64_t)o.row0 * p.N / 2 + (n + r0) * pitch + 16 * c;
+            const uint8_t *sa = p.col[kMapSa] + (int64_t)o.row0 * p.M / 16 + m / 128 * blocks + 16 * id;
+            const uint8_t *sb = p.col[kMapSb] + (int64_t)o.row0 * p.N / 16 + o.n0 / 128 * blocks + 16 * id;
+            const uint32_t to = 128 * r0 + ((c ^ (r0 & 7)) << 4);       // 128-byte swizzle
+            for (int kb = 0; kb < o.kb; ++kb) {
+                if (used >= kStages &&
+                    !__all_sync(0xffffffffu, mbar_wait_for(&bar.empty[at.s], at.phase ^ 1, kWaitNs))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t a = ring + at.s * C::kStageBytes, b = a + C::kABytes;
+                const bool in = 128 * kb + 16 * c < pitch;
+                // rows are whole blocks of 128 on both sides; what is not there is not read
+                const bool in_a = in && m < p.M;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    copy16(a + 2048 * i + to, in_a ? ca + 16 * i * pitch + 128 * kb : p.col[kMapA], in_a);
+#pragma unroll
+                for (int i = 0; i < kTileN / kCtas / 16; ++i) {
+                    if (16 * i < half) {                     // whole rounds: half is a multiple of 64
+                        const bool in_b = in && n + 16 * i + r0 < p.N;
+                        copy16(b + 2048 * i + to, in_b ? cb + 16 * i * pitch + 128 * kb : p.col[kMapB], in_b);
+                    }
+                }
+                const uint32_t s0 = b + C::kBBytes + 16 * id;
+                const bool in_s = 2048 * kb + 16 * id < blocks;
+                copy16(s0, in_s && m < p.M ? sa + 2048 * kb : p.col[kMapSa], in_s && m < p.M);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool in_b = in_s && o.n0 + 128 * i < p.N;
+                    copy16(s0 + C::kSaBytes + 2048 * i, in_b ? sb + i * blocks + 2048 * kb : p.col[kMapSb], in_b);
+                }
+                copy16_arrive(smem_u32(&bar.tail[at.s]));
+                at.step();
+                ++used;
+            }
+        }
+        copy16_wait_all();
+        // leave only when every stage has been read
+        for (uint32_t i = min(used, (uint32_t)kStages); i > 0 && ok; --i) {
+            const GroupedRing<kStages> back = at.before(i);
+            ok = mbar_wait_for(&bar.empty[back.s], back.phase, kWaitNs);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+    } else if (!C::kRows && warp == kWarpCopy) {
         // ------------------------------------------------------------ copies
         GroupedRing<kStages> at;
         uint32_t used = 0, cut_it = 0;
-        int last_e = -1;
-        const CUtensorMap *maps = p.map;
         for (int t = unit; t < tiles && ok; t += units) {
             const GroupedTile o = walk.tile();
             const int half = ((o.n + 63) / 64 * 64) / kCtas;              // of the N side: this CTA's
             const uint32_t bytes = C::kABytes + C::kSaBytes + C::kSbBytes + (half + 63) / 64 * 8192;
-            if (C::kFp4 && C::kWgrad && o.e != last_e && o.kb > 0) {
-                maps = p.maps + 4 * o.e;
-                // by every thread, that is also by the one that uses the maps: their
-                // place may have held other maps before
-                for (int i = 0; i < 4; ++i)
-                    tensormap_acquire(maps + i);
-                __syncwarp();
-                last_e = o.e;
-            }
             const bool has_cut = C::kBmn && p.counts && o.rows % C::kBlockK;
             const int m = o.m0 + 128 * (int)rank, n = o.n0 + half * (int)rank;
             for (int kb = 0; kb < o.kb; ++kb) {
@@ -346,27 +412,25 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                     if constexpr (C::kFp4) {
                         const int x = k0 / 2, ys = k0 / 16;               // bytes; pieces of 128 bytes of scales
                         const uint32_t sa = b + C::kBBytes, sb = sa + C::kSaBytes;
-                        const int z = C::kWgrad ? 0 : o.e, zs = z * ((p.M + 127) / 128);
-                        const int nrow = C::kWgrad ? n : o.row0 + n;
-                        tma_load_3d<kCtas>(a, maps + kMapA, x, m, z, f);
+                        tma_load_3d<kCtas>(a, p.map + kMapA, x, m, o.e, f);
                         for (int i = 0; i < half; i += 64)
-                            tma_load_3d<kCtas>(b + i * 128, maps + kMapB, x, nrow + i, 0, f);
-                        tma_load_3d<kCtas>(sa, maps + kMapSa, 0, ys, zs + m / 128, f);
-                        tma_load_3d<kCtas>(sb, maps + kMapSb, 0, ys, (C::kWgrad ? o.n0 : o.row0 + o.n0) / 128, f);
+                            tma_load_3d<kCtas>(b + i * 128, p.map + kMapB, x, o.row0 + n + i, 0, f);
+                        tma_load_3d<kCtas>(sa, p.map + kMapSa, 0, ys, o.e * ((p.M + 127) / 128) + m / 128, f);
+                        tma_load_3d<kCtas>(sb, p.map + kMapSb, 0, ys, (o.row0 + o.n0) / 128, f);
                     } else if constexpr (C::kWgrad) {
                         for (int i = 0; i < 128; i += 64)
-                            tma_load_3d<kCtas>(a + i * 128, maps + kMapA, m + i, o.row0 + k0, 0, f);
+                            tma_load_3d<kCtas>(a + i * 128, p.map + kMapA, m + i, o.row0 + k0, 0, f);
                         for (int i = 0; i < half; i += 64)
-                            tma_load_3d<kCtas>(b + i * 128, maps + kMapB, n + i, o.row0 + k0, 0, f);
+                            tma_load_3d<kCtas>(b + i * 128, p.map + kMapB, n + i, o.row0 + k0, 0, f);
                     } else {
                         if constexpr (C::kAmn) {
                             for (int i = 0; i < 128; i += 64)
-                                tma_load_3d<kCtas>(a + i * 128, maps + kMapA, m + i, k0, o.e, f);
+                                tma_load_3d<kCtas>(a + i * 128, p.map + kMapA, m + i, k0, o.e, f);
                         } else {
-                            tma_load_3d<kCtas>(a, maps + kMapA, k0, m, o.e, f);
+                            tma_load_3d<kCtas>(a, p.map + kMapA, k0, m, o.e, f);
                         }
                         for (int i = 0; i < half; i += 64)
-                            tma_load_3d<kCtas>(b + i * 128, maps + kMapB, k0, o.row0 + n + i, 0, f);
+                            tma_load_3d<kCtas>(b + i * 128, p.map + kMapB, k0, o.row0 + n + i, 0, f);
                     }
                 }
                 __syncwarp();
@@ -419,7 +483,7 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
                         ++acc_it;
                         tmem_fence_after();
                     }
-                    const bool cut = C::kBmn && p.counts && kb == o.kb - 1;
+                    const bool cut = C::kRows || (C::kBmn && p.counts && kb == o.kb - 1);
                     ok = cut ? mbar_wait_for<true>(&bar.full[at.s], at.phase, kWaitNs)
                              : mbar_wait_for(&bar.full[at.s], at.phase, kWaitNs);
                     if (!ok)
@@ -510,16 +574,16 @@ __global__ void __launch_bounds__(kGThreads, 1) grouped_kernel(const __grid_cons
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     const int f = m + 8 * h + lane / 4;
-                    ms[h] = f < p.M ? __ldg(p.m_scale + (int64_t)o.e * p.M + f) : 0.f;
+                    ms[h] = f < p.M ? ld_word(p.m_scale + (int64_t)o.e * p.M + f) : 0.f;
                 }
             } else if constexpr (C::kFp4) {
-                scale0 = __fdiv_rn(1.f, __ldg(p.m_scale + o.e));
-                scale1 = __fdiv_rn(1.f, __ldg(p.n_scale + o.e));
+                scale0 = __fdiv_rn(1.f, ld_word(p.m_scale + o.e));
+                scale1 = __fdiv_rn(1.f, ld_word(p.n_scale + o.e));
             }
             // the row scale of token `lane` of a piece
             auto row_scale = [&](int cc) {
                 const int i = 32 * (back ? nch - 1 - cc : cc) + lane;
-                return C::kFp4 && !C::kWgrad && cc < nch && i < o.n ? __ldg(p.n_scale + o.row0 + o.n0 + i) : 0.f;
+                return C::kFp4 && !C::kWgrad && cc < nch && i < o.n ? ld_word(p.n_scale + o.row0 + o.n0 + i) : 0.f;
             };
             float ts_next = row_scale(side), ts_lane = 0.f;
             auto emit = [&](int cc, uint32_t *r, bool add) {
@@ -700,7 +764,7 @@ template <class C> cudaError_t grouped_units(const LaunchCtx &c, int &units)
     attr[0].val.clusterDim.x = C::kCtas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(c.num_sms / C::kCtas * C::kCtas));
-    cfg.blockDim = dim3(kGThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -746,7 +810,7 @@ template <class C> cudaError_t launch_grouped(const LaunchCtx &c, const GroupedP
     attr[1].val.clusterDim.x = C::kCtas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(units * C::kCtas));
-    cfg.blockDim = dim3(kGThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = grouped_smem_bytes<C>();
     cfg.stream = c.stream;
     cfg.attrs = attr;

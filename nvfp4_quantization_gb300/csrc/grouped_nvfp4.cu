@@ -1,6 +1,5 @@
 // NVFP4 matrix products grouped by expert (the kernel is in grouped.cuh), and
-// what prepares their operands: the tiled scales of packed rows, the tensor
-// maps of the columnwise operands.
+// what prepares their operands: the tiled scales of packed rows.
 #include "grouped.cuh"
 
 namespace epq {
@@ -27,7 +26,7 @@ __global__ void __launch_bounds__(kOpThreads) operand_kernel(const __grid_consta
     pdl_wait();
     int64_t limit = a.per_group;                  // rows of a group
     if (a.offsets) {
-        const int R = __ldg(a.offsets + a.E);
+        const int R = ld_word(a.offsets + a.E);
         if (R > limit && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0)
             raise_status(a.status, kDevErrCapacity);
         limit = R < limit ? R : limit;
@@ -78,59 +77,7 @@ __global__ void __launch_bounds__(kOpThreads) operand_kernel(const __grid_consta
     }
 }
 
-// ---------------------------------------------------------------- maps
-// The columnwise operand of an expert is a matrix of its own, whose pitch (n_e)
-// only the device knows: a warp an expert and map sets base, sizes and pitch in
-// a copy of the call's map.
-struct MapArgs {
-    CUtensorMap like[4];                          // A, B, scales of A, scales of B
-    const uint8_t *base[4];
-    int H[4];                                     // columns (rows of the matrix)
-};
-
-template <int kDim> __device__ __forceinline__ void map_set_dim(uint32_t m, uint32_t v)
-{
-    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], %1, %2;" ::"r"(m), "n"(kDim), "r"(v)
-                 : "memory");
-}
-
-template <int kDim> __device__ __forceinline__ void map_set_pitch(uint32_t m, uint64_t v)
-{
-    asm volatile("tensormap.replace.tile.global_stride.shared::cta.b1024.b64 [%0], %1, %2;" ::"r"(m), "n"(kDim), "l"(v)
-                 : "memory");
-}
-
-__global__ void __launch_bounds__(128) wgrad_maps_kernel(const __grid_constant__ MapArgs a, const int32_t *offsets,
-                                                         int R_cap, CUtensorMap *out)
-{
-    __shared__ __align__(128) CUtensorMap m[4];
-    const int lane = threadIdx.x & 31, i = threadIdx.x >> 5, e = blockIdx.x;
-    pdl_launch_dependents();
-    reinterpret_cast<uint32_t *>(&m[i])[lane] = reinterpret_cast<const uint32_t *>(&a.like[i])[lane];
-    __syncwarp();
-    pdl_wait();
-    const int off = offsets ? __ldg(offsets + e) : 0, end = offsets ? __ldg(offsets + e + 1) : R_cap;
-    if (off < 0 || end <= off || ((off | end) & 127) || end > R_cap)
-        return;                                   // no rows: not used
-    if (lane == 0) {
-        const uint32_t at = smem_u32(&m[i]);
-        const int64_t n = end - off, H = a.H[i];      // dimension 0 of the codes and 1 of the scales, and their pitches
-        const uint64_t base = (uint64_t)(a.base[i] + off * H / (i < 2 ? 2 : 16));
-        asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(at), "l"(base)
-                     : "memory");
-        if (i < 2) {                              // codes: [H][n / 2] bytes
-            map_set_dim<0>(at, (uint32_t)(n / 2));
-            map_set_pitch<0>(at, n / 2);
-        } else {                                  // scales: [H / 128][n / 16][128] bytes
-            map_set_dim<1>(at, (uint32_t)(n / 16));
-            map_set_pitch<1>(at, n * 8);
-        }
-    }
-    __syncwarp();
-    asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned"
-                 " [%0], [%1], 128;" ::"l"((uint64_t)(out + 4 * e + i)), "r"(smem_u32(&m[i])) : "memory");
-}
-
+// ---------------------------------------------------------------- products
 // Codes [outer][inner bytes], copied in boxes of 128 bytes x `rows`.
 bool code_map(CUtensorMap *m, const void *p, int64_t inner, int64_t outer, int64_t pitch, int64_t experts, int rows)
 {
@@ -182,29 +129,10 @@ template <bool kF32, int kCtas> cudaError_t wgrad(const LaunchCtx &c, const Nvfp
     if (!make_map_3d(&p.out, kF32 ? MapType::F32 : MapType::Bf16, a.d_w, {(uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E},
                      {a.K * size, a.K * size * a.N}, {(uint32_t)C::kChunk, 32, 1}, 128))
         return cudaErrorInvalidValue;
-    if (a.R_cap > 0) {
-        // the sizes of one expert with all rows; wgrad_maps_kernel sets each expert's own
-        MapArgs m = {};
-        const int64_t n = (a.R_cap + 127) / 128 * 128;
-        const bool ok = code_map(&m.like[kMapA], a.dy, n / 2, a.N, n / 2, 1, 128) &&
-                        code_map(&m.like[kMapB], a.x, n / 2, a.K, n / 2, 1, 64) &&
-                        scale_map(&m.like[kMapSa], a.dy_scales, n / 64, a.N / 128, 1) &&
-                        scale_map(&m.like[kMapSb], a.x_scales, n / 64, a.K / 128, 2);
-        if (!ok)
-            return cudaErrorInvalidValue;
-        m.base[kMapA] = a.dy;
-        m.base[kMapB] = a.x;
-        m.base[kMapSa] = a.dy_scales;
-        m.base[kMapSb] = a.x_scales;
-        m.H[kMapA] = m.H[kMapSa] = a.N;
-        m.H[kMapB] = m.H[kMapSb] = a.K;
-        CUtensorMap *out = static_cast<CUtensorMap *>(a.workspace);
-        cudaError_t e = launch_pdl(wgrad_maps_kernel, dim3((unsigned)a.E), dim3(128), 0, c.stream, m, a.offsets,
-                                   a.R_cap, out);
-        if (e != cudaSuccess)
-            return e;
-    }
-    p.maps = static_cast<const CUtensorMap *>(a.workspace);
+    p.col[kMapA] = a.dy;
+    p.col[kMapB] = a.x;
+    p.col[kMapSa] = a.dy_scales;
+    p.col[kMapSb] = a.x_scales;
     p.offsets = a.offsets;
     p.m_scale = a.dy_enc;
     p.n_scale = a.x_enc;

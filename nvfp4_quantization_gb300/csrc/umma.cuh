@@ -7,6 +7,38 @@
 
 namespace epq {
 
+// ---------------------------------------------------------------- loads
+// A word that an earlier kernel may have written just before: not moved ahead of
+// the wait for that kernel, as a load of unchanging memory could be.
+__device__ __forceinline__ int ld_word(const int32_t *p)
+{
+    int v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float ld_word(const float *p)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// 16 bytes to shared memory without a register between, zeros where !ok; and
+// this thread's arrival on `bar` (counted beforehand) when its copies so far
+// have landed.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
+}
+
+__device__ __forceinline__ void copy16_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void copy16_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ---------------------------------------------------------------- waits
 __device__ __forceinline__ uint64_t now_ns()
 {
@@ -114,13 +146,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int x, int y,
     else
         asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                          (uint64_t)m), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
-}
-
-// A tensor map that another kernel wrote: its bytes before any use through the
-// tensor-map proxy.
-__device__ __forceinline__ void tensormap_acquire(const CUtensorMap *m)
-{
-    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"((uint64_t)m) : "memory");
 }
 
 // ---------------------------------------------------------------- tensor memory

@@ -348,9 +348,7 @@ def test_nvfp4_wgrad(counts, K, N, dtype, accumulate):
     base = torch.randn(E, N, K, generator=g, device="cuda") if accumulate else torch.full((E, N, K), NAN, device="cuda")
     d_w = base.to(dtype, copy=True)
     status = nq.new_status("cuda")
-    ws = torch.full((512 * E,), 0xEE, dtype=torch.uint8, device="cuda")
-    nq.ep_nvfp4_grouped_wgrad(ops[0], ops[1], N, K, offsets, E, d_w=d_w, accumulate=accumulate, workspace=ws,
-                              status=status)
+    nq.ep_nvfp4_grouped_wgrad(ops[0], ops[1], N, K, offsets, E, d_w=d_w, accumulate=accumulate, status=status)
     for e in range(E):
         n = off[e + 1] - off[e]
         a, b = (columnwise_values(op, H, off, e) if n else torch.zeros(H, 1, dtype=torch.float64, device="cuda")

@@ -84,11 +84,9 @@ def test_graph_replay_with_other_values_and_offsets():
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
-def test_one_workspace_for_many_calls():
-    """Calls of other sizes and operands in turn with one workspace, nothing between
-    them: each uses its own tensor maps, not those that lay there before."""
+def test_calls_of_other_sizes_in_turn():
+    """Nothing between them, so that one starts while another ends."""
     g = gen(32)
-    ws = torch.empty(512 * 7, dtype=torch.uint8, device="cuda")
     sets = []
     for counts, n, k in (([130, 0, 300, 7, 128], 256, 384), ([1500], 128, 128), ([5, 700, 1, 128, 0, 64, 900], 512, 256),
                          ([128] * 7, 256, 384)):
@@ -106,7 +104,7 @@ def test_one_workspace_for_many_calls():
         for ops, n, k, offsets, E, want, out, status in sets:
             out.fill_(NAN)
         for ops, n, k, offsets, E, want, out, status in sets:
-            nq.ep_nvfp4_grouped_wgrad(ops[0], ops[1], n, k, offsets, E, d_w=out, workspace=ws, status=status)
+            nq.ep_nvfp4_grouped_wgrad(ops[0], ops[1], n, k, offsets, E, d_w=out, status=status)
         assert all(torch.equal(out, want) and int(status) == 0 for *_, want, out, status in sets)
 
 

@@ -82,21 +82,20 @@ def test_nvfp4_gemm_refusals(kw, status):
 
 
 def _nwgrad(**kw):
-    a = dict(y=FAKE, ys=FAKE, ye=FAKE, x=FAKE, xs=FAKE, xe=FAKE, R=640, N=128, K=256, off=FAKE, E=4, ws=FAKE, nws=2048,
+    a = dict(y=FAKE, ys=FAKE, ye=FAKE, x=FAKE, xs=FAKE, xe=FAKE, R=640, N=128, K=256, off=FAKE, E=4,
              dw=FAKE, dt=1, acc=0, st=FAKE)
     a.update(kw)
     return nq.lib().ep_nvfp4_grouped_wgrad(a["y"], a["ys"], a["ye"], a["x"], a["xs"], a["xe"], a["R"], a["N"], a["K"],
-                                           a["off"], a["E"], a["ws"], a["nws"], a["dw"], a["dt"], a["acc"], a["st"],
-                                           None)
+                                           a["off"], a["E"], a["dw"], a["dt"], a["acc"], a["st"], None)
 
 
 @pytest.mark.parametrize("kw, status", [
     (dict(y=None), -1), (dict(ys=None), -1), (dict(ye=None), -1), (dict(x=None), -1), (dict(xs=None), -1),
-    (dict(xe=None), -1), (dict(ws=None), -1), (dict(dw=None), -1), (dict(st=None), -1), (dict(N=64), -2),
-    (dict(K=192), -2), (dict(off=None), -2), (dict(off=None, E=1, R=600), -2), (dict(E=1025, nws=1 << 20), -2),
-    (dict(R=-1), -4), (dict(nws=2047), -4), (dict(dt=3), -5), (dict(dt=0, acc=1), -5), (dict(y=HALF), -3),
+    (dict(xe=None), -1), (dict(dw=None), -1), (dict(st=None), -1), (dict(N=64), -2),
+    (dict(K=192), -2), (dict(off=None), -2), (dict(off=None, E=1, R=600), -2), (dict(E=1025), -2),
+    (dict(R=-1), -4), (dict(dt=3), -5), (dict(dt=0, acc=1), -5), (dict(y=HALF), -3),
     (dict(ys=HALF), -3), (dict(ye=ODD), -3), (dict(x=HALF), -3), (dict(xs=HALF), -3), (dict(xe=ODD), -3),
-    (dict(ws=ctypes.c_void_p(0x10010)), -3), (dict(dw=HALF), -3)])
+    (dict(dw=HALF), -3)])
 def test_nvfp4_wgrad_refusals(kw, status):
     assert _nwgrad(**kw) == status
 
@@ -114,7 +113,7 @@ def test_host_memory_is_refused_with_ep_err_device():
     assert _wgrad(dy=h, x=h, off=h, cnt=h, dw=h, st=h) == -6
     assert _operand(rows=h, off=h, sc=h, rs=h, st=h) == -6
     assert _ngemm(x=h, xs=h, xr=h, w=h, ws=h, wr=h, off=h, out=h, st=h) == -6
-    assert _nwgrad(y=h, ys=h, ye=h, x=h, xs=h, xe=h, off=h, ws=h, dw=h, st=h) == -6
+    assert _nwgrad(y=h, ys=h, ye=h, x=h, xs=h, xe=h, off=h, dw=h, st=h) == -6
     assert buf.sum() == 0
 
 
@@ -122,7 +121,6 @@ def test_sizes():
     L = nq.lib()
     for rows, H in ((0, 64), (1, 32), (128, 64), (129, 96), (1000, 7168)):
         assert L.ep_nvfp4_scale_bytes(rows, H) == nq.nvfp4_scale_bytes(rows, H) == -(-rows // 128) * -(-H // 64) * 512
-    assert L.ep_nvfp4_wgrad_workspace_bytes(7) == 7 * 512
 
 
 def test_binding_refuses_host_tensors():
