@@ -338,40 +338,44 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
         uint32_t used = 0;
         for (int t = unit; t < tiles && ok; t += units) {
             const GroupedTile o = walk.tile();
-            const int half = ((o.n + 63) / 64 * 64) / kCtas, m = o.m0 + 128 * (int)rank, n = o.n0 + half * (int)rank;
+            // M and N are multiples of 128 here, so a tile's rows on either side are
+            // there or not as a whole.  What is not there is not copied and not used:
+            // lanes past M are not stored, steps past a row's end are not made.
+            const int half = o.n / kCtas, m = o.m0 + 128 * (int)rank, n = o.n0 + half * (int)rank;
+            const bool have_a = m < p.M;
             const int64_t pitch = o.rows / 2, blocks = (int64_t)o.rows * 8;    // bytes of a row, of 128 rows' scales
+            const int64_t pitch16 = 16 * pitch;
             const uint8_t *ca = p.col[kMapA] + (int64_t)o.row0 * p.M / 2 + (m + r0) * pitch + 16 * c;
             const uint8_t *cb = p.col[kMapB] + (int64_t)o.row0 * p.N / 2 + (n + r0) * pitch + 16 * c;
             const uint8_t *sa = p.col[kMapSa] + (int64_t)o.row0 * p.M / 16 + m / 128 * blocks + 16 * id;
             const uint8_t *sb = p.col[kMapSb] + (int64_t)o.row0 * p.N / 16 + o.n0 / 128 * blocks + 16 * id;
             const uint32_t to = 128 * r0 + ((c ^ (r0 & 7)) << 4);       // 128-byte swizzle
-            for (int kb = 0; kb < o.kb; ++kb) {
+            for (int kb = 0; kb < o.kb; ++kb, ca += 128, cb += 128, sa += 2048, sb += 2048) {
                 if (used >= kStages &&
                     !__all_sync(0xffffffffu, mbar_wait_for(&bar.empty[at.s], at.phase ^ 1, kWaitNs))) {
                     ok = false;
                     break;
                 }
-                const uint32_t a = ring + at.s * C::kStageBytes, b = a + C::kABytes;
-                const bool in = 128 * kb + 16 * c < pitch;
-                // rows are whole blocks of 128 on both sides; what is not there is not read
-                const bool in_a = in && m < p.M;
+                const uint32_t a = ring + at.s * C::kStageBytes, b = a + C::kABytes, s0 = b + C::kBBytes + 16 * id;
+                if (128 * kb + 16 * c < pitch) {
+                    if (have_a) {
+                        const uint8_t *q = ca;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    copy16(a + 2048 * i + to, in_a ? ca + 16 * i * pitch + 128 * kb : p.col[kMapA], in_a);
-#pragma unroll
-                for (int i = 0; i < kTileN / kCtas / 16; ++i) {
-                    if (16 * i < half) {                     // whole rounds: half is a multiple of 64
-                        const bool in_b = in && n + 16 * i + r0 < p.N;
-                        copy16(b + 2048 * i + to, in_b ? cb + 16 * i * pitch + 128 * kb : p.col[kMapB], in_b);
+                        for (int i = 0; i < 8; ++i, q += pitch16)
+                            copy16(a + to + 2048 * i, q);
                     }
-                }
-                const uint32_t s0 = b + C::kBBytes + 16 * id;
-                const bool in_s = 2048 * kb + 16 * id < blocks;
-                copy16(s0, in_s && m < p.M ? sa + 2048 * kb : p.col[kMapSa], in_s && m < p.M);
+                    const uint8_t *q = cb;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool in_b = in_s && o.n0 + 128 * i < p.N;
-                    copy16(s0 + C::kSaBytes + 2048 * i, in_b ? sb + i * blocks + 2048 * kb : p.col[kMapSb], in_b);
+                    for (int i = 0; i < kTileN / kCtas / 16; ++i, q += pitch16)
+                        if (16 * i < half)
+                            copy16(b + to + 2048 * i, q);
+                }
+                if (2048 * kb + 16 * id < blocks) {
+                    if (have_a)
+                        copy16(s0, sa);
+                    copy16(s0 + C::kSaBytes, sb);
+                    if (o.n > 128)
+                        copy16(s0 + C::kSaBytes + 2048, sb + blocks);
                 }
                 copy16_arrive(smem_u32(&bar.tail[at.s]));
                 at.step();
@@ -483,9 +487,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
                         ++acc_it;
                         tmem_fence_after();
                     }
-                    const bool cut = C::kRows || (C::kBmn && p.counts && kb == o.kb - 1);
-                    ok = cut ? mbar_wait_for<true>(&bar.full[at.s], at.phase, kWaitNs)
-                             : mbar_wait_for(&bar.full[at.s], at.phase, kWaitNs);
+                    ok = mbar_wait_for(&bar.full[at.s], at.phase, kWaitNs);
                     if (!ok)
                         break;
                     tmem_fence_after();

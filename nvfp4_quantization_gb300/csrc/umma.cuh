@@ -24,12 +24,11 @@ __device__ __forceinline__ float ld_word(const float *p)
     return v;
 }
 
-// 16 bytes to shared memory without a register between, zeros where !ok; and
-// this thread's arrival on `bar` (counted beforehand) when its copies so far
-// have landed.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok)
+// 16 bytes to shared memory without a register between; and this thread's
+// arrival on `bar` (counted beforehand) when its copies so far have landed.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void copy16_arrive(uint32_t bar)
@@ -47,28 +46,15 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
-// A try at a phase that a thread of the pair's other CTA completes after writes
-// to its own shared memory.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return ok != 0;
-}
-
 // Wait on a phase of an mbarrier, for limit_ns at most; false if it gave up.
-template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
 {
     for (int i = 0; i < 64; ++i)
-        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))
+        if (mbar_try_wait(bar, parity))
             return true;
     const uint64_t t0 = now_ns();
     while (now_ns() - t0 < limit_ns)
-        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))
+        if (mbar_try_wait(bar, parity))
             return true;
     return false;
 }
@@ -100,13 +86,15 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank)
     return r;
 }
 
-// Arrivals on a barrier of any CTA of the cluster.  The first orders this
-// thread's writes to shared memory before it.  The others order none (a release
-// at cluster scope waits for the thread's earlier copies to be on their way:
-// with one a stage the products below ran at 0.4 of their rate).
+// Arrivals on a barrier of any CTA of the cluster.  The first orders the CTA's
+// earlier writes to its own shared memory before it (they are read there, by
+// the CTA's own part of the matrix unit, so the CTA's scope is enough).  The
+// others order none: a release at cluster scope waits for the thread's earlier
+// copies to be on their way, and with one a stage the BF16 products ran at 0.4
+// of their rate and the NVFP4 weight gradient took 652 us instead of 510.
 __device__ __forceinline__ void mbar_arrive_release_at(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
