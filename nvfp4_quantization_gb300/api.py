@@ -707,10 +707,11 @@ def ep_nvfp4_operand(rows: torch.Tensor, H: int, offsets: torch.Tensor | None = 
                      status: torch.Tensor | None = None, stream=None, copy_codes: bool = False,
                      codes: torch.Tensor | None = None) -> dict:
     """Packed NVFP4 rows as an operand of ep_nvfp4_grouped_gemm: keys rw_codes,
-    rw_scales (tiled) and rw_row_scale.
+    rw_scales (tiled), rw_row_scale and K (= H).
 
-    rw_codes is a view of the rows; with ``copy_codes`` (or ``codes``, uint8 [...,
-    H/2]) a copy, from which large products run up to a fifth faster.
+    rw_codes is ``rows`` itself (a row's codes are its first H/2 bytes); with
+    ``copy_codes`` (or ``codes``, uint8 [..., H/2]) a copy of the codes alone,
+    from which large products run up to a fifth faster.
 
     ``rows`` uint8 [R_cap, row_bytes(H)], of which [0, offsets[E]) are taken
     (all without ``offsets``), or weights [E, N, row_bytes(H)] as
@@ -747,9 +748,7 @@ def ep_nvfp4_operand(rows: torch.Tensor, H: int, offsets: torch.Tensor | None = 
                                      row_scale.data_ptr(), _at(codes), status.data_ptr(), _stream_of(stream, dev))
     if st:
         check("ep_nvfp4_operand", st)
-    if codes is None:
-        codes = rows.as_strided((n, H // 2), (S, 1)) if len(shape) == 2 else rows[..., : H // 2]
-    return {"rw_codes": codes, "rw_scales": scales, "rw_row_scale": row_scale}
+    return {"rw_codes": rows if codes is None else codes, "rw_scales": scales, "rw_row_scale": row_scale, "K": H}
 
 
 def _need_bytes(t: torch.Tensor, name: str, n: int):
@@ -767,19 +766,23 @@ def ep_nvfp4_grouped_gemm(x: dict, w: dict, offsets: torch.Tensor | None = None,
     """Rows of expert e times its weights, both NVFP4: BF16 [R_cap, N].
 
     ``x``: the rowwise operand of R_cap rows (keys rw_codes, rw_scales in tiles,
-    rw_row_scale), from ep_nvfp4_direct_receive(..., swizzled=True) or
-    ep_nvfp4_operand.  ``w``: the operand of weights [E, N, K], from
-    ep_nvfp4_operand.  The gradient of the rows is the same call with the packed
+    rw_row_scale; K where rows of rw_codes are longer than K/2 bytes), from
+    ep_nvfp4_direct_receive(..., swizzled=True) or ep_nvfp4_operand.  ``w``: the
+    operand of weights [E, N, K], from ep_nvfp4_operand.  The gradient of the rows is the same call with the packed
     transposed weights.  ``offsets`` and the rows as in ep_grouped_gemm."""
     xc, wc = x["rw_codes"], w["rw_codes"]
     ld_x = _need_rows(xc, 'x["rw_codes"]', (torch.uint8,))
-    R_cap, K = xc.shape[0], 2 * xc.shape[1]
-    dev = xc.device
-    if wc.dim() != 3 or wc.dtype != torch.uint8 or wc.shape[2] != xc.shape[1]:
-        raise ValueError(f'w["rw_codes"] must be uint8 [E, N, {xc.shape[1]}], got {wc.dtype} {tuple(wc.shape)}')
-    E, N = wc.shape[:2]
-    ld_w = wc.stride(1) if N > 1 else wc.stride(0) if E > 1 else max(K // 2, 1)
-    if (K > 2 and wc.stride(2) != 1) or (E > 1 and wc.stride(0) != N * ld_w) or ld_w < K // 2:
+    R_cap, width = xc.shape
+    K, dev = x.get("K", 2 * width), xc.device
+    if wc.dim() != 3 or wc.dtype != torch.uint8:
+        raise ValueError(f'w["rw_codes"] must be uint8 with three dimensions, got {wc.dtype} {tuple(wc.shape)}')
+    E, N, w_width = wc.shape
+    if w.get("K", 2 * w_width) != K or K % 2 or K > 2 * width or K > 2 * w_width:
+        raise ValueError(f"x has rows of {K} elements in {width} bytes, w of {w.get('K', 2 * w_width)} in {w_width}")
+    ld_e, ld_w, unit = wc.stride()
+    if N <= 1:
+        ld_w = ld_e if E > 1 else max(w_width, 1)
+    if (w_width > 1 and unit != 1) or (E > 1 and ld_e != N * ld_w) or ld_w < w_width:
         raise ValueError('w["rw_codes"] must have contiguous rows at one distance')
     # blocks of 128 rows that the call may read; without offsets the last may be cut
     blocks = R_cap // 128 if offsets is not None else -(-R_cap // 128)

@@ -202,14 +202,15 @@ def test_operand(R, K):
     g = gen(5)
     rows = pack_rows(randn(g, R, K))
     op, copied = nq.ep_nvfp4_operand(rows, K), nq.ep_nvfp4_operand(rows, K, copy_codes=True)
-    assert all(torch.equal(copied[name], op[name]) for name in op) and copied["rw_codes"].is_contiguous()
+    assert torch.equal(copied["rw_codes"], rows[:, : K // 2]) and op["K"] == copied["K"] == K
+    assert all(torch.equal(copied[name], op[name]) for name in ("rw_scales", "rw_row_scale"))
     M, kt = -(-R // 128) * 128, -(-K // 64)
     want = torch.zeros(M, kt * 4, dtype=torch.uint8, device="cuda")
     want[:R, : K // 16] = rows[:, K // 2: 9 * K // 16]
     assert op["rw_scales"].numel() == M * kt * 4 == nq.nvfp4_scale_bytes(R, K) == nq.lib().ep_nvfp4_scale_bytes(R, K)
     assert torch.equal(untile(op["rw_scales"], M, kt * 4), want)
     assert torch.equal(op["rw_row_scale"].double(), decode_rows(rows, K)[1])
-    assert op["rw_codes"].data_ptr() == rows.data_ptr() and op["rw_codes"].shape == (R, K // 2)
+    assert op["rw_codes"] is rows
 
 
 def test_operand_of_slots_and_of_weights():
@@ -231,7 +232,7 @@ def test_operand_of_slots_and_of_weights():
     assert (codes[off[-1]:] == 0xCD).all()
     w = nq.ep_nvfp4_pack_weights(randn(g, 3, 150, K).to(torch.bfloat16))
     op = nq.ep_nvfp4_operand(w, K)
-    assert torch.equal(nq.ep_nvfp4_operand(w, K, copy_codes=True)["rw_codes"], op["rw_codes"])
+    assert torch.equal(nq.ep_nvfp4_operand(w, K, copy_codes=True)["rw_codes"], w[..., : K // 2])
     for e in range(3):
         one = nq.ep_nvfp4_operand(w[e], K)
         assert torch.equal(op["rw_scales"].view(3, -1)[e], one["rw_scales"])
@@ -275,13 +276,15 @@ def test_nvfp4_gemm(counts, K, N):
     wo = nq.ep_nvfp4_operand(w, K)
     outs = []
     received = nq.ep_nvfp4_direct_receive(rows, K, offsets, E, swizzled=True)
-    for x in (received, nq.ep_nvfp4_operand(rows, K, offsets, E)):
+    packed, copied = (nq.ep_nvfp4_operand(rows, K, offsets, E, copy_codes=c) for c in (False, True))
+    view = dict(rw_codes=rows[:, : K // 2], rw_scales=packed["rw_scales"], rw_row_scale=packed["rw_row_scale"])
+    for x in (received, packed, copied, view):
         out = torch.full((R_cap, N), 7.0, dtype=torch.bfloat16, device="cuda")
         status = nq.new_status("cuda")
         nq.ep_nvfp4_grouped_gemm(x, wo, offsets, out=out, status=status)
         assert int(status) == 0
         outs.append(out)
-    assert torch.equal(outs[0], outs[1])
+    assert all(torch.equal(o, outs[0]) for o in outs)
     for e, c in enumerate(counts):
         if c:
             at = slice(off[e], off[e + 1])

@@ -76,7 +76,8 @@ def test_graph_replay_with_other_values_and_offsets():
         t = operands(g, R_cap, 5, K, N, o2, live2)
         for name, v in t.items():
             for a, b in zip(*((d.values() if isinstance(d, dict) else [d]) for d in (s[name], v))):
-                a.copy_(b)
+                if isinstance(a, torch.Tensor):
+                    a.copy_(b)
         offsets.copy_(o2)
         counts.copy_(ints(c))
         graph.replay()
@@ -157,7 +158,7 @@ def test_rows_past_the_capacity():
     assert int(status) == nq.EP_DEV_ERR_CAPACITY
     assert torch.equal(d_w[0], want[4][0]) and (d_w[1] == 0).all()
     status.zero_()
-    few = dict(rw_codes=s["xo"]["rw_codes"][:cut], rw_scales=s["xo"]["rw_scales"], rw_row_scale=s["xo"]["rw_row_scale"])
+    few = dict(s["xo"], rw_codes=s["xo"]["rw_codes"][:cut])
     guard.fill_(7.0)
     nq.ep_nvfp4_grouped_gemm(few, s["wo"], offsets, out=guard[:cut], status=status)
     assert int(status) == nq.EP_DEV_ERR_CAPACITY
@@ -327,6 +328,8 @@ def test_empty_calls():
 
 def test_binding_refusals():
     z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")   # noqa: E731
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8, device="cuda")   # noqa: E731
+    operand = lambda *s: nq.ep_nvfp4_operand(u8((*s[:-1], nq.row_bytes(s[-1]))), s[-1])   # noqa: E731
     off = ints([0, 128, 128])
     for bad in (lambda: nq.ep_grouped_gemm(z(128, 64), z(2, 8, 72), off),
                 lambda: nq.ep_grouped_gemm(z(128, 64), z(2, 8, 64)),
@@ -338,7 +341,11 @@ def test_binding_refusals():
                 lambda: nq.ep_grouped_wgrad(z(128, 64), z(128, 64), off, 2, accumulate=True),
                 lambda: nq.ep_grouped_wgrad(z(128, 64), z(128, 64), off, 2, dtype=torch.float16),
                 lambda: nq.ep_grouped_wgrad(z(128, 64), z(128, 64), off, 2, counts=ints([1])),
-                lambda: nq.ep_nvfp4_operand(torch.zeros(4, 40, dtype=torch.uint8, device="cuda"), 64)):
+                lambda: nq.ep_nvfp4_operand(torch.zeros(4, 40, dtype=torch.uint8, device="cuda"), 64),
+                lambda: nq.ep_nvfp4_grouped_gemm(operand(8, 64), operand(1, 8, 96)),
+                lambda: nq.ep_nvfp4_grouped_gemm(dict(operand(8, 64), K=128), dict(operand(1, 8, 64), K=128)),
+                lambda: nq.ep_nvfp4_grouped_gemm(operand(300, 64), dict(operand(1, 8, 64), rw_scales=u8(500))),
+                lambda: nq.ep_nvfp4_grouped_gemm(dict(operand(300, 64), rw_scales=u8(1024)), operand(1, 8, 64))):
         with pytest.raises(ValueError):
             bad()
     for bad in (lambda: nq.ep_grouped_gemm(z(128, 60), z(2, 8, 60), off),
