@@ -18,6 +18,38 @@
 // pitch only the device knows, so no tensor map of the host's fits them.  There
 // warps 12-15 copy the rows in 16-byte pieces, and warp 8 passes the arrival of
 // a stage on to the matrix products.
+//
+// What bounds it.  Large BF16 products: the tensor cores (busy 97 % of the time
+// on 8192 x 8192 x 4096), and with them the card's power: 8192^3 runs at 1.94
+// PFLOP/s in a burst and 1.62 for seconds on end, where torch.matmul has 1.98 and
+// 1.69.  NVFP4 products: the copies into shared memory.  Rows that start on a
+// line of 128 bytes reach 6.3 PFLOP/s (98304 rows, 64 experts of 4096 x 4096,
+// 525 us), packed rows, two lines to every 128 bytes, 5.2 (630 us); copies of the
+// block scales to tensor memory cost the products a quarter of their rate where
+// the tile has 128 columns, little where it has 256.  Small batches: reading the
+// weights (128 tokens, 8 of 64 experts of 4096 x 4096: NVFP4 119 us, 5.2 TB/s;
+// BF16 354 us, 6.1 TB/s).  Weight gradients with few rows an expert: writing them
+// (1536 rows, NVFP4, FP32 out: 505 us, 4.9 TB/s with the reads).
+//
+// Why it is as it is, each step against the state before (98304 rows, 64 experts
+// of 4096 x 4096, BF16 / NVFP4):
+//  - CTA pairs, tiles of 256 x 256: a CTA reads half of the N side and the matrix
+//    unit the other half from its neighbour.  One CTA a tile is within 6 % of the
+//    pair's time for BF16, but takes 1.36 times it for NVFP4.
+//  - instructions that take uniform registers (copies, products) under an elected
+//    thread (umma.cuh): 2.19 / 1.18 ms -> 1.88 / 0.69.
+//  - the next tiles worked out 32 at a time, a lane each: a change of tiles made
+//    the products pause for about 0.5 us before.
+//  - accumulators of 256 columns twice, so that a tile is written while the next
+//    is computed.  Block scales take 48 columns; there the two overlap in 64,
+//    which are emptied first and waited for only where both tiles use them
+//    (1021 tokens, 5 of 61 experts of 2056 x 1056: 31.9 -> 28.7 us with the next
+//    step).
+//  - eight warps for the epilogue, one piece of output each: with two pieces a
+//    warp, and so a stage less, the weight gradients took 5 to 9 % longer.
+//  - measured and dropped: hints to L2 for what is written or read (no change);
+//    block scales copied as 64-bit words in one piece (no change); a register
+//    split between the warps (the epilogue spilled more, not less).
 #pragma once
 
 #include "epq_internal.h"
