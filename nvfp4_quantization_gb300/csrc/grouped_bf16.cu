@@ -31,7 +31,7 @@ template <bool kAmn, int kCtas> cudaError_t gemm(const LaunchCtx &c, const Group
     p.E = a.E;
     p.M = p.N = a.N;
     p.K = a.K;
-    return launch_grouped<C>(c, p, ceil_div(a.N, 128 * kCtas) * (ceil_div(a.R_cap, kTileN) + a.E));
+    return launch_grouped<C>(c, p, ceil_div(a.N, C::kSpan) * (ceil_div(a.R_cap, kTileN) + a.E));
 }
 
 template <bool kF32, int kCtas> cudaError_t wgrad(const LaunchCtx &c, const GroupedWgradArgs &a)
@@ -54,7 +54,7 @@ template <bool kF32, int kCtas> cudaError_t wgrad(const LaunchCtx &c, const Grou
     p.M = a.N;
     p.N = a.K;
     p.add = a.add;
-    return launch_grouped<C>(c, p, a.E * ceil_div(a.N, 128 * kCtas) * ceil_div(a.K, kTileN));
+    return launch_grouped<C>(c, p, a.E * ceil_div(a.N, C::kSpan) * ceil_div(a.K, kTileN));
 }
 
 } // namespace

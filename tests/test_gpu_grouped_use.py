@@ -376,3 +376,27 @@ def test_nvfp4_layer(T, H, I, E, k):
     assert err["d_x_nvfp4"] <= d_h + SR + FP4
     assert err["d_w1_nvfp4"] <= d_h + SR + 2 * FP4    # d_h once more, x packed and again along the tokens
     assert err["d_w2_nvfp4"] <= 2 * SR + 4 * FP4 + BF16
+
+
+@pytest.mark.parametrize("n,k", [(4096, 1056), (3000, 544), (2568, 96)])
+def test_large_products_of_packed_rows(n, k):
+    """Enough rows and features for clusters that share the rows' side, the last
+    tile of the features cut; rows of experts of 1 to 2300 tokens."""
+    g = gen(33)
+    counts = [2300, 1, 900, 0, 1500, 256, 700, 1024]
+    offsets, off, R_cap, live = slots(counts, spare=40)
+    rows = torch.zeros(R_cap, nq.row_bytes(k), dtype=torch.uint8, device="cuda")
+    rows[: off[-1]] = tg.pack_rows(randn(g, off[-1], k))
+    w = nq.ep_nvfp4_pack_weights(randn(g, len(counts), n, k).to(torch.bfloat16))
+    status = nq.new_status("cuda")
+    out = torch.full((R_cap, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    nq.ep_nvfp4_grouped_gemm(nq.ep_nvfp4_operand(rows, k, offsets, len(counts)), nq.ep_nvfp4_operand(w, k), offsets,
+                             out=out, status=status)
+    copied = nq.ep_nvfp4_grouped_gemm(nq.ep_nvfp4_operand(rows, k, offsets, len(counts), copy_codes=True),
+                                      nq.ep_nvfp4_operand(w, k, copy_codes=True), offsets, status=status)
+    assert torch.equal(out[: off[-1]], copied[: off[-1]]) and (out[off[-1]:] == 7.0).all() and int(status) == 0
+    for e in range(len(counts)):
+        if counts[e]:
+            at = slice(off[e], off[e + 1])
+            want, mag = tg.nvfp4_reference(rows[at], w[e], k)
+            within(out[at], want, sum_bound(k, mag, want, torch.bfloat16, more=2))
