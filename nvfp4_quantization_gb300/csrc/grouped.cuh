@@ -61,7 +61,6 @@
 
 namespace epq {
 
-constexpr int kTileN = 256;
 constexpr int kGroupTiles = 8;       // tiles of the N side that share the M side's tiles in L2
 constexpr int kOutWarps = 8;         // two to a quarter of the accumulator's lanes
 constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpCut = 10, kWarpRows = 12, kRowWarps = 4;
@@ -87,6 +86,9 @@ template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_, int kPai
     static constexpr bool kFp4 = kFp4_, kWgrad = kWgrad_, kF32 = kF32_;
     static constexpr int kCtas = kCtas_;                      // that compute a tile: one or a pair
     static constexpr int kPairs = kPairs_;                    // pairs of a cluster, with the same N side
+    // columns of a tile: where single CTAs take a product, slots are short and
+    // stages in flight count
+    static constexpr int kTileN = kCtas == 1 && !kWgrad ? 128 : 256;
     static constexpr int kCluster = kCtas * kPairs, kSpan = 128 * kCluster;
     static constexpr bool kAmn = kAmn_;                       // A with its M side contiguous (BF16)
     static constexpr bool kRows = kFp4 && kWgrad;             // copied in pieces, not by TMA
@@ -97,7 +99,7 @@ template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_, int kPai
     static constexpr uint32_t kABytes = 128 * 128;
     static constexpr uint32_t kBBytes = kTileN / kCtas * 128;
     static constexpr uint32_t kSaBytes = kFp4 ? 2048 : 0;
-    static constexpr uint32_t kSbBytes = kFp4 ? 4096 : 0;
+    static constexpr uint32_t kSbBytes = kFp4 ? kTileN / 128 * 2048 : 0;
     static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
     static constexpr uint32_t kOutBytes = kWgrad ? 4096 : 2048;   // a warp's piece of a tile
     static constexpr uint32_t kOutAll = kOutWarps * kOutBytes;
@@ -183,26 +185,26 @@ __device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams &p, cons
     int j = t - start[lo];
     o.e = 2 * lo;
     int rows = expert_rows<C>(p, o.e, o.row0, err);
-    int nt = ((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN;
+    int nt = ((C::kWgrad ? p.N : rows) + C::kTileN - 1) / C::kTileN;
     if (j >= mt * nt) {
         j -= mt * nt;
         rows = expert_rows<C>(p, ++o.e, o.row0, err);
-        nt = ((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN;
+        nt = ((C::kWgrad ? p.N : rows) + C::kTileN - 1) / C::kTileN;
     }
     // groups of kGroupTiles tiles of the N side; in a group they change fastest
     const int g = j / (kGroupTiles * mt), in = j - g * kGroupTiles * mt;
     const int gn = min(kGroupTiles, nt - g * kGroupTiles);
     const int mi = in / gn, ni = g * kGroupTiles + in - mi * gn;
     o.m0 = mi * C::kSpan;
-    o.n0 = ni * kTileN;
+    o.n0 = ni * C::kTileN;
     if (C::kWgrad) {
         o.rows = rows;
         if (p.counts)
             o.rows = max(0, min(rows, ld_word(p.counts + o.e)));
-        o.n = min(kTileN, p.N - o.n0);
+        o.n = min(C::kTileN, p.N - o.n0);
         o.kb = (o.rows + C::kBlockK - 1) / C::kBlockK;
     } else {
-        o.rows = o.n = min(kTileN, rows - o.n0);
+        o.rows = o.n = min(C::kTileN, rows - o.n0);
         o.kb = (p.K + C::kBlockK - 1) / C::kBlockK;
     }
     return o;
@@ -255,7 +257,7 @@ __device__ __forceinline__ void grouped_plan(const GroupedParams &p, int *start,
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int rows = e0 + i < p.E ? expert_rows<C>(p, e0 + i, off, err) : 0;
-        n[i] = e0 + i < p.E ? mt * (((C::kWgrad ? p.N : rows) + kTileN - 1) / kTileN) : 0;
+        n[i] = e0 + i < p.E ? mt * (((C::kWgrad ? p.N : rows) + C::kTileN - 1) / C::kTileN) : 0;
         mine += n[i];
     }
     int sum = mine;
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
                     }
                     const uint8_t *q = cb;
 #pragma unroll
-                    for (int i = 0; i < kTileN / kCtas / 16; ++i, q += pitch16)
+                    for (int i = 0; i < C::kTileN / kCtas / 16; ++i, q += pitch16)
                         if (16 * i < half)
                             copy16(b + to + 2048 * i, q);
                 }
@@ -706,7 +708,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
                 }
                 continue;
             }
-            float keep[C::kKeep ? 4 : 1][32];
+            float keep[C::kKeep ? C::kTileN / 64 : 1][32];
             for (int part = 0; part < parts; ++part) {
                 if (C::kParts && !C::kKeep && part > 0 && elect_one())
                     tma_store_wait0();             // what is added to has been written
@@ -721,7 +723,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
                 tmem_fence_after();
                 const bool shared_first = C::kFp4 && (back || b == 1);
 #pragma unroll
-                for (int q = 0; q < kTileN / 2 / C::kChunk; ++q) {
+                for (int q = 0; q < C::kTileN / 2 / C::kChunk; ++q) {
                     const int cc = side + 2 * q;
                     if (q > 0 && cc >= nch)
                         break;
@@ -825,19 +827,20 @@ template <class C> cudaError_t grouped_units(const LaunchCtx &c, int &units)
     return cudaSuccess;
 }
 
-// Whether single CTAs (128 x 256 a tile) rather than pairs (256 x 256) take a call
-// whose M side has M rows and whose N sides make n_tiles tiles.  A pair reads half
-// the bytes of the N side a CTA; single CTAs have the finer tiles.  Measured on
-// GB300, single against pair: where all tiles run at once 8.5 us against 9.2 (one
-// token, 2 of 8 experts of 1024 x 1024, BF16); where rounds of tiles decide 14.5
-// against 18.0 (16 experts of 1152 x 1024, NVFP4 weight gradient: 4 rounds against
-// 5); with many rounds 1.06 (BF16 products), 1.14 to 1.23 (weight gradients) and
-// 1.36 (NVFP4 products) times the pair's time.
+// Whether single CTAs rather than pairs take a call whose M side has M rows and
+// whose N sides make n_tiles of the single CTA's tiles.  Products (128 x 128 a
+// tile): where all tiles run at once.  Measured on GB300, single against pair:
+// 8.5 us against 9.2 (one token, 2 of 8 experts of 1024 x 1024), 8.8 against 10.6
+// and in NVFP4 7.2 against 8.7 (300 tokens, 2 of 8 of 1024 x 1024); with two rounds
+// 8.8 against 8.5 (1000 tokens, 4 experts of 2048 x 512).  Weight gradients (128 x
+// 256): there, and where rounds of tiles decide: 13.1 against 18 (16 experts of
+// 1152 x 1024, NVFP4: 4 rounds against 5); with many rounds a single CTA's tile
+// takes 1.14 to 1.23 times the pair's time.
 template <class C> bool single_ctas(const LaunchCtx &c, int64_t M, int64_t n_tiles)
 {
     const int64_t one = (M + 127) / 128 * n_tiles, pair = (M + 255) / 256 * n_tiles;
     const int64_t rounds1 = (one + c.num_sms - 1) / c.num_sms, rounds2 = (pair + c.num_sms / 2 - 1) / (c.num_sms / 2);
-    return one <= c.num_sms || rounds1 * (C::kWgrad ? 12 : C::kFp4 ? 14 : 11) < rounds2 * 10;
+    return one <= c.num_sms || (C::kWgrad && rounds1 * 12 < rounds2 * 10);
 }
 
 // `most_tiles`: a bound on the call's tiles that the host knows.

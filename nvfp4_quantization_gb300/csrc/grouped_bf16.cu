@@ -31,7 +31,7 @@ template <bool kAmn, int kCtas> cudaError_t gemm(const LaunchCtx &c, const Group
     p.E = a.E;
     p.M = p.N = a.N;
     p.K = a.K;
-    return launch_grouped<C>(c, p, ceil_div(a.N, C::kSpan) * (ceil_div(a.R_cap, kTileN) + a.E));
+    return launch_grouped<C>(c, p, ceil_div(a.N, C::kSpan) * (ceil_div(a.R_cap, C::kTileN) + a.E));
 }
 
 template <bool kF32, int kCtas> cudaError_t wgrad(const LaunchCtx &c, const GroupedWgradArgs &a)
@@ -54,7 +54,7 @@ template <bool kF32, int kCtas> cudaError_t wgrad(const LaunchCtx &c, const Grou
     p.M = a.N;
     p.N = a.K;
     p.add = a.add;
-    return launch_grouped<C>(c, p, a.E * ceil_div(a.N, C::kSpan) * ceil_div(a.K, kTileN));
+    return launch_grouped<C>(c, p, a.E * ceil_div(a.N, C::kSpan) * ceil_div(a.K, C::kTileN));
 }
 
 } // namespace
@@ -63,15 +63,16 @@ cudaError_t launch_grouped_gemm(const LaunchCtx &c, const GroupedGemmArgs &a)
 {
     if (a.R_cap == 0)
         return cudaSuccess;
-    // tiles of the rows: about half a tile an expert is lost in its slot
-    if (single_ctas<GroupedCfg<false, false, false, 1, false>>(c, a.N, ceil_div(a.R_cap, kTileN) + a.E / 2))
+    using One = GroupedCfg<false, false, false, 1, false>;
+    if (single_ctas<One>(c, a.N, ceil_div(a.R_cap, One::kTileN)))
         return a.transposed ? gemm<true, 1>(c, a) : gemm<false, 1>(c, a);
     return a.transposed ? gemm<true, 2>(c, a) : gemm<false, 2>(c, a);
 }
 
 cudaError_t launch_grouped_wgrad(const LaunchCtx &c, const GroupedWgradArgs &a)
 {
-    if (single_ctas<GroupedCfg<false, true, true, 1, false>>(c, a.N, a.E * ceil_div(a.K, kTileN)))
+    using One = GroupedCfg<false, true, true, 1, false>;
+    if (single_ctas<One>(c, a.N, a.E * ceil_div(a.K, One::kTileN)))
         return a.f32 ? wgrad<true, 1>(c, a) : wgrad<false, 1>(c, a);
     return a.f32 ? wgrad<true, 2>(c, a) : wgrad<false, 2>(c, a);
 }

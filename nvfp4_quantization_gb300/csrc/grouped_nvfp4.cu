@@ -105,7 +105,7 @@ template <int kCtas, int kPairs = 1> cudaError_t gemm(const LaunchCtx &c, const 
     const bool ok = code_map(&p.map[kMapA], a.w, a.K / 2, a.N, a.ld_w, a.E, 128) &&
                     code_map(&p.map[kMapB], a.x, a.K / 2, a.R_cap, a.ld_x, 1, 64) &&
                     scale_map(&p.map[kMapSa], a.w_scales, kt, ceil_div(a.N, 128) * a.E, 1) &&
-                    scale_map(&p.map[kMapSb], a.x_scales, kt, blocks, 2) &&
+                    scale_map(&p.map[kMapSb], a.x_scales, kt, blocks, C::kTileN / 128) &&
                     make_map_3d(&p.out, MapType::Bf16, a.out, {(uint64_t)a.N, (uint64_t)a.R_cap, 1},
                                 {(uint64_t)a.N * 2, (uint64_t)a.N * 2 * a.R_cap}, {32, 32, 1}, 64);
     if (!ok)
@@ -118,7 +118,7 @@ template <int kCtas, int kPairs = 1> cudaError_t gemm(const LaunchCtx &c, const 
     p.E = a.E;
     p.M = p.N = a.N;
     p.K = a.K;
-    return launch_grouped<C>(c, p, ceil_div(a.N, C::kSpan) * (ceil_div(a.R_cap, kTileN) + a.E));
+    return launch_grouped<C>(c, p, ceil_div(a.N, C::kSpan) * (ceil_div(a.R_cap, C::kTileN) + a.E));
 }
 
 // Whether clusters of two pairs take the product: where rows straddle lines of
@@ -138,7 +138,7 @@ bool shared_n_side(const LaunchCtx &c, const Nvfp4GemmArgs &a)
     int pairs = 0, clusters = 0;
     if (grouped_units<Pair>(c, pairs) != cudaSuccess || grouped_units<Cluster>(c, clusters) != cudaSuccess)
         return false;
-    const int64_t n = ceil_div(a.R_cap, kTileN);
+    const int64_t n = ceil_div(a.R_cap, Pair::kTileN);
     return 86 * ceil_div(ceil_div(a.N, Cluster::kSpan) * n, clusters) < 100 * ceil_div(ceil_div(a.N, Pair::kSpan) * n, pairs);
 }
 
@@ -163,7 +163,7 @@ template <bool kF32, int kCtas> cudaError_t wgrad(const LaunchCtx &c, const Nvfp
     p.M = a.N;
     p.N = a.K;
     p.add = a.add;
-    return launch_grouped<C>(c, p, a.E * ceil_div(a.N, 128 * kCtas) * ceil_div(a.K, kTileN));
+    return launch_grouped<C>(c, p, a.E * ceil_div(a.N, C::kSpan) * ceil_div(a.K, C::kTileN));
 }
 
 } // namespace
@@ -179,7 +179,8 @@ cudaError_t launch_operand(const LaunchCtx &c, const OperandArgs &a)
 
 cudaError_t launch_nvfp4_gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a)
 {
-    if (single_ctas<GroupedCfg<true, false, false, 1, false>>(c, a.N, ceil_div(a.R_cap, kTileN) + a.E / 2))
+    using One = GroupedCfg<true, false, false, 1, false>;
+    if (single_ctas<One>(c, a.N, ceil_div(a.R_cap, One::kTileN)))
         return gemm<1>(c, a);
     if (shared_n_side(c, a))
         return gemm<2, 2>(c, a);
@@ -188,7 +189,8 @@ cudaError_t launch_nvfp4_gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a)
 
 cudaError_t launch_nvfp4_wgrad(const LaunchCtx &c, const Nvfp4WgradArgs &a)
 {
-    if (single_ctas<GroupedCfg<true, true, false, 1, false>>(c, a.N, a.E * ceil_div(a.K, kTileN)))
+    using One = GroupedCfg<true, true, false, 1, false>;
+    if (single_ctas<One>(c, a.N, a.E * ceil_div(a.K, One::kTileN)))
         return a.f32 ? wgrad<true, 1>(c, a) : wgrad<false, 1>(c, a);
     return a.f32 ? wgrad<true, 2>(c, a) : wgrad<false, 2>(c, a);
 }
