@@ -642,8 +642,8 @@ size_t ep_nvfp4_scale_bytes(int64_t rows, int64_t H);
  *   codes           device u8 [groups * rows_per_group, H/2] or NULL.  With it
  *                   the codes are copied there, row after row.  Packed rows
  *                   start anywhere on 16 bytes, which costs the products' copies
- *                   a fifth of their rate: large batches gain from rows of their
- *                   own (98304 rows, 64 experts of 4096 x 4096 on GB300: 630 us
+ *                   a part of their rate: large batches gain from rows of their
+ *                   own (98304 rows, 64 experts of 4096 x 4096 on GB300: 600 us
  *                   from packed rows and weights, 525 from copies; 128 tokens 8
  *                   of 64 experts 121 and 112).
  */

@@ -711,7 +711,7 @@ def ep_nvfp4_operand(rows: torch.Tensor, H: int, offsets: torch.Tensor | None = 
 
     rw_codes is ``rows`` itself (a row's codes are its first H/2 bytes); with
     ``copy_codes`` (or ``codes``, uint8 [..., H/2]) a copy of the codes alone,
-    from which large products run up to a fifth faster.
+    from which large products run up to an eighth faster.
 
     ``rows`` uint8 [R_cap, row_bytes(H)], of which [0, offsets[E]) are taken
     (all without ``offsets``), or weights [E, N, row_bytes(H)] as

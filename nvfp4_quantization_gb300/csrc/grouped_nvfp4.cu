@@ -98,14 +98,13 @@ template <int kCtas, int kPairs = 1> cudaError_t gemm(const LaunchCtx &c, const 
     using C = GroupedCfg<true, false, false, kCtas, false, kPairs>;
     GroupedParams p = {};
     const int64_t kt = ceil_div(a.K, 64);
-    // slots are whole blocks of 128 rows; without slots the last block may be cut
+    // slots are whole blocks of 128 rows, so that rows past the last whole block are
+    // past the capacity; without slots the last block may be cut
     const int64_t blocks = a.offsets ? a.R_cap / 128 : ceil_div(a.R_cap, 128);
-    if (blocks == 0)
-        return cudaSuccess;
     const bool ok = code_map(&p.map[kMapA], a.w, a.K / 2, a.N, a.ld_w, a.E, 128) &&
                     code_map(&p.map[kMapB], a.x, a.K / 2, a.R_cap, a.ld_x, 1, 64) &&
                     scale_map(&p.map[kMapSa], a.w_scales, kt, ceil_div(a.N, 128) * a.E, 1) &&
-                    scale_map(&p.map[kMapSb], a.x_scales, kt, blocks, C::kTileN / 128) &&
+                    scale_map(&p.map[kMapSb], a.x_scales, kt, blocks > 0 ? blocks : 1, C::kTileN / 128) &&
                     make_map_3d(&p.out, MapType::Bf16, a.out, {(uint64_t)a.N, (uint64_t)a.R_cap, 1},
                                 {(uint64_t)a.N * 2, (uint64_t)a.N * 2 * a.R_cap}, {32, 32, 1}, 64);
     if (!ok)
@@ -114,7 +113,7 @@ template <int kCtas, int kPairs = 1> cudaError_t gemm(const LaunchCtx &c, const 
     p.m_scale = a.w_row;
     p.n_scale = a.x_row;
     p.status = a.status;
-    p.R_cap = a.R_cap;
+    p.R_cap = a.offsets ? (int)(128 * blocks) : a.R_cap;
     p.E = a.E;
     p.M = p.N = a.N;
     p.K = a.K;

@@ -165,6 +165,19 @@ def test_rows_past_the_capacity():
     assert torch.equal(guard[:cut], want[3][:cut]) and (guard[cut:] == 7.0).all()
 
 
+def test_nvfp4_capacity_below_a_slot():
+    """Fewer rows than a tile hold no slot: one that is there all the same is past
+    the capacity, and nothing is written."""
+    g = gen(34)
+    rows = tg.pack_rows(randn(g, 100, 64))
+    wo = nq.ep_nvfp4_operand(nq.ep_nvfp4_pack_weights(randn(g, 2, 16, 64).to(torch.bfloat16)), 64)
+    for offsets, want in (([0, 0, 0], 0), ([0, 128, 128], nq.EP_DEV_ERR_CAPACITY)):
+        out = torch.full((100, 16), 7.0, dtype=torch.bfloat16, device="cuda")
+        status = nq.new_status("cuda")
+        nq.ep_nvfp4_grouped_gemm(nq.ep_nvfp4_operand(rows, 64), wo, ints(offsets), out=out, status=status)
+        assert int(status) == want and (out == 7.0).all()
+
+
 def test_counts_beyond_the_slot_and_below_zero():
     g = gen(25)
     offsets, off, R_cap, live = slots([128, 256, 128])
