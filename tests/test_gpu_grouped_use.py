@@ -413,3 +413,89 @@ def test_large_products_of_packed_rows(n, k):
             at = slice(off[e], off[e + 1])
             want, mag = tg.nvfp4_reference(rows[at], w[e], k)
             within(out[at], want, sum_bound(k, mag, want, torch.bfloat16, more=2))
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(40, 256, 128, 4, 2), (3000, 1024, 512, 16, 4)])
+def test_chain_in_a_graph_without_anything_between(T, H, I, E, k):
+    """Plan, pack, products, activation and combine and their gradients one after
+    another in a captured graph, each launch let in while the one before ends;
+    replayed with other tokens and routing, twice in a row."""
+    g = gen(35)
+    w1, w2 = ((torch.randn(*s, generator=g, device="cuda") / s[-1] ** 0.5).to(torch.bfloat16)
+              for s in ((E, 2 * I, H), (E, H, I)))
+    w1o, w2o = (nq.ep_nvfp4_operand(nq.ep_nvfp4_pack_weights(w), w.shape[2]) for w in (w1, w2))
+    R_cap = nq.rows_capacity(T, k, E)
+    x, d_out = (torch.zeros(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    topk, weights = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")
+    status, ws = nq.new_status("cuda"), nq.new_route_workspace(T, k, E, "cuda")
+    new = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")   # noqa: E731
+    plan = nq.RoutePlan(new(E + 1, dt=torch.int32), new(E, dt=torch.int32), new(T * k, dt=torch.int32), T, k, E, 128,
+                        R_cap, status)
+    b = dict(rows=new(R_cap, H), h=new(R_cap, 2 * I), act=new(R_cap, I), y=new(R_cap, H), out=new(T, H),
+             packed=new(R_cap, nq.row_bytes(H), dt=torch.uint8), h4=new(R_cap, 2 * I), d_y=new(R_cap, H),
+             d_act=new(R_cap, I), d_w=new(E, H, I, dt=torch.float32), amax=new(E, dt=torch.float32),
+             ckpt=new(nq.swiglu_checkpoint_bytes(R_cap, I), dt=torch.uint8), d_wt=new(T, k, dt=torch.float32),
+             scales=new(nq.nvfp4_scale_bytes(R_cap, H), dt=torch.uint8), row_scale=new(R_cap, dt=torch.float32))
+    ops = nq.alloc_grouped(R_cap, H, E, "cuda")
+    d_w4 = new(E, H, H, dt=torch.float32)
+
+    def step():
+        at = plan.offsets
+        nq.ep_route_plan(topk, E, plan=plan, workspace=ws)
+        nq.ep_pack(x, plan, rows=b["rows"])
+        nq.ep_grouped_gemm(b["rows"], w1, at, out=b["h"], status=status)
+        nq.ep_swiglu(b["h"], at, E, act=b["act"], ckpt=b["ckpt"], status=status)
+        nq.ep_grouped_gemm(b["act"], w2, at, out=b["y"], status=status)
+        nq.ep_combine(b["y"], plan, weights, out=b["out"])
+        nq.ep_combine_backward(d_out, plan, weights, rows=b["y"], d_rows=b["d_y"], d_weights=b["d_wt"])
+        nq.ep_grouped_gemm(b["d_y"], w2, at, transpose=True, out=b["d_act"], status=status)
+        nq.ep_grouped_wgrad(b["d_y"], b["act"], at, E, counts=plan.counts, d_w=b["d_w"], status=status)
+        nq.ep_nvfp4_dispatch(x, topk, E, plan=plan, workspace=ws, rows=b["packed"], expert_amax=b["amax"])
+        nq.ep_nvfp4_direct_receive(b["packed"], H, at, E, out=ops, swizzled=True, expert_amax=b["amax"], status=status)
+        nq.ep_nvfp4_grouped_gemm(ops, w1o, at, out=b["h4"], status=status)
+        nq.ep_nvfp4_grouped_wgrad(ops, ops, H, H, at, E, d_w=d_w4, status=status)
+        op = nq.ep_nvfp4_operand(b["packed"], H, at, E, scales=b["scales"], row_scale=b["row_scale"], status=status)
+        nq.ep_nvfp4_grouped_gemm(op, w1o, at, out=b["h"], status=status)
+
+    def fill(seed):
+        h = gen(seed)
+        x.copy_(torch.randn(T, H, generator=h, device="cuda"))
+        d_out.copy_(torch.randn(T, H, generator=h, device="cuda"))
+        score, ids = torch.rand(T, E, generator=h, device="cuda").topk(k, dim=1)
+        topk.copy_(ids)
+        weights.copy_(score)
+
+    fill(0)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    kept = dict(b, d_w4=d_w4)
+    for seed in (1, 2, 3):
+        fill(seed)
+        for t in kept.values():
+            t.zero_()
+        graph.replay()
+        graph.replay()
+        got = {n: t.clone() for n, t in kept.items()}
+        for t in kept.values():
+            t.zero_()
+        step_alone(step)
+        R = int(plan.offsets[-1])
+        for n, t in kept.items():
+            rows = n in ("rows", "h", "act", "y", "packed", "h4", "d_y", "d_act", "row_scale")
+            assert torch.equal(got[n][:R] if rows else got[n], t[:R] if rows else t), n
+    assert int(status) == 0
+
+
+def step_alone(step):
+    """The same calls, each alone on the GPU."""
+    waiting = {n: getattr(nq, n) for n in dir(nq) if n.startswith("ep_")}
+    try:
+        for n, f in waiting.items():
+            setattr(nq, n, lambda *a, _f=f, **kw: (_f(*a, **kw), torch.cuda.synchronize())[0])
+        step()
+    finally:
+        for n, f in waiting.items():
+            setattr(nq, n, f)
