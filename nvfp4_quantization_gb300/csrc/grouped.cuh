@@ -51,7 +51,10 @@
 //    start on lines, and BF16 ones, lose 3 to 5 %.
 //  - eight warps for the epilogue, one piece of output each: with two pieces a
 //    warp, and so a stage less, the weight gradients took 5 to 9 % longer.
-//  - measured and dropped: hints to L2 for what is written or read (no change);
+//  - measured and dropped: tiles of 128 columns for pairs with short slots, with
+//    more stages (128 tokens, 8 of 64 experts of 4096 x 4096: BF16 354 -> 344 us,
+//    NVFP4 no change; 56.5 -> 59.4 us where a few slots are longer); hints to L2
+//    for what is written or read, and other sizes of its fetches (no change);
 //    block scales copied as 64-bit words in one piece (no change); a register
 //    split between the warps (the epilogue spilled more, not less).
 #pragma once
