@@ -45,10 +45,6 @@
 //    which are emptied first and waited for only where both tiles use them
 //    (1021 tokens, 5 of 61 experts of 2056 x 1056: 31.9 -> 28.7 us with the next
 //    step).
-//  - clusters of two pairs that share the N side, each copying half of it for
-//    both (NVFP4 products of packed rows): 15.6 -> 13.4 us a tile of a pair; but
-//    clusters of four CTAs reach only 144 of 152 SMs, so that products whose rows
-//    start on lines, and BF16 ones, lose 3 to 5 %.
 //  - eight warps for the epilogue, one piece of output each: with two pieces a
 //    warp, and so a stage less, the weight gradients took 5 to 9 % longer.
 //  - measured and dropped: tiles of 128 columns for pairs with short slots, with
@@ -85,14 +81,13 @@ struct GroupedParams {
     int add;                         // rows as K, FP32: add to d_w
 };
 
-template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_, int kPairs_ = 1> struct GroupedCfg {
+template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_> struct GroupedCfg {
     static constexpr bool kFp4 = kFp4_, kWgrad = kWgrad_, kF32 = kF32_;
     static constexpr int kCtas = kCtas_;                      // that compute a tile: one or a pair
-    static constexpr int kPairs = kPairs_;                    // pairs of a cluster, with the same N side
     // columns of a tile: where single CTAs take a product, slots are short and
     // stages in flight count
     static constexpr int kTileN = kCtas == 1 && !kWgrad ? 128 : 256;
-    static constexpr int kCluster = kCtas * kPairs, kSpan = 128 * kCluster;
+    static constexpr int kSpan = 128 * kCtas;                 // of the M side
     static constexpr bool kAmn = kAmn_;                       // A with its M side contiguous (BF16)
     static constexpr bool kRows = kFp4 && kWgrad;             // copied in pieces, not by TMA
     static constexpr int kThreads = kRows ? 32 * (kWarpRows + kRowWarps) : 352;
@@ -323,13 +318,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
     int *const start = partial + C::kThreads / 32;               // [(E + 1) / 2 + 1]
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t crank = kCtas == 2 ? cluster_rank() : 0, rank = crank & 1, pair = crank >> 1;
-    const int unit = (int)blockIdx.x / C::kCluster, units = (int)gridDim.x / C::kCluster;
+    const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
+    const int unit = (int)blockIdx.x / kCtas, units = (int)gridDim.x / kCtas;
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bar.full[s], kCtas);
-            mbar_init(&bar.empty[s], C::kPairs);
+            mbar_init(&bar.empty[s], 1);
             mbar_init(&bar.tail[s], C::kRows ? 32 * kRowWarps : 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -352,7 +347,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
     const uint32_t tmem = bar.tmem;
     const int tiles = start[(p.E + 1) >> 1];
     // barriers that the products wait on: the leader's
-    auto at_leader = [&](uint64_t *b) { return kCtas == 2 ? at_rank(smem_u32(b), crank - rank) : smem_u32(b); };
+    auto at_leader = [&](uint64_t *b) { return kCtas == 2 ? at_rank(smem_u32(b), 0) : smem_u32(b); };
     const uint32_t full0 = at_leader(&bar.full[0]);
     bool ok = true;
     GroupedWalk<C> walk(p, start, unit, units);
@@ -384,7 +379,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
             // M and N are multiples of 128 here, so a tile's rows on either side are
             // there or not as a whole.  What is not there is not copied and not used:
             // lanes past M are not stored, steps past a row's end are not made.
-            const int half = o.n / kCtas, m = o.m0 + 128 * (int)crank, n = o.n0 + half * (int)rank;
+            const int half = o.n / kCtas, m = o.m0 + 128 * (int)rank, n = o.n0 + half * (int)rank;
             const bool have_a = m < p.M;
             const int64_t pitch = o.rows / 2, blocks = (int64_t)o.rows * 8;    // bytes of a row, of 128 rows' scales
             const int64_t pitch16 = 16 * pitch;
@@ -441,7 +436,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
             const int half = ((o.n + 63) / 64 * 64) / kCtas;              // of the N side: this CTA's
             const uint32_t bytes = C::kABytes + C::kSaBytes + C::kSbBytes + (half + 63) / 64 * 8192;
             const bool has_cut = C::kBmn && p.counts && o.rows % C::kBlockK;
-            const int m = o.m0 + 128 * (int)crank, n = o.n0 + half * (int)rank;
+            const int m = o.m0 + 128 * (int)rank, n = o.n0 + half * (int)rank;
             for (int kb = 0; kb < o.kb; ++kb) {
                 if (used >= kStages &&
                     !__all_sync(0xffffffffu, mbar_wait_for(&bar.empty[at.s], at.phase ^ 1, kWaitNs))) {
@@ -456,12 +451,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
                     const uint32_t a = ring + at.s * C::kStageBytes, b = a + C::kABytes;
                     const int k0 = kb * C::kBlockK;
                     mbar_arrive_expect_tx_at(f, bytes);
-                    // the N side: a box of 64 at a time, each by one of the pairs for all
+                    // the N side: a box of 64 at a time
                     auto load_b = [&](int i, int x, int y) {
-                        if constexpr (C::kPairs == 1)
-                            tma_load_3d<kCtas>(b + i * 128, p.map + kMapB, x, y, 0, f);
-                        else if (((uint32_t)(i / 64) & 1) == pair)
-                            tma_load_3d_multicast(b + i * 128, p.map + kMapB, x, y, 0, f, 5u << rank);
+                        tma_load_3d<kCtas>(b + i * 128, p.map + kMapB, x, y, 0, f);
                     };
                     if constexpr (C::kFp4) {
                         const int x = k0 / 2, ys = k0 / 16;               // bytes; pieces of 128 bytes of scales
@@ -569,10 +561,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
                                 mma_bf16<kCtas>(d, da + ja * j, db + jb * j, idesc, add || j > 0);
                     }
                     add = true;
-                    mma_commit<kCtas>(smem_u32(&bar.empty[at.s]), (1u << C::kCluster) - 1);
+                    mma_commit<kCtas>(smem_u32(&bar.empty[at.s]));
                     at.step();
                     if (kb == o.kb - 1 || (C::kParts && (kb + 1) % C::kPartBlocks == 0))
-                        mma_commit<kCtas>(smem_u32(&bar.acc_full[b]), 3u << crank);
+                        mma_commit<kCtas>(smem_u32(&bar.acc_full[b]));
                 }
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -614,7 +606,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
             const GroupedTile o = walk.tile();
             if (o.kb == 0 && p.add)
                 continue;
-            const int m = o.m0 + 128 * (int)crank + 32 * w;      // first of this warp's 32 rows of the M side
+            const int m = o.m0 + 128 * (int)rank + 32 * w;      // first of this warp's 32 rows of the M side
             const int nch = (o.n + C::kChunk - 1) / C::kChunk;
             const int parts = C::kParts ? (o.kb + C::kPartBlocks - 1) / C::kPartBlocks : 1;
             // with overlapping accumulators the shared columns come first: the end
@@ -795,7 +787,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------- launch
-// Clusters of this kernel that are resident at once.
+// CTAs or pairs of this kernel that are resident at once.
 template <class C> cudaError_t grouped_units(const LaunchCtx &c, int &units)
 {
     static std::atomic<int> known[64];
@@ -813,9 +805,9 @@ template <class C> cudaError_t grouped_units(const LaunchCtx &c, int &units)
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = C::kCluster;
+    attr[0].val.clusterDim.x = C::kCtas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(c.num_sms / C::kCluster * C::kCluster));
+    cfg.gridDim = dim3((unsigned)(c.num_sms / C::kCtas * C::kCtas));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
@@ -860,9 +852,9 @@ template <class C> cudaError_t launch_grouped(const LaunchCtx &c, const GroupedP
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C::kCluster;
+    attr[1].val.clusterDim.x = C::kCtas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(units * C::kCluster));
+    cfg.gridDim = dim3((unsigned)(units * C::kCtas));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = grouped_smem_bytes<C>();
     cfg.stream = c.stream;

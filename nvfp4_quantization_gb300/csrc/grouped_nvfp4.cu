@@ -93,9 +93,9 @@ bool scale_map(CUtensorMap *m, const void *p, int64_t tiles, int64_t count, int 
                        {128, 16, (uint32_t)blocks}, 0);
 }
 
-template <int kCtas, int kPairs = 1> cudaError_t gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a)
+template <int kCtas> cudaError_t gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a)
 {
-    using C = GroupedCfg<true, false, false, kCtas, false, kPairs>;
+    using C = GroupedCfg<true, false, false, kCtas, false>;
     GroupedParams p = {};
     const int64_t kt = ceil_div(a.K, 64);
     // slots are whole blocks of 128 rows, so that rows past the last whole block are
@@ -118,27 +118,6 @@ template <int kCtas, int kPairs = 1> cudaError_t gemm(const LaunchCtx &c, const 
     p.M = p.N = a.N;
     p.K = a.K;
     return launch_grouped<C>(c, p, ceil_div(a.N, C::kSpan) * (ceil_div(a.R_cap, C::kTileN) + a.E));
-}
-
-// Whether clusters of two pairs take the product: where rows straddle lines of
-// 128 bytes (packed rows mostly do), tiles are whole (256 rows an expert and its
-// padding) and the rounds do not eat up what a tile gains.  Measured on GB300, a
-// cluster's tile of 512 x 256 against a pair's of 256 x 256: 13.4 us against 15.6
-// (8192^3, 202 us against 219); rows on lines 12.6 against 13.0, which the SMs out
-// of clusters' reach outweigh (190 us against 182); 128 rows an expert 124 us
-// against 121 (128 tokens, 8 of 64 experts of 4096 x 4096).
-bool shared_n_side(const LaunchCtx &c, const Nvfp4GemmArgs &a)
-{
-    const bool lines = ((a.ld_w | a.ld_x | (int64_t)(uintptr_t)a.w | (int64_t)(uintptr_t)a.x) & 127) == 0;
-    if (lines || a.R_cap < 384 * (int64_t)a.E)
-        return false;
-    using Pair = GroupedCfg<true, false, false, 2, false>;
-    using Cluster = GroupedCfg<true, false, false, 2, false, 2>;
-    int pairs = 0, clusters = 0;
-    if (grouped_units<Pair>(c, pairs) != cudaSuccess || grouped_units<Cluster>(c, clusters) != cudaSuccess)
-        return false;
-    const int64_t n = ceil_div(a.R_cap, Pair::kTileN);
-    return 86 * ceil_div(ceil_div(a.N, Cluster::kSpan) * n, clusters) < 100 * ceil_div(ceil_div(a.N, Pair::kSpan) * n, pairs);
 }
 
 template <bool kF32, int kCtas> cudaError_t wgrad(const LaunchCtx &c, const Nvfp4WgradArgs &a)
@@ -181,8 +160,6 @@ cudaError_t launch_nvfp4_gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a)
     using One = GroupedCfg<true, false, false, 1, false>;
     if (single_ctas<One>(c, a.N, ceil_div(a.R_cap, One::kTileN)))
         return gemm<1>(c, a);
-    if (shared_n_side(c, a))
-        return gemm<2, 2>(c, a);
     return gemm<2>(c, a);
 }
 

@@ -125,16 +125,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
                      : "memory");
 }
 
-// The same into the CTAs of `mask` at once (pairs of a cluster; to the same place
-// in each), counted in each of their pairs on the barrier at the place of `bar`.
-__device__ __forceinline__ void tma_load_3d_multicast(uint32_t dst, const CUtensorMap *m, int x, int y, int z,
-                                                      uint32_t bar, uint32_t mask)
-{
-    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 ".multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst), "l"((uint64_t)m), "r"(x), "r"(y),
-                 "r"(z), "r"(bar), "h"((uint16_t)mask) : "memory");
-}
-
 // 3-D tiled store; with kAdd an FP32 addition to what is there.
 template <bool kAdd>
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int x, int y, int z, uint32_t src)
@@ -283,14 +273,14 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc)
         asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// `bar` (with pairs: at the same place in the CTAs of `mask`) completes an
-// arrival when this thread's products and copies so far are done.
+// `bar` (of a pair: at the same place in both CTAs) completes an arrival when
+// this thread's products and copies so far are done.
 template <int kCtas>
-__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t mask)
+__device__ __forceinline__ void mma_commit(uint32_t bar)
 {
     if constexpr (kCtas == 2)
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                     ::"r"(bar), "h"((uint16_t)mask) : "memory");
+                     ::"r"(bar), "h"((uint16_t)3) : "memory");
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                      : "memory");
