@@ -16,8 +16,8 @@
 //
 // The columnwise NVFP4 operands are a matrix of its own for every expert, whose
 // pitch only the device knows, so no tensor map of the host's fits them.  There
-// warps 12-15 copy the rows in 16-byte pieces, and warp 8 passes the arrival of
-// a stage on to the matrix products.
+// warps 12-15 copy the rows in 16-byte pieces, and warp 8 (in a pair's second
+// CTA warps 8-10 in turn) passes the arrival of a stage on to the matrix products.
 //
 // What bounds it.  Large BF16 products: the tensor cores (busy 97 % of the time
 // on 8192 x 8192 x 4096), and with them the card's power: 8192^3 runs at 1.94
@@ -63,6 +63,13 @@ namespace epq {
 constexpr int kGroupTiles = 8;       // tiles of the N side that share the M side's tiles in L2
 constexpr int kOutWarps = 8;         // two to a quarter of the accumulator's lanes
 constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpCut = 10, kWarpRows = 12, kRowWarps = 4;
+// Warps of a pair's second CTA that pass on what its threads copied (from
+// kWarpCopy on; the products and cut blocks of that CTA are not theirs).  Their
+// arrivals release at cluster scope, which takes longer than a stage: one warp
+// held the NVFP4 weight gradient of 98304 rows (64 experts of 2048 x 4096) at 642
+// us and that of 65536 (8 of 4096 x 4096) at 697, two 541 and 504, three 539 and
+// 498, four 539 and 496.
+constexpr int kPassers = 3;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 enum { kMapA = 0, kMapB = 1, kMapSa = 2, kMapSb = 3 };
@@ -349,23 +356,36 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
     // barriers that the products wait on: the leader's
     auto at_leader = [&](uint64_t *b) { return kCtas == 2 ? at_rank(smem_u32(b), 0) : smem_u32(b); };
     const uint32_t full0 = at_leader(&bar.full[0]);
+    // after writes to this CTA's stage s by threads
+    auto arrive_at_leader = [&](uint32_t s) {
+        if (rank == 0)
+            mbar_arrive(&bar.full[s]);
+        else
+            mbar_arrive_release_at(full0 + 8 * s);
+    };
     bool ok = true;
     GroupedWalk<C> walk(p, start, unit, units);
 
-    if (C::kRows && warp == kWarpCopy) {
+    if (C::kRows && warp >= kWarpCopy && warp < kWarpCopy + (rank == 0 ? 1 : kPassers)) {
         // ------------------------------------------------------------ arrivals
-        // what the other threads copied, ordered before the matrix unit's reads
+        // what the other threads copied, ordered before the matrix unit's reads;
+        // each passing warp has every `passers`-th stage
+        const int passers = rank == 0 ? 1 : kPassers, first = warp - kWarpCopy;
         GroupedRing<kStages> at;
+        int turn = 0;
         for (int t = unit; t < tiles && ok; t += units) {
             const GroupedTile o = walk.tile();
             for (int kb = 0; kb < o.kb; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait_for(&bar.tail[at.s], at.phase, kWaitNs));
-                if (!ok)
-                    break;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_release_at(full0 + 8 * at.s);
+                if (turn == first) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_for(&bar.tail[at.s], at.phase, kWaitNs));
+                    if (!ok)
+                        break;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        arrive_at_leader(at.s);
+                }
+                turn = turn + 1 == passers ? 0 : turn + 1;
                 at.step();
             }
         }
@@ -529,7 +549,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
                         ++acc_it;
                         tmem_fence_after();
                     }
-                    ok = mbar_wait_for(&bar.full[at.s], at.phase, kWaitNs);
+                    // a stage that threads wrote, in a pair those of both CTAs
+                    const bool threads = kCtas == 2 && (C::kRows || (C::kBmn && p.counts && kb == o.kb - 1));
+                    ok = threads ? mbar_wait_for<true>(&bar.full[at.s], at.phase, kWaitNs)
+                                 : mbar_wait_for(&bar.full[at.s], at.phase, kWaitNs);
                     if (!ok)
                         break;
                     tmem_fence_after();
@@ -593,7 +616,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_release_at(full0 + 8 * s);
+                arrive_at_leader(s);
         }
     } else if (warp < kOutWarps) {
         // ------------------------------------------------------------ sums

@@ -46,15 +46,30 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
+// mbar_try_wait that also sees what threads of the cluster's other CTAs ordered
+// before their arrivals.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // Wait on a phase of an mbarrier, for limit_ns at most; false if it gave up.
+// kCluster: for arrivals that threads of another CTA make after writes of theirs.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
 {
+    auto done = [&]() { return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
     for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity))
+        if (done())
             return true;
     const uint64_t t0 = now_ns();
     while (now_ns() - t0 < limit_ns)
-        if (mbar_try_wait(bar, parity))
+        if (done())
             return true;
     return false;
 }
@@ -86,16 +101,13 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank)
     return r;
 }
 
-// Arrivals on a barrier of any CTA of the cluster.  The first orders the CTA's
-// earlier writes to its own shared memory before it (they are read there, by
-// the CTA's own part of the matrix unit, so the CTA's scope is enough).  The
-// others order none: a release at cluster scope waits for the thread's earlier
-// copies to be on their way.  With one a stage (and waits at that scope) the BF16
-// products ran at 0.4 of their rate, and the NVFP4 weight gradient, with one by a
-// thread that copies nothing, took 652 us instead of 510.
+// Arrivals on a barrier of any CTA of the cluster.  The first orders what this
+// thread wrote, or saw written, to shared memory before it, for a thread of
+// another CTA that waits at cluster scope: the products of a pair are issued in
+// one CTA and read the shared memory of both.  The others order none.
 __device__ __forceinline__ void mbar_arrive_release_at(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
