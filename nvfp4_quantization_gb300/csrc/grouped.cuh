@@ -592,9 +592,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
             }
             ok = __all_sync(0xffffffffu, ok);
         }
-    } else if (C::kWgrad && !C::kFp4 && warp == kWarpCut && p.counts) {
+    } else if (C::kWgrad && !C::kFp4 && (warp == kWarpCut || warp == kWarpMma) && p.counts) {
         // ------------------------------------------------------------ cut blocks
-        // rows of a slot behind the expert's tokens count as zero, whatever they hold
+        // rows of a slot behind the expert's tokens count as zero, whatever they hold;
+        // in a pair's second CTA, whose arrivals take longer, two warps take them in
+        // turn (5000 rows, 61 experts of 1000 x 2056: 72 us, with one 76)
+        const uint32_t cutters = rank == 0 ? 1 : 2, first = rank == 0 ? 0 : warp - kWarpMma;
         uint32_t it = 0, cut_it = 0;
         for (int t = unit; t < tiles && ok; t += units) {
             const GroupedTile o = walk.tile();
@@ -602,6 +605,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) grouped_kernel(const __grid_co
             it += o.kb;
             if (!rem)
                 continue;
+            if (cut_it % cutters != first) {
+                ++cut_it;
+                continue;
+            }
             const int s = (int)((it - 1) % kStages);
             ok = __all_sync(0xffffffffu,
                             mbar_wait_for(&bar.tail[cut_it % kStages], (cut_it / kStages) & 1, kWaitNs));
