@@ -158,7 +158,7 @@ __device__ __forceinline__ void st_global_32B(uint8_t *p, uint2 a, uint2 b, uint
 template <bool kSR>
 __global__ void __launch_bounds__(kCbWarps * 32, 1)
 colwise_rht_bf16_kernel(const __grid_constant__ CUtensorMap tm_x, int H, int R_cap,
-                        const int32_t *__restrict__ offsets, int E, const float *__restrict__ amax_in,
+                        const int32_t *offsets, int E, const float *amax_in,
                         uint8_t *__restrict__ cw_codes, uint8_t *__restrict__ cw_scales, float *__restrict__ amax_row,
                         float *__restrict__ amax_col, float *__restrict__ scale_enc,
                         const __grid_constant__ PhiloxKey key, uint32_t sign_mask, uint32_t *__restrict__ status,
@@ -179,13 +179,13 @@ colwise_rht_bf16_kernel(const __grid_constant__ CUtensorMap tm_x, int H, int R_c
     pdl_launch_dependents();
     pdl_wait();
     for (int i = tid; i <= E; i += blockDim.x)
-        offs[i] = __ldg(offsets + i);
+        offs[i] = ld_word(offsets + i);
     for (int i = tid; i < 128; i += blockDim.x)
         sm.rcp[i] = rcp.v[i];
     // per expert: amax_row = BF16_RNE(supplied amax), amax_col = 4 amax_row,
     // S_enc = min(2688 / amax_col, FLT_MAX) (1 when amax_col = 0)
     for (int e = tid; e < E; e += blockDim.x) {
-        const float a = round_bf16(__ldg(amax_in + e));
+        const float a = round_bf16(ld_word(amax_in + e));
         float ac;
         const float se = colwise_encode_scale(a, ac);
         se_s[e] = se;
@@ -307,7 +307,7 @@ struct __align__(128) MxSmem {
 
 template <bool kV8>
 __global__ void __launch_bounds__(kMxWarps * 32, 1)
-mxfp8_colwise_kernel(const __grid_constant__ CUtensorMap tm_x, int H, int R_cap, const int32_t *__restrict__ offsets,
+mxfp8_colwise_kernel(const __grid_constant__ CUtensorMap tm_x, int H, int R_cap, const int32_t *offsets,
                      int E, uint8_t *__restrict__ buf, uint32_t *__restrict__ status)
 {
     extern __shared__ uint8_t mx_smem_raw[];
@@ -324,7 +324,7 @@ mxfp8_colwise_kernel(const __grid_constant__ CUtensorMap tm_x, int H, int R_cap,
     pdl_launch_dependents();
     pdl_wait();
     for (int i = tid; i <= E; i += blockDim.x)
-        offs[i] = __ldg(offsets + i);
+        offs[i] = ld_word(offsets + i);
     __syncthreads();
     int R = offs[E];
     if (R > R_cap) {

@@ -54,8 +54,6 @@ __device__ __forceinline__ uint4 pack(const float (&f)[4])
     return make_uint4(f2u(f[0]), f2u(f[1]), f2u(f[2]), f2u(f[3]));
 }
 
-__device__ __forceinline__ uint4 load16(const void *p) { return __ldg(static_cast<const uint4 *>(p)); }
-
 // ---------------------------------------------------------------- rows that start anywhere
 // E elements from any element's address, as the two aligned 16-byte words that
 // hold them (the second is the neighbouring thread's first: it comes from L1)
@@ -81,17 +79,17 @@ __device__ __forceinline__ Window load_window(const T *p, bool inner, int first,
         const uintptr_t at = reinterpret_cast<uintptr_t>(p);
         w.shift = (uint32_t)at & 15u;
         const uint4 *q = reinterpret_cast<const uint4 *>(at - w.shift);
-        w.lo = __ldg(q);
-        w.hi = __ldg(q + (w.shift ? 1 : 0));
+        w.lo = ld_16bytes(q);
+        w.hi = ld_16bytes(q + (w.shift ? 1 : 0));
     } else {
         uint32_t v[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < E<T>; ++i)
             if (i >= first && i < n) {
                 if constexpr (sizeof(T) == 2)
-                    v[i / 2] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+                    v[i / 2] |= ld_half_word(p + i) << (16 * (i & 1));
                 else
-                    v[i] = f2u(__ldg(p + i));
+                    v[i] = f2u(ld_word(p + i));
             }
         w.lo = w.hi = make_uint4(v[0], v[1], v[2], v[3]);
         w.shift = 0;
@@ -171,11 +169,11 @@ __device__ __forceinline__ void read_slots(const CombineArgs &a, int64_t slot0, 
         w[j] = 1.0f;
         if (j0 + j < a.k) {
             const int64_t s = slot0 + j0 + j;
-            d[j] = a.index ? __ldg(a.index + s) : 0;
+            d[j] = a.index ? ld_word(a.index + s) : 0;
             if (a.slot_order && d[j] >= 0)
                 d[j] = (int)s;
             if (a.weights)
-                w[j] = __ldg(a.weights + s);
+                w[j] = ld_word(a.weights + s);
         }
     }
 }
@@ -208,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a)
 #pragma unroll
                 for (int u = 0; u < UNR; ++u)
                     if (c0 + u * step < a.H)
-                        raw[j][u] = load16(rows + (int64_t)d[j] * a.ld_rows + c0 + u * step);
+                        raw[j][u] = ld_16bytes(rows + (int64_t)d[j] * a.ld_rows + c0 + u * step);
             }
         }
 #pragma unroll
@@ -283,9 +281,9 @@ template <typename T, bool SHORT>
 __device__ void zero_padding(const ScatterArgs &a, int cta)
 {
     const int e = cta / a.pad_split;
-    const int end = __ldg(a.offsets + e + 1);
+    const int end = ld_word(a.offsets + e + 1);
     T *rows = static_cast<T *>(a.rows_out);
-    const int first = __ldg(a.offsets + e) + __ldg(a.counts + e) + (SHORT ? (int)threadIdx.y * a.pad_split : 0);
+    const int first = ld_word(a.offsets + e) + ld_word(a.counts + e) + (SHORT ? (int)threadIdx.y * a.pad_split : 0);
     for (int r = first + cta % a.pad_split; r < end; r += SHORT ? a.pad_split * (int)blockDim.y : a.pad_split) {
         if (r < 0 || r >= a.R_cap) {
             if (threadIdx.x == 0)
@@ -325,19 +323,19 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(ScatterArgs a)
             w[j] = 1.0f;
             dot[j] = 0.0f;
             if (here && j0 + j < a.k) {
-                d[j] = live_row(__ldg(a.dest + slot0 + j0 + j), a.R_cap, a.status);
+                d[j] = live_row(ld_word(a.dest + slot0 + j0 + j), a.R_cap, a.status);
                 if (a.weights)
-                    w[j] = __ldg(a.weights + slot0 + j0 + j);
+                    w[j] = ld_word(a.weights + slot0 + j0 + j);
             }
         }
         for (int c = here ? threadIdx.x * E<T> : a.H; c < a.H; c += blockDim.x * E<T>) {
-            const uint4 raw = load16(src + c);
+            const uint4 raw = ld_16bytes(src + c);
             uint4 in[KCH];
             if (DOT) {
 #pragma unroll
                 for (int j = 0; j < KCH; ++j)
                     if (d[j] >= 0)
-                        in[j] = load16(rows_in + (int64_t)d[j] * a.ld_in + c);
+                        in[j] = ld_16bytes(rows_in + (int64_t)d[j] * a.ld_in + c);
             }
             float f[E<T>];
             unpack(raw, f);
@@ -393,8 +391,8 @@ template <typename T>
 __device__ void zero_padding_any(const ScatterArgs &a, int cta)
 {
     const int e = cta / a.pad_split, part = cta % a.pad_split;
-    const int64_t row0 = (int64_t)__ldg(a.offsets + e) + __ldg(a.counts + e);
-    int64_t row1 = __ldg(a.offsets + e + 1);
+    const int64_t row0 = (int64_t)ld_word(a.offsets + e) + ld_word(a.counts + e);
+    int64_t row1 = ld_word(a.offsets + e + 1);
     if (row1 > a.R_cap || row0 < 0) {
         if (threadIdx.x == 0)
             raise_status(a.status, kDevErrCapacity);
@@ -440,11 +438,11 @@ __global__ void __launch_bounds__(kThreads) scatter_any_kernel(ScatterArgs a)
     }
     const int lane = threadIdx.x % L;
     const int64_t s = (int64_t)blockIdx.x * kSlots + threadIdx.x / L;
-    const int d = s < slots ? live_row(__ldg(a.dest + s), a.R_cap, a.status) : -1;
+    const int d = s < slots ? live_row(ld_word(a.dest + s), a.R_cap, a.status) : -1;
     float dot = 0.0f;
     if (d >= 0) {
         const int64_t t = s / a.k;
-        const float w = a.weights ? __ldg(a.weights + s) : 1.0f;
+        const float w = a.weights ? ld_word(a.weights + s) : 1.0f;
         const T *src = static_cast<const T *>(a.src) + t * a.ld_src;
         const T *in = DOT ? static_cast<const T *>(a.rows_in) + (int64_t)d * a.ld_in : nullptr;
         T *to = static_cast<T *>(a.rows_out) + (int64_t)d * a.H;

@@ -138,6 +138,58 @@ __device__ __forceinline__ void pdl_launch_dependents()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Loads of what an earlier kernel may have written just before.  A kernel that is
+// launched early is running while that one still writes, so its inputs do not stay
+// the same for its whole lifetime, which loads through the read-only path (__ldg,
+// ld.global.nc, and plain loads of const __restrict__ parameters) rely on, and the
+// compiler could move such a load ahead of the wait.  These stay behind it: volatile
+// statements keep their order among themselves.  They claim no other memory, since no
+// kernel writes its own inputs.
+__device__ __forceinline__ uint32_t ld_word(const uint32_t *p)
+{
+    uint32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ int ld_word(const int32_t *p)
+{
+    return (int)ld_word(reinterpret_cast<const uint32_t *>(p));
+}
+
+__device__ __forceinline__ float ld_word(const float *p)
+{
+    return u2f(ld_word(reinterpret_cast<const uint32_t *>(p)));
+}
+
+__device__ __forceinline__ uint32_t ld_half_word(const uint16_t *p)
+{
+    uint16_t v;
+    asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_byte(const uint8_t *p)
+{
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint2 ld_8bytes(const void *p)
+{
+    uint2 v;
+    asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint4 ld_16bytes(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // ---------------------------------------------------------------- gpu-scope loads
 __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t *p)
 {
@@ -164,12 +216,12 @@ __device__ __forceinline__ void red_max_nonneg(float *p, float v)
 
 // The expert whose slot holds row d: the last e with offsets[e] <= d (empty
 // slots before it share its offset and are skipped by taking the last).
-__device__ __forceinline__ int expert_of_dest(const int32_t *__restrict__ offsets, int E, int d)
+__device__ __forceinline__ int expert_of_dest(const int32_t *offsets, int E, int d)
 {
     int lo = 0, hi = E - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(offsets + mid) <= d)
+        if (ld_word(offsets + mid) <= d)
             lo = mid;
         else
             hi = mid - 1;

@@ -263,7 +263,7 @@ constexpr int kMaxSmem = 227 * 1024 - (int)sizeof(Shared);
 // Expert of a slot as the caller gave it, with ids outside [-1, E) as -2.
 __device__ __forceinline__ int read_id(const MatvecArgs &a, int s)
 {
-    const int e = a.topk ? __ldg(a.topk + s) : 0;
+    const int e = a.topk ? ld_word(a.topk + s) : 0;
     return e >= a.E || e < -1 ? -2 : e;
 }
 
@@ -535,7 +535,7 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, 
         for (int i = 0; i < kKeep; ++i) {
             kept[i] = make_uint4(0, 0, 0, 0);
             if (i * kSpan < nq && q0 + i * kSpan < nq)
-                kept[i] = __ldg(x + q0 + i * kSpan);
+                kept[i] = ld_16bytes(x + q0 + i * kSpan);
         }
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
@@ -544,7 +544,7 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, 
             top = finite_absmax(top, kept[i]);
         }
         for (int q = q0 + kKeep * kSpan; q < nq; q += kSpan)
-            top = finite_absmax(top, __ldg(x + q));
+            top = finite_absmax(top, ld_16bytes(x + q));
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if (l == 0 && top)
@@ -564,7 +564,7 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, Shared &sh, int m, 
         }
         if (!once)
             for (int q = q0 + kKeep * kSpan; q < halves * 32; q += kSpan)
-                put(q, q < nq ? __ldg(x + q) : make_uint4(0, 0, 0, 0));
+                put(q, q < nq ? ld_16bytes(x + q) : make_uint4(0, 0, 0, 0));
     }
 }
 
@@ -691,8 +691,8 @@ matvec_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_consta
             turn = (turn + 1) & (parts - 1);
             float row_lo = 0.0f, row_hi = 0.0f;
             if (adds) {
-                row_lo = __ldg(reinterpret_cast<const float *>(w + (int64_t)min(row, a.N - 1) * a.S));
-                row_hi = __ldg(reinterpret_cast<const float *>(w + (int64_t)min(row + 8, a.N - 1) * a.S));
+                row_lo = ld_word(reinterpret_cast<const float *>(w + (int64_t)min(row, a.N - 1) * a.S));
+                row_hi = ld_word(reinterpret_cast<const float *>(w + (int64_t)min(row + 8, a.N - 1) * a.S));
             }
             uint32_t x = x_lane + (uint32_t)(part * HALVES * 32 * G * 16);
             float acc[2][4] = {};

@@ -27,7 +27,7 @@ constexpr int kMaxThreads = 256;
 __device__ __forceinline__ uint4 ld_stream16(const void *p)
 {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
@@ -245,11 +245,11 @@ __device__ __forceinline__ void load_token(uint32_t (&w)[CPT][16], const uint8_t
 // loads are in flight during the encode and the stores.  CTAs from n_tok_ctas on write the padding rows.
 template <int CPT, bool kSR>
 __global__ void __launch_bounds__(kMaxThreads)
-nvfp4_pack_kernel(const uint16_t *__restrict__ tokens, int T, int H, const int32_t *__restrict__ dest,
-                  int k, const int32_t *__restrict__ offsets, const int32_t *__restrict__ counts, int E,
+nvfp4_pack_kernel(const uint16_t *tokens, int T, int H, const int32_t *dest,
+                  int k, const int32_t *offsets, const int32_t *counts, int E,
                   uint8_t *__restrict__ rows, int64_t S, int R_cap, const __grid_constant__ PhiloxKey key,
                   uint32_t *__restrict__ status, int n_tok_ctas, int pad_ctas,
-                  const __grid_constant__ RcpTable rcp, const int32_t *__restrict__ topk,
+                  const __grid_constant__ RcpTable rcp, const int32_t *topk,
                   float *__restrict__ expert_amax)
 {
     __shared__ uint32_t wmax[2][kMaxThreads / 32];
@@ -330,7 +330,7 @@ nvfp4_pack_kernel(const uint16_t *__restrict__ tokens, int T, int H, const int32
         }
 
         for (int j = 0; j < k; ++j) {
-            const int d = __ldg(dest + (int64_t)t * k + j);
+            const int d = ld_word(dest + (int64_t)t * k + j);
             if (d < 0)
                 continue;
             if (d >= R_cap) {
@@ -356,9 +356,9 @@ nvfp4_pack_kernel(const uint16_t *__restrict__ tokens, int T, int H, const int32
         }
         // thread j: slot j's expert takes A_t into its max
         if (expert_amax && (int)threadIdx.x < k) {
-            const int d = __ldg(dest + (int64_t)t * k + threadIdx.x);
+            const int d = ld_word(dest + (int64_t)t * k + threadIdx.x);
             if (d >= 0 && d < R_cap) {
-                const int e = topk ? __ldg(topk + (int64_t)t * k + threadIdx.x) : expert_of_dest(offsets, E, d);
+                const int e = topk ? ld_word(topk + (int64_t)t * k + threadIdx.x) : expert_of_dest(offsets, E, d);
                 if (e >= 0 && e < E)
                     red_max_nonneg(expert_amax + e, u2f(a_bits << 16));
             }
@@ -439,11 +439,11 @@ constexpr int kBuf = 1;
 
 template <int NB, bool kSR>
 __global__ void __launch_bounds__(32 * kPackWarps)
-nvfp4_pack_warp_kernel(const uint16_t *__restrict__ tokens, int T, int H, const int32_t *__restrict__ dest,
-                       int k, const int32_t *__restrict__ offsets, const int32_t *__restrict__ counts, int E,
+nvfp4_pack_warp_kernel(const uint16_t *tokens, int T, int H, const int32_t *dest,
+                       int k, const int32_t *offsets, const int32_t *counts, int E,
                        uint8_t *__restrict__ rows, int64_t S, int R_cap, const __grid_constant__ PhiloxKey key,
                        uint32_t *__restrict__ status, int n_tok_ctas, int pad_ctas,
-                       const __grid_constant__ RcpTable rcp, int early, const int32_t *__restrict__ topk,
+                       const __grid_constant__ RcpTable rcp, int early, const int32_t *topk,
                        float *__restrict__ expert_amax)
 {
     extern __shared__ __align__(128) uint8_t pbuf[];   // [kPackWarps][kBuf][2H]
@@ -525,7 +525,7 @@ nvfp4_pack_warp_kernel(const uint16_t *__restrict__ tokens, int T, int H, const 
             w[q][4] = v1.x; w[q][5] = v1.y; w[q][6] = v1.z; w[q][7] = v1.w;
         }
         // (the first token's destinations, under `early`, only after the wait)
-        int dl = (lane < k && (i > 0 || !early)) ? __ldg(dest + (int64_t)t * k + lane) : -1;
+        int dl = (lane < k && (i > 0 || !early)) ? ld_word(dest + (int64_t)t * k + lane) : -1;
         uint32_t bm[NB];
         uint32_t amax = 0;
 #pragma unroll
@@ -555,7 +555,7 @@ nvfp4_pack_warp_kernel(const uint16_t *__restrict__ tokens, int T, int H, const 
         if (i == 0 && early) {
             pdl_wait();
             if (lane < k)
-                dl = __ldg(dest + (int64_t)t * k + lane);
+                dl = ld_word(dest + (int64_t)t * k + lane);
         }
         for (int j = 0; j < k; ++j) {
             const int d = __shfl_sync(0xffffffffu, dl, j);
@@ -582,7 +582,7 @@ nvfp4_pack_warp_kernel(const uint16_t *__restrict__ tokens, int T, int H, const 
         // the expert of each written row takes the token amax A_t into its max
         // (lane j: slot j; the routing plan zeroed the array, or the caller did)
         if (expert_amax && lane < k && dl >= 0 && dl < R_cap) {
-            const int e = topk ? __ldg(topk + (int64_t)t * k + lane) : expert_of_dest(offsets, E, dl);
+            const int e = topk ? ld_word(topk + (int64_t)t * k + lane) : expert_of_dest(offsets, E, dl);
             if (e >= 0 && e < E)
                 red_max_nonneg(expert_amax + e, u2f(a_bits << 16));
         }
@@ -650,8 +650,8 @@ __device__ __forceinline__ void mxfp8_store_block(const uint32_t (&o)[8], uint32
 
 // MXFP8 pack, one CTA per token (H / 32 > kMaxThreads: several blocks per thread).
 __global__ void __launch_bounds__(kMaxThreads)
-mxfp8_pack_kernel(const uint16_t *__restrict__ tokens, int T, int H, const int32_t *__restrict__ dest,
-                  int k, const int32_t *__restrict__ offsets, const int32_t *__restrict__ counts, int E,
+mxfp8_pack_kernel(const uint16_t *tokens, int T, int H, const int32_t *dest,
+                  int k, const int32_t *offsets, const int32_t *counts, int E,
                   uint8_t *__restrict__ buf, int R_cap, uint32_t *__restrict__ status, int pad_ctas,
                   int cpt)
 {
@@ -690,8 +690,8 @@ mxfp8_pack_kernel(const uint16_t *__restrict__ tokens, int T, int H, const int32
 // (and reading its destinations) before it encodes and stores the current one;
 // CTAs past the token CTAs write the padding rows.
 __global__ void __launch_bounds__(kMaxThreads)
-mxfp8_pack_persistent_kernel(const uint16_t *__restrict__ tokens, int T, int H, const int32_t *__restrict__ dest,
-                             int k, const int32_t *__restrict__ offsets, const int32_t *__restrict__ counts, int E,
+mxfp8_pack_persistent_kernel(const uint16_t *tokens, int T, int H, const int32_t *dest,
+                             int k, const int32_t *offsets, const int32_t *counts, int E,
                              uint8_t *__restrict__ buf, int R_cap, uint32_t *__restrict__ status, int pad_ctas,
                              int n_tok_ctas)
 {

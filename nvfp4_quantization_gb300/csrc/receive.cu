@@ -220,7 +220,7 @@ __device__ __forceinline__ void stage_meta(Sm &sm, const DrArgs &p, int s, int r
 constexpr int kAmaxThreads = 512;
 
 __global__ void __launch_bounds__(kAmaxThreads)
-expert_amax_kernel(const uint8_t *__restrict__ rows, int64_t S, const int32_t *__restrict__ offsets, int E,
+expert_amax_kernel(const uint8_t *rows, int64_t S, const int32_t *offsets, int E,
                    int R_cap, float *__restrict__ amax_row, float *__restrict__ amax_col,
                    float *__restrict__ scale_enc)
 {
@@ -231,15 +231,15 @@ expert_amax_kernel(const uint8_t *__restrict__ rows, int64_t S, const int32_t *_
     const int tid = threadIdx.x;
     const uint8_t *amax_at = rows + S - 12;   // A_t inside each row's trailer
     for (int e = blockIdx.x; e < E; e += gridDim.x) {
-        const int off = __ldg(offsets + e);
-        const int end = min(__ldg(offsets + e + 1), R_cap);
+        const int off = ld_word(offsets + e);
+        const int end = min(ld_word(offsets + e + 1), R_cap);
         uint32_t m = 0; // non-negative floats compare as their bit patterns
         for (int r = off + tid; r < end; r += 8 * kAmaxThreads) {
             uint32_t v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int rr = r + j * kAmaxThreads;
-                v[j] = rr < end ? __ldg(reinterpret_cast<const uint32_t *>(amax_at + (int64_t)rr * S)) : 0u;
+                v[j] = rr < end ? ld_word(reinterpret_cast<const uint32_t *>(amax_at + (int64_t)rr * S)) : 0u;
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -778,8 +778,9 @@ direct_receive_kernel(const __grid_constant__ CUtensorMap tm_codes,
     // amax kernel (only S_enc comes from it), and even before the expert
     // offsets are read: tile 0 of this CTA is loaded if it lies inside the
     // row capacity, and dropped unused if it lies past the rows in use.
-    // With the amax supplied (p.amax_in) the grid before this one is the pack
-    // itself, and no row may be read before the wait on it.
+    // With the amax supplied (p.amax_in) the grid before this one may be any,
+    // also one that started early itself while the routing plan was still being
+    // made: neither rows nor offsets are read before the wait.
     // The other stages' tiles are issued by lane 0 of warps 1 .. kStages - 1,
     // one each, as soon as their rows may be read: the issue of a tile's
     // three boxes holds its thread for a while, and done by thread 0 after
@@ -793,9 +794,14 @@ direct_receive_kernel(const __grid_constant__ CUtensorMap tm_codes,
         issue_tile(sm, &tm_codes, &tm_scales, &tm_trailer, 0, rt0, st0);
     __syncthreads();
     pdl_launch_dependents();
+    if (p.amax_in) {
+        pdl_wait();
+        if (threadIdx.x == 0 && pre)
+            issue_tile(sm, &tm_codes, &tm_scales, &tm_trailer, 0, rt0, st0);
+    }
 
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x)
-        smem_offs(sm)[i] = __ldg(p.offsets + i);
+        smem_offs(sm)[i] = ld_word(p.offsets + i);
     for (int i = threadIdx.x; i < 128; i += blockDim.x)
         sm.rcp[i] = p.rcp[i];
     __syncthreads();
@@ -810,14 +816,9 @@ direct_receive_kernel(const __grid_constant__ CUtensorMap tm_codes,
     const int wn = (int)threadIdx.x >> 5;            // the stage whose tile this thread issues
     int rtn = 0, stn = 0;
     const bool issuer = (threadIdx.x & 31) == 0 && wn >= 1 && wn < Sm::kNS && tile_of(p, n_units, wn, rtn, stn);
-    if (issuer && !p.amax_in)
+    if (issuer)
         issue_tile(sm, &tm_codes, &tm_scales, &tm_trailer, wn, rtn, stn);
 
-    pdl_wait();
-    if (threadIdx.x == 0 && pre && p.amax_in)
-        issue_tile(sm, &tm_codes, &tm_scales, &tm_trailer, 0, rt0, st0);
-    if (issuer && p.amax_in)
-        issue_tile(sm, &tm_codes, &tm_scales, &tm_trailer, wn, rtn, stn);
     if (p.amax_in) {
         // S_enc of every expert from the supplied amax; CTA 0 writes the metadata
         for (int i = threadIdx.x; i < p.E; i += blockDim.x) {
@@ -832,6 +833,7 @@ direct_receive_kernel(const __grid_constant__ CUtensorMap tm_codes,
             }
         }
     } else {
+        pdl_wait();
         for (int i = threadIdx.x; i < p.E; i += blockDim.x)
             smem_se(sm, p.E)[i] = p.scale_enc[i];
     }

@@ -284,7 +284,7 @@ __device__ __forceinline__ int used_rows(const SwigluArgs &a)
 {
     if (!a.offsets)
         return a.R_cap;
-    const int R = __ldg(a.offsets + a.E);
+    const int R = ld_word(a.offsets + a.E);
     if (R > a.R_cap && blockIdx.x == 0 && threadIdx.x == 0)
         raise_status(a.status, kDevErrCapacity);
     return min(R, a.R_cap);
@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluArgs a, int cols
     auto fetch = [&]() {
         if (at.left > 0 && at.r < R && at.unit() < at.nu) {
             const uint16_t *x = a.x + (int64_t)at.r * a.ld + at.unit() * 8;
-            rg = __ldg(reinterpret_cast<const uint4 *>(x));
-            ru = __ldg(reinterpret_cast<const uint4 *>(x + a.I));
+            rg = ld_16bytes(x);
+            ru = ld_16bytes(x + a.I);
         }
     };
     fetch();
@@ -388,11 +388,11 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluArgs a,
             const int q = at.unit();
             const uint8_t *row = a.ckpt + (int64_t)at.r * 2 * a.I + q * 8;
             const uint8_t *sr = scales + (int64_t)at.r * (a.I / 16) + (q >> 2);
-            rd = __ldg(reinterpret_cast<const uint4 *>(a.d_act + (int64_t)at.r * a.ld + q * 8));
-            rg = __ldg(reinterpret_cast<const uint2 *>(row));
-            ru = __ldg(reinterpret_cast<const uint2 *>(row + a.I));
-            rsg = __ldg(sr);
-            rsu = __ldg(sr + a.I / 32);
+            rd = ld_16bytes(a.d_act + (int64_t)at.r * a.ld + q * 8);
+            rg = ld_8bytes(row);
+            ru = ld_8bytes(row + a.I);
+            rsg = ld_byte(sr);
+            rsu = ld_byte(sr + a.I / 32);
         }
     };
     int cur = -1;         // expert whose rows `top` covers ...
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(SwigluArgs a,
             flush();
             if (turn) {
                 cur = a.offsets ? expert_of_dest(a.offsets, a.E, r) : 0;
-                cur_end = a.offsets ? __ldg(a.offsets + cur + 1) : R;
+                cur_end = a.offsets ? ld_word(a.offsets + cur + 1) : R;
             }
         }
         if (on) {

@@ -8,22 +8,6 @@
 namespace epq {
 
 // ---------------------------------------------------------------- loads
-// A word that an earlier kernel may have written just before: not moved ahead of
-// the wait for that kernel, as a load of unchanging memory could be.
-__device__ __forceinline__ int ld_word(const int32_t *p)
-{
-    int v;
-    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float ld_word(const float *p)
-{
-    float v;
-    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-    return v;
-}
-
 // 16 bytes to shared memory without a register between; and this thread's
 // arrival on `bar` (counted beforehand) when its copies so far have landed.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)

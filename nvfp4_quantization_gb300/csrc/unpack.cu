@@ -49,13 +49,13 @@ constexpr int kUnpackThreads = 256;
 constexpr int kUnpackUnits = 4;   // units in flight per thread
 
 __global__ void __launch_bounds__(kUnpackThreads)
-nvfp4_unpack_kernel(const uint8_t *__restrict__ rows, int R_cap, int H, int64_t S,
-                    const int32_t *__restrict__ offsets, int E, uint16_t *__restrict__ out,
+nvfp4_unpack_kernel(const uint8_t *rows, int R_cap, int H, int64_t S,
+                    const int32_t *offsets, int E, uint16_t *__restrict__ out,
                     uint32_t *__restrict__ status, Div32 per_row)
 {
     pdl_launch_dependents();
     pdl_wait();
-    int R = offsets[E];
+    int R = ld_word(offsets + E);
     if (R > R_cap) {
         if (blockIdx.x == 0 && threadIdx.x == 0)
             raise_status(status, kDevErrCapacity);
@@ -78,9 +78,9 @@ nvfp4_unpack_kernel(const uint8_t *__restrict__ rows, int R_cap, int H, int64_t 
             if (i < total) {
                 const uint32_t r = div32(i, per_row), q = i - r * nu;
                 const uint8_t *row = rows + (int64_t)r * S;
-                cw[j] = __ldg(reinterpret_cast<const uint32_t *>(row + 4 * q));
-                sb[j] = __ldg(row + H / 2 + (q >> 1));
-                st[j] = __ldg(reinterpret_cast<const float *>(row + S - 16));
+                cw[j] = ld_word(reinterpret_cast<const uint32_t *>(row + 4 * q));
+                sb[j] = ld_byte(row + H / 2 + (q >> 1));
+                st[j] = ld_word(reinterpret_cast<const float *>(row + S - 16));
             }
         }
 #pragma unroll
