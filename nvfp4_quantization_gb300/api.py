@@ -203,6 +203,22 @@ def alloc_grouped(R_cap: int, H: int, E: int, device, rowwise: bool = True) -> d
     return g
 
 
+# Scales lie row after row or in 128 x 4 tiles, in tensors of the same shape.  The
+# calls that write them note the layout on the tensor, so that the products can
+# refuse the other one.  A tensor made from it (a slice, a copy) carries no note
+# and is taken as it is.
+def _set_layout(out: dict, tiled: bool):
+    for name in ("rw_scales", "cw_scales"):
+        if out.get(name) is not None:
+            out[name].nvfp4_tiled = tiled
+
+
+def _need_tiled(t: torch.Tensor, name: str):
+    if not getattr(t, "nvfp4_tiled", True):
+        raise ValueError(f"{name} holds its scales row after row; the products read them in tiles: make the operand "
+                         "with swizzled=True")
+
+
 def grouped_struct(g: dict) -> EpGrouped:
     return EpGrouped(*[ctypes.c_void_p(g[n].data_ptr()) if g.get(n) is not None else None
                        for n, _ in EpGrouped._fields_])
@@ -233,6 +249,7 @@ def ep_nvfp4_direct_receive(rows: torch.Tensor, H: int, offsets: torch.Tensor, E
                                    int(seed) & ((1 << 64) - 1), int(sign_mask) & 0xFFFF, _ptr(status),
                                    _stream(stream))
     check(name, st)
+    _set_layout(out, swizzled)
     return out
 
 
@@ -263,6 +280,7 @@ def ep_nvfp4_colwise_rht_bf16(x: torch.Tensor, offsets: torch.Tensor, E: int, am
                                    _ptr(out["cw_scale_enc"]), int(rounding), int(seed) & ((1 << 64) - 1),
                                    int(sign_mask) & 0xFFFF, _ptr(status), _stream(stream))
     check(name, st)
+    _set_layout(out, swizzled)
     return out
 
 
@@ -748,6 +766,7 @@ def ep_nvfp4_operand(rows: torch.Tensor, H: int, offsets: torch.Tensor | None = 
                                      row_scale.data_ptr(), _at(codes), status.data_ptr(), _stream_of(stream, dev))
     if st:
         check("ep_nvfp4_operand", st)
+    scales.nvfp4_tiled = True
     return {"rw_codes": rows if codes is None else codes, "rw_scales": scales, "rw_row_scale": row_scale, "K": H}
 
 
@@ -768,8 +787,10 @@ def ep_nvfp4_grouped_gemm(x: dict, w: dict, offsets: torch.Tensor | None = None,
     ``x``: the rowwise operand of R_cap rows (keys rw_codes, rw_scales in tiles,
     rw_row_scale; K where rows of rw_codes are longer than K/2 bytes), from
     ep_nvfp4_direct_receive(..., swizzled=True) or ep_nvfp4_operand.  ``w``: the
-    operand of weights [E, N, K], from ep_nvfp4_operand.  The gradient of the rows is the same call with the packed
-    transposed weights.  ``offsets`` and the rows as in ep_grouped_gemm."""
+    operand of weights [E, N, K], from ep_nvfp4_operand.  Scales that a call
+    wrote row after row (``swizzled=False``) are refused.  The gradient of the
+    rows is the same call with the packed transposed weights.  ``offsets`` and
+    the rows as in ep_grouped_gemm."""
     xc, wc = x["rw_codes"], w["rw_codes"]
     ld_x = _need_rows(xc, 'x["rw_codes"]', (torch.uint8,))
     R_cap, width = xc.shape
@@ -786,6 +807,8 @@ def ep_nvfp4_grouped_gemm(x: dict, w: dict, offsets: torch.Tensor | None = None,
         raise ValueError('w["rw_codes"] must have contiguous rows at one distance')
     # blocks of 128 rows that the call may read; without offsets the last may be cut
     blocks = R_cap // 128 if offsets is not None else -(-R_cap // 128)
+    for op, name in ((x, "x"), (w, "w")):
+        _need_tiled(op["rw_scales"], f'{name}["rw_scales"]')
     _need_bytes(x["rw_scales"], 'x["rw_scales"]', blocks * -(-K // 64) * 512)
     _need_f32(x["rw_row_scale"], 'x["rw_row_scale"]', R_cap)
     _need_bytes(w["rw_scales"], 'w["rw_scales"]', E * nvfp4_scale_bytes(N, K))
@@ -812,8 +835,8 @@ def ep_nvfp4_grouped_wgrad(dy: dict, x: dict, N: int, K: int, offsets: torch.Ten
     """Gradient of the expert weights, [E, N, K], from the columnwise NVFP4
     operands of dy (N columns) and x (K columns): keys cw_codes, cw_scales in
     tiles, cw_scale_enc, as ep_nvfp4_direct_receive and
-    ep_nvfp4_colwise_rht_bf16 make them with ``swizzled=True`` and one sign
-    mask.
+    ep_nvfp4_colwise_rht_bf16 make them with ``swizzled=True`` (others are
+    refused) and one sign mask.
 
     ``d_w``, ``dtype``, ``accumulate`` as in ep_grouped_wgrad."""
     codes = dy["cw_codes"]
@@ -824,6 +847,7 @@ def ep_nvfp4_grouped_wgrad(dy: dict, x: dict, N: int, K: int, offsets: torch.Ten
     R_cap, dev = codes.numel() * 2 // N, codes.device
     for op, name, H in ((dy, "dy", N), (x, "x", K)):
         _need_dense(op["cw_codes"], f'{name}["cw_codes"]', (R_cap * H // 2,), torch.uint8)
+        _need_tiled(op["cw_scales"], f'{name}["cw_scales"]')
         _need_bytes(op["cw_scales"], f'{name}["cw_scales"]', R_cap * H // 16)
         _need_f32(op["cw_scale_enc"], f'{name}["cw_scale_enc"]', E)
     _need_offsets(offsets, E)
