@@ -608,7 +608,8 @@ ep_status ep_grouped_gemm(const void *x_bf16, int64_t R_cap, int64_t K,
  *   d_w             device [E, N, K] of `dtype` (EP_DTYPE_F32 or EP_DTYPE_BF16).
  *                   Written whole: an expert without rows gets zeros.
  *   accumulate      EP_DTYPE_F32 only (EP_ERR_ARG): the sums are added to what
- *                   d_w holds, one FP32 addition an element.
+ *                   d_w holds, one FP32 addition an element.  (An expert without
+ *                   rows leaves its part as it is.)
  * N % 8 == 0, K % 8 == 0.
  */
 ep_status ep_grouped_wgrad(const void *dy_bf16, int64_t ld_dy,
@@ -693,8 +694,11 @@ ep_status ep_nvfp4_grouped_gemm(const uint8_t *x_codes, int64_t ld_x,
  *                   ep_nvfp4_colwise_rht_bf16_swizzled for H = N;
  *   x_codes, x_scales, x_scale_enc: the same for H = K.
  *                   Without expert_offsets R_cap is a multiple of 128.
- *   d_w, dtype, accumulate: as in ep_grouped_wgrad.  An expert whose rows go
- *                   past R_cap counts as empty as a whole.
+ *   d_w, dtype, accumulate: as in ep_grouped_wgrad, but an FP32 d_w takes the
+ *                   sum of every 8192 rows of an expert by an addition of its
+ *                   own, in their order, on top of what it holds (accumulate)
+ *                   or of the first such sum.  An expert whose rows go past
+ *                   R_cap counts as empty as a whole.
  * N % 128 == 0, K % 128 == 0.
  */
 ep_status ep_nvfp4_grouped_wgrad(const uint8_t *dy_codes,

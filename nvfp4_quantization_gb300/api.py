@@ -838,7 +838,8 @@ def ep_nvfp4_grouped_wgrad(dy: dict, x: dict, N: int, K: int, offsets: torch.Ten
     ep_nvfp4_colwise_rht_bf16 make them with ``swizzled=True`` (others are
     refused) and one sign mask.
 
-    ``d_w``, ``dtype``, ``accumulate`` as in ep_grouped_wgrad."""
+    ``d_w``, ``dtype``, ``accumulate`` as in ep_grouped_wgrad; an FP32 ``d_w``
+    takes the sum of every 8192 rows of an expert by an addition of its own."""
     codes = dy["cw_codes"]
     if not codes.is_cuda:
         raise ValueError('dy["cw_codes"] must be a CUDA tensor')
