@@ -778,7 +778,7 @@ ep_status ep_nvfp4_grouped_gemm(const uint8_t *x_codes, int64_t ld_x, const uint
     a.K = (int)K;
     a.N = (int)N;
     a.status = dev_status;
-    return cuda_status(R_cap > 0 ? epq::launch_nvfp4_gemm(c, a) : cudaSuccess);
+    return cuda_status(epq::launch_nvfp4_gemm(c, a));
 }
 
 ep_status ep_nvfp4_grouped_wgrad(const uint8_t *dy_codes, const uint8_t *dy_scales, const float *dy_scale_enc,

@@ -18,11 +18,13 @@ template <bool kAmn, int kCtas> cudaError_t gemm(const LaunchCtx &c, const Group
 {
     using C = GroupedCfg<false, false, kAmn, kCtas, false>;
     GroupedParams p = {};
-    const bool ok = (kAmn ? bf16_map(&p.map[kMapA], a.w, a.N, a.K, a.N, a.E, 64)
-                          : bf16_map(&p.map[kMapA], a.w, a.K, a.N, a.K, a.E, 128)) &&
-                    bf16_map(&p.map[kMapB], a.x, a.K, a.R_cap, a.ld_x, 1, 64) &&
-                    make_map_3d(&p.out, MapType::Bf16, a.out, {(uint64_t)a.N, (uint64_t)a.R_cap, 1},
-                                {(uint64_t)a.N * 2, (uint64_t)a.N * 2 * a.R_cap}, {32, 32, 1}, 64);
+    // without rows there is nothing to copy: the kernel only looks at the offsets
+    const bool ok = a.R_cap == 0 ||
+                    ((kAmn ? bf16_map(&p.map[kMapA], a.w, a.N, a.K, a.N, a.E, 64)
+                           : bf16_map(&p.map[kMapA], a.w, a.K, a.N, a.K, a.E, 128)) &&
+                     bf16_map(&p.map[kMapB], a.x, a.K, a.R_cap, a.ld_x, 1, 64) &&
+                     make_map_3d(&p.out, MapType::Bf16, a.out, {(uint64_t)a.N, (uint64_t)a.R_cap, 1},
+                                 {(uint64_t)a.N * 2, (uint64_t)a.N * 2 * a.R_cap}, {32, 32, 1}, 64));
     if (!ok)
         return cudaErrorInvalidValue;
     p.offsets = a.offsets;
@@ -61,7 +63,7 @@ template <bool kF32, int kCtas> cudaError_t wgrad(const LaunchCtx &c, const Grou
 
 cudaError_t launch_grouped_gemm(const LaunchCtx &c, const GroupedGemmArgs &a)
 {
-    if (a.R_cap == 0)
+    if (a.R_cap == 0 && !a.offsets)
         return cudaSuccess;
     using One = GroupedCfg<false, false, false, 1, false>;
     if (single_ctas<One>(c, a.N, ceil_div(a.R_cap, One::kTileN)))

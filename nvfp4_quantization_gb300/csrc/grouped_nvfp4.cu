@@ -1,5 +1,7 @@
 // NVFP4 matrix products grouped by expert (the kernel is in grouped.cuh), and
 // what prepares their operands: the tiled scales of packed rows.
+#include <algorithm>
+
 #include "grouped.cuh"
 
 namespace epq {
@@ -101,12 +103,14 @@ template <int kCtas> cudaError_t gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a
     // slots are whole blocks of 128 rows, so that rows past the last whole block are
     // past the capacity; without slots the last block may be cut
     const int64_t blocks = a.offsets ? a.R_cap / 128 : ceil_div(a.R_cap, 128);
-    const bool ok = code_map(&p.map[kMapA], a.w, a.K / 2, a.N, a.ld_w, a.E, 128) &&
-                    code_map(&p.map[kMapB], a.x, a.K / 2, a.R_cap, a.ld_x, 1, 64) &&
-                    scale_map(&p.map[kMapSa], a.w_scales, kt, ceil_div(a.N, 128) * a.E, 1) &&
-                    scale_map(&p.map[kMapSb], a.x_scales, kt, blocks > 0 ? blocks : 1, C::kTileN / 128) &&
-                    make_map_3d(&p.out, MapType::Bf16, a.out, {(uint64_t)a.N, (uint64_t)a.R_cap, 1},
-                                {(uint64_t)a.N * 2, (uint64_t)a.N * 2 * a.R_cap}, {32, 32, 1}, 64);
+    // without whole blocks there is nothing to copy: the kernel only looks at the offsets
+    const bool ok = blocks == 0 ||
+                    (code_map(&p.map[kMapA], a.w, a.K / 2, a.N, a.ld_w, a.E, 128) &&
+                     code_map(&p.map[kMapB], a.x, a.K / 2, a.R_cap, a.ld_x, 1, 64) &&
+                     scale_map(&p.map[kMapSa], a.w_scales, kt, ceil_div(a.N, 128) * a.E, 1) &&
+                     scale_map(&p.map[kMapSb], a.x_scales, kt, blocks, C::kTileN / 128) &&
+                     make_map_3d(&p.out, MapType::Bf16, a.out, {(uint64_t)a.N, (uint64_t)a.R_cap, 1},
+                                 {(uint64_t)a.N * 2, (uint64_t)a.N * 2 * a.R_cap}, {32, 32, 1}, 64));
     if (!ok)
         return cudaErrorInvalidValue;
     p.offsets = a.offsets;
@@ -148,7 +152,9 @@ template <bool kF32, int kCtas> cudaError_t wgrad(const LaunchCtx &c, const Nvfp
 
 cudaError_t launch_operand(const LaunchCtx &c, const OperandArgs &a)
 {
-    const int64_t mt = ceil_div(a.per_group, 128), kt = ceil_div(a.K, 64);
+    // (without any rows a CTA still looks at the offsets)
+    const int64_t mt = a.offsets ? std::max<int64_t>(1, ceil_div(a.per_group, 128)) : ceil_div(a.per_group, 128);
+    const int64_t kt = ceil_div(a.K, 64);
     if (a.groups * mt == 0)
         return cudaSuccess;
     return launch_pdl(operand_kernel, dim3((unsigned)(a.groups * mt), (unsigned)ceil_div(kt, kOpTiles)),
@@ -157,6 +163,8 @@ cudaError_t launch_operand(const LaunchCtx &c, const OperandArgs &a)
 
 cudaError_t launch_nvfp4_gemm(const LaunchCtx &c, const Nvfp4GemmArgs &a)
 {
+    if (a.R_cap == 0 && !a.offsets)
+        return cudaSuccess;
     using One = GroupedCfg<true, false, false, 1, false>;
     if (single_ctas<One>(c, a.N, ceil_div(a.R_cap, One::kTileN)))
         return gemm<1>(c, a);
