@@ -644,9 +644,10 @@ size_t ep_nvfp4_scale_bytes(int64_t rows, int64_t H);
  *                   the codes are copied there, row after row.  Packed rows
  *                   start anywhere on 16 bytes, which costs the products' copies
  *                   a part of their rate: large batches gain from rows of their
- *                   own (98304 rows, 64 experts of 4096 x 4096 on GB300: 600 us
- *                   from packed rows and weights, 525 from copies; 128 tokens 8
- *                   of 64 experts 121 and 112).
+ *                   own (98304 rows, 64 experts of 4096 x 4096 on GB300: 716 us
+ *                   from packed rows and weights, 621 from copies, 646 with copies
+ *                   of the weights' codes alone; 128 tokens, 8 of 64 experts: 119,
+ *                   110 and 111).
  */
 ep_status ep_nvfp4_operand(const uint8_t *rows, int64_t groups,
                            int64_t rows_per_group, int64_t H,

@@ -19,17 +19,22 @@
 // warps 12-15 copy the rows in 16-byte pieces, and warp 8 (in a pair's second
 // CTA warps 8-10 in turn) passes the arrival of a stage on to the matrix products.
 //
-// What bounds it.  Large BF16 products: the tensor cores (busy 97 % of the time
-// on 8192 x 8192 x 4096), and with them the card's power: 8192^3 runs at 1.94
-// PFLOP/s in a burst and 1.62 to 1.69 for seconds on end, where torch.matmul has
-// 1.98 and 1.69.  NVFP4 products: the copies into shared memory.  Rows that start
-// on a line of 128 bytes reach 6.3 PFLOP/s (98304 rows, 64 experts of 4096 x 4096,
-// 525 us), packed rows, two lines to every 128 bytes, 5.5 (600 us); copies of the
-// block scales to tensor memory cost the products a quarter of their rate where
-// the tile has 128 columns, little where it has 256.  Small batches: reading the
-// weights (128 tokens, 8 of 64 experts of 4096 x 4096: NVFP4 119 us, 5.2 TB/s;
-// BF16 354 us, 6.1 TB/s).  Weight gradients with few rows an expert: writing them
-// (1536 rows, NVFP4, FP32 out: 505 us, 4.9 TB/s with the reads).
+// What bounds it (times of calls back to back for seconds, "alone" of one call
+// after a pause).  Large BF16 products: the tensor cores (busy 97 % of the time on
+// 8192 x 8192 x 4096), and with them the card's power: 8192^3 runs at 1.86 PFLOP/s
+// alone and 1.68 for seconds on end, where torch.matmul has 1.86 and 1.73.  NVFP4
+// products of packed rows: the copies into shared memory, two lines to every 128
+// bytes: 4.6 PFLOP/s (98304 rows, 64 experts of 4096 x 4096: 716 us, 705 alone).
+// Of rows that start on a line: 5.3 (621 us, 582 alone), then at the power limit.
+// Copies of the block scales to tensor memory cost the products a quarter of their
+// rate where the tile has 128 columns, little where it has 256.  Small batches:
+// reading the weights (128 tokens, 8 of 64 experts of 4096 x 4096: NVFP4 118 us, 5.2
+// TB/s; BF16 344 us, 6.2 TB/s).  Weight gradients with few rows an expert: writing
+// them (1536 rows, NVFP4, FP32 out, 64 experts of 2048 x 4096: 335 us, 6.4 TB/s).
+// With many, in NVFP4: not that (98304 rows: 545 us, where a fill of the results
+// takes 278), but copying rows by threads, which keeps the matrix unit waiting (busy
+// a third of the time).  Adding to FP32 results: reading and writing them (the same,
+// 915 us, 5.1 TB/s).
 //
 // Why it is as it is, each step against the state before (98304 rows, 64 experts
 // of 4096 x 4096, BF16 / NVFP4):
@@ -121,8 +126,9 @@ template <bool kFp4_, bool kWgrad_, bool kAmn_, int kCtas_, bool kF32_> struct G
     // error grows with its additions: over 2048 rows of BF16 (128 additions) 2.1e-6
     // of the result, over 65536 7.6e-5; in parts of 768 rows 6.8e-7 and 7.5e-7.
     // NVFP4 loses less (16384 rows 2.0e-6, in parts of 8192 8.2e-7).  BF16 keeps
-    // its parts in registers (4 % of a step with 2048 rows an expert), NVFP4, where
-    // there is seldom more than one, adds them in global memory.
+    // its parts in registers (4 % of a step with 2048 rows an expert; the 128 of them
+    // leave about 240 bytes a thread that are spilled), NVFP4, where there is seldom
+    // more than one, adds them in global memory.
     static constexpr bool kParts = kWgrad && kF32, kKeep = kParts && !kFp4;
     static constexpr int kPartBlocks = kFp4 ? 32 : 12;
 };
